@@ -52,6 +52,7 @@
 #ifndef Q4GEMV_H
 #define Q4GEMV_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -72,7 +73,11 @@ enum {
 enum {
     Q4_FAULT_BAD_EXPERT = 4,   /* moe_q4_gemv or moe_q4_pure_read saw an expert id outside [0, E) */
     Q4_FAULT_WAIT_TIMEOUT = 8, /* a wait for a weight stage ran out of its cycle limit (rows written as NaN) */
-    Q4_FAULT_COPY_LOST = 16    /* even the final wait for a warp's issued copies ran out (not seen in practice) */
+    Q4_FAULT_COPY_LOST = 16,   /* even the final wait for a warp's issued copies ran out (not seen in practice) */
+    Q4_FAULT_BAD_SLOT = 32,    /* kv4_write or kv4_read saw a slot >= num_pages * page_size */
+    Q4_FAULT_BAD_PAGE = 64,    /* kv4_attention saw a page id outside [0, num_pages) */
+    Q4_FAULT_BAD_LENGTH = 128, /* kv4_attention saw a length outside [0, max_pages * page_size] */
+    Q4_FAULT_BAD_POSITION = 256 /* qk_norm_rope saw a position outside [0, max_pos) */
 };
 
 /*
@@ -185,6 +190,91 @@ int moe_router_q4(int32_t *expert_ids, float *expert_weights, float *logits, con
                   const float *x, int T, int E, int K, int topk, int normalize, q4_stream_t stream);
 
 /*
+ * ---- Between two projections of a decode step: q/k norm and rotation, the 4-bit cache, attention over it ----
+ * (No counterpart in the source pages, whose kernels end at the projections.)
+ *
+ * Activations here are fp32, fp16 or bf16 (`dtype`, the same for every activation of a call); sums, statistics and
+ * products are fp32 or wider in effect, and values are rounded to the type once, when they are stored. A tensor of T
+ * tokens is rows of heads * D contiguous elements, `stride` elements from one token's row to the next (so q, k and v
+ * may be columns of one projection output); every row must be 16-byte aligned.
+ */
+enum { Q4_F32 = 0, Q4_F16 = 1, Q4_BF16 = 2 };
+
+/*
+ * qk_norm_rope: RMSNorm of each query and key head and the rotary position rotation, in one pass.
+ *   y_i = x_i * gamma_i / sqrt(sum_j x_j^2 / D + eps) for each head row x (gamma NULL: y = x), then each pair (a, b)
+ *   of the first rot_dim elements becomes (a c - b s, b c + a s), c and s the cos and sin of the token's position.
+ *   Pair i is (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved != 0. Elements from rot_dim on are not rotated.
+ *   q, q_out [T][Hq][D], k, k_out [T][Hkv][D]; an output may be its input (same pointer and stride) or must not overlap
+ *   any input; q_gamma, k_gamma float[D] or NULL; cos_sin float[max_pos][rot_dim]: row p holds cos for the rot_dim / 2
+ *   pairs, then sin; positions int32[T] (device). gamma and cos_sin 16-byte aligned.
+ *   D a multiple of 32 up to 256; rot_dim a multiple of 16, 0..D (0: no rotation, cos_sin and positions unused).
+ *   A token whose position is outside [0, max_pos) gets NaN heads and Q4_FAULT_BAD_POSITION is recorded.
+ */
+int qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k, const float *q_gamma, const float *k_gamma,
+                 float eps, const float *cos_sin, const int32_t *positions, int T, int Hq, int Hkv, int D, int rot_dim,
+                 int max_pos, int interleaved, long long q_stride, long long k_stride, long long q_out_stride,
+                 long long k_out_stride, int dtype, q4_stream_t stream);
+
+/*
+ * A paged key/value cache in planar Q4 (see Formats): a token's keys of one head are one row of head_dim weights.
+ *   k_qs, v_qs uint8[num_pages][num_kv_heads][page_size][head_dim/2], k_d, v_d uint16[num_pages][num_kv_heads]
+ *   [page_size][head_dim/32] (binary16), all 16-byte aligned device memory of the caller (so q4_dequant reads a cache
+ *   as a matrix of num_pages * num_kv_heads * page_size rows). head_dim a multiple of 32 up to 256; page_size a power
+ *   of two; at most 2^31 - 1 rows. Slot s is page s / page_size, offset s % page_size. The struct itself is host memory
+ *   and is copied by the call.
+ */
+typedef struct {
+    uint8_t *k_qs;
+    uint16_t *k_d;
+    uint8_t *v_qs;
+    uint16_t *v_d;
+    int num_pages, num_kv_heads, page_size, head_dim;
+} kv4_cache;
+
+/*
+ * kv4_write: quantise the keys and values of T tokens into their slots. A 32-element block becomes
+ *   d = binary16(min(max|x| / 7, 65504)), code = 8 + clamp(nearest(x / d), -7, 7) with ties to even (d = 0: codes 8);
+ *   the nearest is exact, so equal inputs give equal bytes whatever the type they come in. A block that holds a NaN or
+ *   an infinity is stored as d = NaN, codes 8 (it reads back as NaN).
+ *   k, v [T][num_kv_heads][head_dim]; slots int32[T] (device). A token whose slot is negative is skipped; one whose slot
+ *   is past the cache is skipped and Q4_FAULT_BAD_SLOT recorded. The slots >= 0 of one call must be distinct (a slot
+ *   given twice ends up with a mixture of the two rows).
+ * kv4_read: the rows at T slots as values (code - 8) * d.
+ *   k_out, v_out [T][num_kv_heads][head_dim], either may be NULL. A row whose slot is negative is left as it is; one
+ *   whose slot is past the cache becomes NaN and Q4_FAULT_BAD_SLOT is recorded. A slot may be given more than once.
+ */
+int kv4_write(const kv4_cache *cache, const void *k, const void *v, const int32_t *slots, int T, long long k_stride,
+              long long v_stride, int dtype, q4_stream_t stream);
+int kv4_read(void *k_out, void *v_out, const kv4_cache *cache, const int32_t *slots, int T, long long k_stride,
+             long long v_stride, int dtype, q4_stream_t stream);
+
+/*
+ * kv4_attention: attention of the M newest tokens of each of B sequences over the cache (their own keys and values are
+ * in it already). Query m of a sequence of length n sits at position p = n - M + m and sees the tokens
+ * max(0, p + 1 - window) <= t <= p (window 0: from token 0); token t of sequence b is at page
+ * block_table[b][t / page_size], offset t % page_size. Query head h reads key head h / (Hq / num_kv_heads).
+ *   out = sum_t softmax_t(scale * q . k_t) v_t;  lse = log sum_t exp(scale * q . k_t) (natural; written if not NULL).
+ * A query that sees nothing (n = 0, or p < 0) gets zeros and lse = -infinity. Tokens that no query of the sequence sees
+ * are not read, and what a query does not see does not enter its result, whatever bits it holds.
+ *   q, out [B*M][Hq][head_dim] (token rows with strides as above); lse float[B*M][Hq]; block_table
+ *   int32[B][max_pages], seq_lens int32[B] (device). 1 <= M <= 16; 1 <= B <= 1024; head_dim 64, 128 or 256;
+ *   Hq a multiple of num_kv_heads; scale finite and > 0; max_pages * page_size <= 2^30.
+ *   A sequence whose length is outside [0, max_pages * page_size], or that reads a page id outside [0, num_pages), gets
+ *   NaN rows, and Q4_FAULT_BAD_LENGTH or Q4_FAULT_BAD_PAGE is recorded. A query row that holds a NaN or an infinity
+ *   gives NaN.
+ *   workspace: device memory, 16-byte aligned, of at least the bytes that kv4_attention_workspace states for these
+ *   sizes on the current device (whatever B and the lengths); its contents do not matter before or after. Calls that
+ *   may run at the same time need a workspace each.
+ *   The work is divided by the lengths of all sequences of the call, so a sequence's result may differ in the last bits
+ *   when it is computed in another batch; the same call gives the same bits.
+ */
+int kv4_attention_workspace(size_t *bytes, int M, int Hq, int Hkv, int D, int dtype);
+int kv4_attention(void *out, float *lse, const void *q, const kv4_cache *cache, const int32_t *block_table,
+                  const int32_t *seq_lens, int B, int M, int Hq, int max_pages, long long q_stride, long long out_stride,
+                  float scale, int window, int dtype, void *workspace, size_t workspace_bytes, q4_stream_t stream);
+
+/*
  * Pure-read ceiling instruments: the same bytes, the same addressing and the same launch shape as the
  * matching GEMV, but no unpack and no dot products. Each output row receives the XOR of the 32-bit quant
  * words and zero-extended 16-bit scales (Q4) or of the 32-bit words of the super-blocks (Q4_K) of that
@@ -235,7 +325,8 @@ const char *q4_last_error(void);
  * launched so that it may start while the kernel before it in the same stream is still running: the Q4
  * and Q4_K kernels issue their first weight copies at once, then wait for that kernel's completion (and
  * the visibility of its writes) before they read x, gamma or expert ids or write any output; the MoE kernel
- * waits before it reads the expert ids. So a chain of calls where each x is the previous output stays
+ * waits before it reads the expert ids. The norm/rotation, cache and attention calls launch the same way and wait before
+ * they read anything, so their caches and page tables may come from the call before. So a chain of calls where each x is the previous output stays
  * exact, and each call's weight streaming overlaps the previous call's tail.
  * Requirement while it is on: the kernel that runs directly before a call in the same stream must not
  * write that call's weight bytes (qs, d or the Q4_K blocks); weights written earlier in the stream, or on

@@ -8,7 +8,9 @@ library's message. There is no CPU path: without the compiled library every call
 Layouts (row-major, little-endian):
   * Q4 planar: ``qs`` uint8 ``[N, K/32, 16]`` (or ``[N, K/2]``), ``d`` float16 ``[N, K/32]``.
   * Q4_K: ``w`` uint8 ``[N, K/256, 144]`` (or ``[N, K/256*144]``).
-  * inputs and outputs float32.
+  * inputs and outputs of the GEMVs float32; of the norm/rotation, cache and attention calls float32, float16 or
+    bfloat16 (one type per call).
+  * 4-bit cache: :class:`KV4Cache`, planar Q4 rows in pages ``[num_pages, num_kv_heads, page_size, ...]``.
 """
 
 from __future__ import annotations
@@ -25,14 +27,20 @@ __all__ = [
     "moe_q4_gemv", "q4k_gemv_batched", "fused_gateup_swiglu_q4k_gemv", "moe_q4_swiglu_gemv", "moe_router_q4", "q4_pure_read",
     "q4k_pure_read",
     "moe_q4_pure_read", "q4_dequant", "q4k_dequant",
+    "KV4Cache", "qk_norm_rope", "kv4_write", "kv4_read", "kv4_attention", "kv4_attention_workspace",
     "q4_device_faults", "q4_set_launch_overlap", "q4_get_launch_overlap", "q4_set_wait_limit", "q4_get_wait_limit",
     "FAULT_BAD_EXPERT", "FAULT_WAIT_TIMEOUT", "FAULT_COPY_LOST", "DEFAULT_WAIT_LIMIT",
+    "FAULT_BAD_SLOT", "FAULT_BAD_PAGE", "FAULT_BAD_LENGTH", "FAULT_BAD_POSITION",
 ]
 
 Q4_OK, Q4_EINVAL, Q4_EALIGN, Q4_ECUDA, Q4_EUNSUPPORTED = 0, -1, -2, -3, -4
 FAULT_BAD_EXPERT = 4
 FAULT_WAIT_TIMEOUT = 8
 FAULT_COPY_LOST = 16
+FAULT_BAD_SLOT = 32
+FAULT_BAD_PAGE = 64
+FAULT_BAD_LENGTH = 128
+FAULT_BAD_POSITION = 256
 DEFAULT_WAIT_LIMIT = 4_000_000_000
 _CODE_NAMES = {Q4_EINVAL: "EINVAL", Q4_EALIGN: "EALIGN", Q4_ECUDA: "ECUDA", Q4_EUNSUPPORTED: "EUNSUPPORTED"}
 
@@ -46,6 +54,7 @@ class Q4Error(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 
 _SIGNATURES = {
     "q4_gemv": [_P, _P, _P, _P, _I, _I, _P],
@@ -62,6 +71,11 @@ _SIGNATURES = {
     "moe_q4_swiglu_gemv": [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P],
     "moe_router_q4": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P],
     "q4k_gemv_batched": [_P, _P, _P, _I, _I, _I, _P],
+    "qk_norm_rope": [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _I, _I, _I, _I, _I, _I, _I, _L, _L, _L, _L, _I, _P],
+    "kv4_write": [_P, _P, _P, _P, _I, _L, _L, _I, _P],
+    "kv4_read": [_P, _P, _P, _P, _I, _L, _L, _I, _P],
+    "kv4_attention_workspace": [ctypes.POINTER(ctypes.c_size_t), _I, _I, _I, _I, _I],
+    "kv4_attention": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _L, _L, ctypes.c_float, _I, _I, _P, ctypes.c_size_t, _P],
     "q4_device_faults": [ctypes.POINTER(ctypes.c_uint)],
     "q4_fma_ceiling": [_P, _I, ctypes.c_longlong, ctypes.c_float, ctypes.c_float, ctypes.POINTER(ctypes.c_longlong),
                        _P],
@@ -310,6 +324,217 @@ def q4_set_wait_limit(cycles: int) -> None:
 
 def q4_get_wait_limit() -> int:
     return int(load().q4_get_wait_limit())
+
+
+# ---- between two projections of a decode step: q/k norm and rotation, the 4-bit cache, attention over it ----
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+class KV4Cache:
+    """A paged key/value cache in planar Q4 (``kv4_cache`` of the header).
+
+    ``k_qs``, ``v_qs`` uint8 ``[num_pages, num_kv_heads, page_size, head_dim/2]`` and ``k_d``, ``v_d`` float16
+    ``[num_pages, num_kv_heads, page_size, head_dim/32]``, contiguous on one CUDA device. The object keeps the tensors
+    (and the struct that the calls take) and nothing else; :meth:`allocate` makes an empty one, whose rows read as zeros.
+    """
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [("k_qs", _P), ("k_d", _P), ("v_qs", _P), ("v_d", _P), ("num_pages", _I), ("num_kv_heads", _I),
+                    ("page_size", _I), ("head_dim", _I)]
+
+    def __init__(self, k_qs, k_d, v_qs, v_d):
+        if k_qs.dim() != 4:
+            raise ValueError("k_qs must be [num_pages, num_kv_heads, page_size, head_dim/2]")
+        pages, heads, page, half = k_qs.shape
+        if v_qs.shape != k_qs.shape or half % 16 or any(tuple(t.shape) != (pages, heads, page, half // 16) for t in (k_d, v_d)):
+            raise ValueError("the codes must be [num_pages, num_kv_heads, page_size, head_dim/2] and the scales "
+                             "[num_pages, num_kv_heads, page_size, head_dim/32], head_dim a multiple of 32")
+        if any(t.device != k_qs.device for t in (k_d, v_qs, v_d)):
+            raise ValueError("the cache's tensors must be on one device")
+        self.k_qs, self.k_d, self.v_qs, self.v_d = k_qs, k_d, v_qs, v_d
+        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = pages, heads, page, half * 2
+        self.device = k_qs.device
+        self._struct = KV4Cache._Struct(_ptr(k_qs, torch.uint8, "k_qs"), _ptr(k_d, torch.float16, "k_d"),
+                                        _ptr(v_qs, torch.uint8, "v_qs"), _ptr(v_d, torch.float16, "v_d"), pages, heads, page,
+                                        half * 2)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, device="cuda") -> "KV4Cache":
+        shape = (num_pages, num_kv_heads, page_size)
+        made = []
+        for _ in range(2):
+            made.append(torch.full((*shape, head_dim // 2), 0x88, dtype=torch.uint8, device=device))
+            made.append(torch.zeros(*shape, head_dim // 32, dtype=torch.float16, device=device))
+        return cls(*made)
+
+
+def _rows(t: torch.Tensor, heads: int, D: int, dtype: torch.dtype, device, name: str):
+    """(address, elements from one token to the next) of a tensor of token rows [..., heads, D]."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    shape, st = t.shape, t.stride()
+    if len(shape) < 3 or shape[-2] != heads or shape[-1] != D:
+        raise ValueError(f"{name}: expected [..., {heads}, {D}], got {list(shape)}")
+    if st[-1] != 1 or (heads > 1 and st[-2] != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    # token axes must lie evenly: the outer ones follow from the innermost that has more than one token
+    step, n = 0, 1
+    for size, s in zip(shape[-3::-1], st[-3::-1]):
+        if size != 1:
+            if n == 1:
+                step = s
+            elif s != step * n:
+                raise ValueError(f"{name}: the token rows must be evenly spaced")
+            n *= size
+    return t.data_ptr(), step if n > 1 else heads * D
+
+
+def _index(t: torch.Tensor, device, name: str, shape: tuple) -> int:
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _floats(t: torch.Tensor | None, device, name: str, numel: int) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {numel} contiguous values")
+    return t.data_ptr()
+
+
+def _act(t: torch.Tensor, name: str):
+    """(C code of the activation type, device) of a call, from its first activation."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    return code, t.device
+
+
+def _call(fn, device, stream, *args) -> None:
+    """Call a C entry on the tensors' device (made current if it is not) and the given or current stream of it."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+    else:
+        _check(fn(*args, _stream(stream)))
+
+
+def qk_norm_rope(q_out, k_out, q, k, q_gamma, k_gamma, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
+                 stream=None) -> None:
+    """RMSNorm of every head of q [T, Hq, D] and k [T, Hkv, D] (gamma float32 [D], or None: no norm) and the rotary
+    rotation of the first ``cos_sin.shape[1]`` elements by the table row cos_sin[positions[t]] (cos, then sin; None: no
+    rotation). The outputs may be the inputs."""
+    code, dev = _act(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out must be [T, Hq, D] and k_out [T, Hkv, D]")
+    max_pos = rot = 0
+    table = where = None
+    if cos_sin is not None:
+        max_pos, rot = cos_sin.shape
+        table = _floats(cos_sin, dev, "cos_sin", max_pos * rot)
+        where = _index(positions, dev, "positions", (T,))
+    qp, qs = _rows(q, Hq, D, q.dtype, dev, "q")
+    kp, ks = _rows(k, Hkv, D, q.dtype, dev, "k")
+    qop, qos = _rows(q_out, Hq, D, q.dtype, dev, "q_out")
+    kop, kos = _rows(k_out, Hkv, D, q.dtype, dev, "k_out")
+    _call(load().qk_norm_rope, dev, stream, qop, kop, qp, kp, _floats(q_gamma, dev, "q_gamma", D),
+          _floats(k_gamma, dev, "k_gamma", D), eps, table, where, T, Hq, Hkv, D, rot, max_pos, 1 if interleaved else 0, qs,
+          ks, qos, kos, code)
+
+
+def kv4_write(cache: KV4Cache, k, v, slots, stream=None) -> None:
+    """Quantise k and v [T, num_kv_heads, head_dim] into the cache's slots (int32 [T]; negative: skipped; the others
+    distinct)."""
+    code, dev = _act(k, "k")
+    T, H, D = k.shape[0], cache.num_kv_heads, cache.head_dim
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be [T, num_kv_heads, head_dim]")
+    if dev != cache.device:
+        raise ValueError(f"k: expected a tensor on {cache.device}, got {dev}")
+    kp, ks = _rows(k, H, D, k.dtype, dev, "k")
+    vp, vs = _rows(v, H, D, k.dtype, dev, "v")
+    _call(load().kv4_write, dev, stream, cache._ref, kp, vp, _index(slots, dev, "slots", (T,)), T, ks, vs, code)
+
+
+def kv4_read(k_out, v_out, cache: KV4Cache, slots, stream=None) -> None:
+    """Values of the cache's rows at slots (int32 [T]; negative: the row is left as it is) into k_out and v_out
+    [T, num_kv_heads, head_dim] (one of them may be None)."""
+    first = v_out if k_out is None else k_out
+    if first is None:
+        raise ValueError("k_out and v_out cannot both be None")
+    code, dev = _act(first, "k_out" if k_out is not None else "v_out")
+    T, H, D = first.shape[0], cache.num_kv_heads, cache.head_dim
+    if first.dim() != 3 or (v_out is not None and v_out.shape != first.shape):
+        raise ValueError("k_out and v_out must be [T, num_kv_heads, head_dim]")
+    if dev != cache.device:
+        raise ValueError(f"k_out: expected a tensor on {cache.device}, got {dev}")
+    kp, ks = (None, 0) if k_out is None else _rows(k_out, H, D, first.dtype, dev, "k_out")
+    vp, vs = (None, 0) if v_out is None else _rows(v_out, H, D, first.dtype, dev, "v_out")
+    _call(load().kv4_read, dev, stream, kp, vp, cache._ref, _index(slots, dev, "slots", (T,)), T, ks, vs, code)
+
+
+def kv4_attention_workspace(q, cache: KV4Cache) -> torch.Tensor:
+    """Workspace for kv4_attention calls with q's [..., M, Hq, D] and type over `cache` (any batch and lengths). Calls that
+    may run at the same time (other streams, other graphs) need one each."""
+    code, dev = _act(q, "q")
+    M, Hq = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
+    need = ctypes.c_size_t(0)
+    with torch.cuda.device(dev):
+        _check(load().kv4_attention_workspace(ctypes.byref(need), M, Hq, cache.num_kv_heads, cache.head_dim, code))
+    return torch.empty(max(16, need.value), dtype=torch.uint8, device=dev)
+
+
+def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float | None = None, window: int = 0, lse=None,
+                  workspace=None, stream=None) -> None:
+    """Attention of the newest M tokens of B sequences over the cache: q and out [B, M, Hq, D] ([B, Hq, D]: M = 1),
+    block_table int32 [B, max_pages], seq_lens int32 [B] (the M tokens included), scale None: D ** -0.5, window 0: all
+    tokens, lse float32 [B, M, Hq] or None. workspace: from kv4_attention_workspace, kept between calls; None: allocated
+    for this call."""
+    code, dev = _act(q, "q")
+    if q.dim() not in (3, 4) or out.shape != q.shape:
+        raise ValueError("q and out must be [B, M, Hq, D] or [B, Hq, D]")
+    B, Hq, D = q.shape[0], q.shape[-2], cache.head_dim
+    M = q.shape[1] if q.dim() == 4 else 1
+    if dev != cache.device:
+        raise ValueError(f"q: expected a tensor on {cache.device}, got {dev}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    qp, qs = _rows(q, Hq, D, q.dtype, dev, "q")
+    op, os_ = _rows(out, Hq, D, q.dtype, dev, "out")
+    max_pages = block_table.shape[1]
+    if workspace is None:
+        # on the stream that uses it, so that the allocator hands it on only to work behind this call
+        s = torch.cuda.current_stream(dev) if stream is None else (
+            stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev))
+        with torch.cuda.stream(s):
+            workspace = kv4_attention_workspace(q, cache)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+    _call(load().kv4_attention, dev, stream, op, _floats(lse, dev, "lse", B * M * Hq), qp, cache._ref,
+          _index(block_table, dev, "block_table", (B, max_pages)), _index(seq_lens, dev, "seq_lens", (B,)), B, M, Hq,
+          max_pages, qs, os_, D ** -0.5 if scale is None else scale, window, code, _ptr(workspace, torch.uint8, "workspace"),
+          workspace.numel())
 
 
 def q4_device_faults() -> int:

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "../../include/q4gemv.h"
+#include "kv.h"
 #include "launch.h"
 
 namespace q4 {
@@ -351,6 +352,178 @@ int q4k_dequant(float* W, const uint8_t* w, int N, int K, q4_stream_t stream) {
     DeviceInfo di;
     Q4_TRY(check_device(what, &di));
     return finish(what, launch_q4k_dequant(W, w, N, K, (cudaStream_t)stream));
+}
+
+static size_t dtype_bytes(int dtype) { return dtype == Q4_F32 ? 4 : 2; }
+
+static int check_dtype(const char* what, int dtype) {
+    if (dtype != Q4_F32 && dtype != Q4_F16 && dtype != Q4_BF16)
+        return fail(Q4_EINVAL, "%s: dtype must be Q4_F32, Q4_F16 or Q4_BF16 (got %d)", what, dtype);
+    return Q4_OK;
+}
+
+// Rows of activations: [tokens] of `width` elements, `stride` elements apart, every row 16-byte aligned.
+static int check_rows(const char* what, const char* name, const void* p, long long stride, long long width, int dtype) {
+    if (!p) return fail(Q4_EINVAL, "%s: null %s", what, name);
+    if (stride < width)
+        return fail(Q4_EINVAL, "%s: token stride of %s is %lld, below its row of %lld elements", what, name, stride, width);
+    if (!aligned(p, 16) || (stride * (long long)dtype_bytes(dtype)) % 16 != 0)
+        return fail(Q4_EALIGN, "%s: every row of %s must be 16-byte aligned", what, name);
+    return Q4_OK;
+}
+
+static int check_heads(const char* what, int Hkv, int D) {
+    if (Hkv <= 0) return fail(Q4_EINVAL, "%s: the number of key heads must be >= 1 (got %d)", what, Hkv);
+    if (D <= 0 || D % 32 != 0 || D > 256)
+        return fail(Q4_EINVAL, "%s: the head size must be a multiple of 32 up to 256 (got %d)", what, D);
+    if ((long long)Hkv * D > (1 << 20)) return fail(Q4_EINVAL, "%s: key heads * head size exceeds 2^20", what);
+    return Q4_OK;
+}
+
+static int check_cache(const char* what, const kv4_cache* c) {
+    if (!c) return fail(Q4_EINVAL, "%s: null cache", what);
+    if (!c->k_qs || !c->k_d || !c->v_qs || !c->v_d) return fail(Q4_EINVAL, "%s: null cache pointer", what);
+    Q4_TRY(check_heads(what, c->num_kv_heads, c->head_dim));
+    if (c->num_pages <= 0) return fail(Q4_EINVAL, "%s: num_pages must be >= 1 (got %d)", what, c->num_pages);
+    if (c->page_size <= 0 || (c->page_size & (c->page_size - 1)) != 0)
+        return fail(Q4_EINVAL, "%s: page_size must be a power of two (got %d)", what, c->page_size);
+    if ((long long)c->num_pages * c->page_size * c->num_kv_heads > 0x7fffffffLL)
+        return fail(Q4_EINVAL, "%s: the cache exceeds 2^31-1 rows", what);
+    if (!aligned(c->k_qs, 16) || !aligned(c->v_qs, 16))
+        return fail(Q4_EALIGN, "%s: k_qs and v_qs must be 16-byte aligned", what);
+    if (!aligned(c->k_d, 16) || !aligned(c->v_d, 16))
+        return fail(Q4_EALIGN, "%s: k_d and v_d must be 16-byte aligned", what);
+    return Q4_OK;
+}
+
+static int check_index(const char* what, const char* name, const int32_t* p) {
+    if (!p) return fail(Q4_EINVAL, "%s: null %s", what, name);
+    if (!aligned(p, 4)) return fail(Q4_EALIGN, "%s: %s must be 4-byte aligned", what, name);
+    return Q4_OK;
+}
+
+// The device check, and the fault word that the kernels record in.
+static int check_device_faults(const char* what, DeviceInfo* di, unsigned** fault) {
+    Q4_TRY(check_device(what, di));
+    *fault = device_fault_word(di->device);
+    if (!*fault) return fail(Q4_ECUDA, "%s: the device's fault word cannot be resolved", what);
+    return Q4_OK;
+}
+
+int qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, const float* q_gamma, const float* k_gamma,
+                 float eps, const float* cos_sin, const int32_t* positions, int T, int Hq, int Hkv, int D, int rot_dim,
+                 int max_pos, int interleaved, long long q_stride, long long k_stride, long long q_out_stride,
+                 long long k_out_stride, int dtype, q4_stream_t stream) {
+    const char* what = "qk_norm_rope";
+    if (T <= 0) return fail(Q4_EINVAL, "%s: T must be >= 1 (got %d)", what, T);
+    Q4_TRY(check_dtype(what, dtype));
+    Q4_TRY(check_heads(what, Hkv, D));
+    if (Hq <= 0 || Hq > 65535 || Hkv > 65535) return fail(Q4_EINVAL, "%s: 1 to 65535 heads are taken", what);
+    Q4_TRY(check_rows(what, "q", q, q_stride, (long long)Hq * D, dtype));
+    Q4_TRY(check_rows(what, "k", k, k_stride, (long long)Hkv * D, dtype));
+    Q4_TRY(check_rows(what, "q_out", q_out, q_out_stride, (long long)Hq * D, dtype));
+    Q4_TRY(check_rows(what, "k_out", k_out, k_out_stride, (long long)Hkv * D, dtype));
+    if (q_gamma) Q4_TRY(check_vec(what, "q_gamma", q_gamma));
+    if (k_gamma) Q4_TRY(check_vec(what, "k_gamma", k_gamma));
+    Q4_TRY(check_eps(what, eps));
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0)
+        return fail(Q4_EINVAL, "%s: rot_dim must be a multiple of 16 up to the head size (got %d)", what, rot_dim);
+    if (rot_dim > 0) {
+        if (max_pos <= 0) return fail(Q4_EINVAL, "%s: max_pos must be >= 1 (got %d)", what, max_pos);
+        Q4_TRY(check_vec(what, "cos_sin", cos_sin));
+        Q4_TRY(check_index(what, "positions", positions));
+    }
+    DeviceInfo di;
+    RopeArgs a = {q_out, k_out, q, k, q_gamma, k_gamma, cos_sin, positions, eps, T, Hq, Hkv, D, rot_dim, max_pos,
+                  interleaved != 0, q_stride, k_stride, q_out_stride, k_out_stride, nullptr};
+    Q4_TRY(check_device_faults(what, &di, &a.fault));
+    return finish(what, launch_qk_norm_rope(a, dtype, (cudaStream_t)stream));
+}
+
+int kv4_write(const kv4_cache* cache, const void* k, const void* v, const int32_t* slots, int T, long long k_stride,
+              long long v_stride, int dtype, q4_stream_t stream) {
+    const char* what = "kv4_write";
+    Q4_TRY(check_cache(what, cache));
+    if (T <= 0) return fail(Q4_EINVAL, "%s: T must be >= 1 (got %d)", what, T);
+    Q4_TRY(check_dtype(what, dtype));
+    const long long width = (long long)cache->num_kv_heads * cache->head_dim;
+    Q4_TRY(check_rows(what, "k", k, k_stride, width, dtype));
+    Q4_TRY(check_rows(what, "v", v, v_stride, width, dtype));
+    Q4_TRY(check_index(what, "slots", slots));
+    DeviceInfo di;
+    KvRowsArgs a = {*cache, const_cast<void*>(k), const_cast<void*>(v), slots, T, k_stride, v_stride, nullptr};
+    Q4_TRY(check_device_faults(what, &di, &a.fault));
+    return finish(what, launch_kv4_write(a, dtype, (cudaStream_t)stream));
+}
+
+int kv4_read(void* k_out, void* v_out, const kv4_cache* cache, const int32_t* slots, int T, long long k_stride,
+             long long v_stride, int dtype, q4_stream_t stream) {
+    const char* what = "kv4_read";
+    Q4_TRY(check_cache(what, cache));
+    if (T <= 0) return fail(Q4_EINVAL, "%s: T must be >= 1 (got %d)", what, T);
+    Q4_TRY(check_dtype(what, dtype));
+    if (!k_out && !v_out) return fail(Q4_EINVAL, "%s: null k_out and v_out", what);
+    const long long width = (long long)cache->num_kv_heads * cache->head_dim;
+    if (k_out) Q4_TRY(check_rows(what, "k_out", k_out, k_stride, width, dtype));
+    if (v_out) Q4_TRY(check_rows(what, "v_out", v_out, v_stride, width, dtype));
+    Q4_TRY(check_index(what, "slots", slots));
+    DeviceInfo di;
+    KvRowsArgs a = {*cache, k_out, v_out, slots, T, k_stride, v_stride, nullptr};
+    Q4_TRY(check_device_faults(what, &di, &a.fault));
+    return finish(what, launch_kv4_read(a, dtype, (cudaStream_t)stream));
+}
+
+static int check_attention_sizes(const char* what, int M, int Hq, int Hkv, int D, int dtype) {
+    Q4_TRY(check_dtype(what, dtype));
+    Q4_TRY(check_heads(what, Hkv, D));
+    if (D != 64 && D != 128 && D != 256)
+        return fail(Q4_EINVAL, "%s: the head size must be 64, 128 or 256 (got %d)", what, D);
+    if (M < 1 || M > 16) return fail(Q4_EINVAL, "%s: M=%d outside 1..16 (refused, not clamped)", what, M);
+    if (Hq <= 0 || Hq % Hkv != 0 || Hq > 65535)
+        return fail(Q4_EINVAL, "%s: the query heads (%d) must be a multiple of the key heads (%d), up to 65535", what, Hq,
+                    Hkv);
+    return Q4_OK;
+}
+
+int kv4_attention_workspace(size_t* bytes, int M, int Hq, int Hkv, int D, int dtype) {
+    const char* what = "kv4_attention_workspace";
+    if (!bytes) return fail(Q4_EINVAL, "%s: null output pointer", what);
+    Q4_TRY(check_attention_sizes(what, M, Hq, Hkv, D, dtype));
+    DeviceInfo di;
+    Q4_TRY(check_device(what, &di));
+    *bytes = kv4_attention_workspace_bytes(M, Hq / Hkv, D, dtype, di.sm_count);
+    return finish(what, cudaSuccess);
+}
+
+int kv4_attention(void* out, float* lse, const void* q, const kv4_cache* cache, const int32_t* block_table,
+                  const int32_t* seq_lens, int B, int M, int Hq, int max_pages, long long q_stride, long long out_stride,
+                  float scale, int window, int dtype, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+    const char* what = "kv4_attention";
+    Q4_TRY(check_cache(what, cache));
+    Q4_TRY(check_attention_sizes(what, M, Hq, cache->num_kv_heads, cache->head_dim, dtype));
+    if (B <= 0 || B > 1024) return fail(Q4_EINVAL, "%s: B must be in 1..1024 (got %d)", what, B);
+    const long long width = (long long)Hq * cache->head_dim;
+    Q4_TRY(check_rows(what, "q", q, q_stride, width, dtype));
+    Q4_TRY(check_rows(what, "out", out, out_stride, width, dtype));
+    if (lse && !aligned(lse, 4)) return fail(Q4_EALIGN, "%s: lse must be 4-byte aligned", what);
+    Q4_TRY(check_index(what, "block_table", block_table));
+    Q4_TRY(check_index(what, "seq_lens", seq_lens));
+    if (max_pages <= 0 || (long long)max_pages * cache->page_size > (1LL << 30))
+        return fail(Q4_EINVAL, "%s: max_pages must be >= 1 and hold up to 2^30 tokens (got %d)", what, max_pages);
+    if (!(scale > 0.f) || !std::isfinite(scale)) return fail(Q4_EINVAL, "%s: scale must be finite and > 0", what);
+    if (window < 0) return fail(Q4_EINVAL, "%s: window must be >= 0 (got %d)", what, window);
+    DeviceInfo di;
+    KvAttnArgs a = {*cache, out, lse, q, block_table, seq_lens, B, M, Hq, max_pages, q_stride, out_stride, scale, window,
+                    dtype, nullptr};
+    Q4_TRY(check_device_faults(what, &di, &a.fault));
+    const size_t need = kv4_attention_workspace_bytes(M, Hq / cache->num_kv_heads, cache->head_dim, dtype, di.sm_count);
+    if (need) {
+        if (!workspace) return fail(Q4_EINVAL, "%s: null workspace", what);
+        if (!aligned(workspace, 16)) return fail(Q4_EALIGN, "%s: workspace must be 16-byte aligned", what);
+        if (workspace_bytes < need)
+            return fail(Q4_EINVAL, "%s: the workspace holds %zu bytes, %zu are needed", what, workspace_bytes, need);
+    }
+    return finish(what, launch_kv4_attention(a, workspace, di.sm_count, (cudaStream_t)stream));
 }
 
 const char* q4_last_error(void) { return g_last_error.c_str(); }
