@@ -34,6 +34,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;      // tokens a warp takes at a time
 constexpr int kMaxB = 1024;    // sequences of a call
 constexpr int kStages = 3;     // tiles of a warp in flight or in use
+constexpr int kItemCost = 6;   // what starting on an item costs a CTA, in tiles
 
 template <int DB>
 struct Geo {
@@ -121,13 +122,15 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int len) {
     return s;
 }
 
-// prefix[b] = tiles (of one key head and chunk) of the sequences before b, prefix[B] = of all.
+// prefix[b] = cost (of one key head and chunk) of the sequences before b, prefix[B] = of all. An item costs its tiles and
+// kItemCost for its start: 64 ragged sequences with empty and one-token ones among them took 168 us where tiles alone
+// were divided (the CTA with all the short ones worked alone for 60 us).
 __device__ void scan_tiles(const KvAttnArgs& a, long long* prefix) {
     __shared__ long long warp_sum[kWarps];
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = threadIdx.x * per;
     long long sum = 0;
-    for (int b = b0; b < min(a.B, b0 + per); ++b) sum += span_of(a, a.seq_lens[b]).tiles;
+    for (int b = b0; b < min(a.B, b0 + per); ++b) sum += span_of(a, a.seq_lens[b]).tiles + kItemCost;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long up = sum;
 #pragma unroll
@@ -141,7 +144,7 @@ __device__ void scan_tiles(const KvAttnArgs& a, long long* prefix) {
     for (int w = 0; w < warp; ++w) at += warp_sum[w];
     for (int b = b0; b < min(a.B, b0 + per); ++b) {
         prefix[b] = at;
-        at += span_of(a, a.seq_lens[b]).tiles;
+        at += span_of(a, a.seq_lens[b]).tiles + kItemCost;
         if (b == a.B - 1) prefix[a.B] = at;
     }
     __syncthreads();
@@ -228,20 +231,25 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
     scan_tiles(a, prefix);
     const int items = a.c.num_kv_heads * p.chunks;
     const long long total = prefix[a.B] * items;
-    // an even share of all tiles, no less than one tile per warp
-    const long long share = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)kWarps);
+    // an even share of the cost, no less than an item of one tile per warp
+    const long long share = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)(kWarps + kItemCost));
     const long long begin = min(total, share * blockIdx.x), end = min(total, begin + share);
     if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
     for (long long at = begin; at < end;) {
-        // the item (sequence b, head h, chunk) that tile `at` belongs to, and how many of its tiles are this CTA's
+        // the item (sequence b, head h, chunk) that place `at` belongs to, and how many of its tiles are this CTA's
         int b = 0;
         for (int step = 512; step > 0; step >>= 1)
             if (b + step < a.B && prefix[b + step] * items <= at) b += step;
         const Span s = span_of(a, a.seq_lens[b]);
         const long long rem = at - prefix[b] * items;
-        const int item = (int)(rem / s.tiles), tile0 = (int)(rem - (long long)item * s.tiles);
-        const int count = (int)min(end - at, (long long)(s.tiles - tile0));
+        const int cost = s.tiles + kItemCost;
+        const int item = (int)(rem / cost), from = (int)(rem - (long long)item * cost);  // tiles follow the item's start
+        const int tile0 = max(from - kItemCost, 0);
+        const int count = (int)min(end - at + from - kItemCost, (long long)s.tiles) - tile0;
+        const long long item_at = at - from;
+        at = min(end, item_at + cost);
+        if (count <= 0) break;  // the share ends in the item's start: its tiles are the next CTA's
         const int h = item / p.chunks, row0 = (item - h * p.chunks) * ROWS;
         const int* table = a.block_table + (long long)b * a.max_pages;
         bool bad = s.bad;
@@ -254,24 +262,35 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
             if (page < 0 || page >= a.c.num_pages) return -2;
             return (int)cache_row(a.c, page, h, t & (a.c.page_size - 1));
         };
+        // lane's part of a tile's copies: chunk `lane % DB` of every (32 / DB)-th token, and the scales of token `lane`
+        const uint8_t *k_src = a.c.k_qs + (lane % DB) * 16, *v_src = a.c.v_qs + (lane % DB) * 16;
         auto issue = [&](int i, int row) {
             if (i * kWarps + warp < count) {
-                if (row == -2) bad = true;
                 const uint32_t st = base + (uint32_t)(i % kStages) * G::kStage;
+                const uint32_t ds = st + 2 * G::kCodes + (uint32_t)(lane * DB * 2);
+                auto copies = [&](auto all) {  // all: every token of the tile is read
+                    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-                for (int j = 0; j < DB; ++j) {
-                    const int tok = (j * 32 + lane) / DB, c = (j * 32 + lane) % DB;
-                    const int r = __shfl_sync(0xffffffffu, row, tok);
-                    const long long off = (long long)max(r, 0) * G::kRow + c * 16;
-                    const uint32_t dst = st + (uint32_t)(tok * G::kRow + swizzled<DB>(tok, c) * 16);
-                    const uint32_t bytes = r >= 0 ? 16u : 0u;
-                    copy_async<16>(dst, a.c.k_qs + off, bytes);
-                    copy_async<16>(dst + G::kCodes, a.c.v_qs + off, bytes);
+                    for (int j = 0; j < DB; ++j) {
+                        const int tok = (j * 32 + lane) / DB;
+                        const int r = __shfl_sync(0xffffffffu, row, tok);
+                        const long long off = (long long)(ALL ? r : max(r, 0)) * G::kRow;
+                        const uint32_t dst = st + (uint32_t)(tok * G::kRow + swizzled<DB>(tok, lane % DB) * 16);
+                        const uint32_t bytes = ALL || r >= 0 ? 16u : 0u;
+                        copy_async<16>(dst, k_src + off, bytes);
+                        copy_async<16>(dst + G::kCodes, v_src + off, bytes);
+                    }
+                    const long long off = (long long)(ALL ? row : max(row, 0)) * DB;
+                    const uint32_t bytes = ALL || row >= 0 ? DB * 2 : 0;
+                    copy_async<DB * 2>(ds, a.c.k_d + off, bytes);
+                    copy_async<DB * 2>(ds + G::kScales, a.c.v_d + off, bytes);
+                };
+                if (__all_sync(0xffffffffu, row >= 0)) {
+                    copies(std::true_type());
+                } else {
+                    if (row == -2) bad = true;
+                    copies(std::false_type());
                 }
-                const long long off = (long long)max(row, 0) * DB;
-                const uint32_t dst = st + 2 * G::kCodes + (uint32_t)(lane * DB * 2);
-                copy_async<DB * 2>(dst, a.c.k_d + off, row >= 0 ? DB * 2 : 0);
-                copy_async<DB * 2>(dst + G::kScales, a.c.v_d + off, row >= 0 ? DB * 2 : 0);
             }
             cp_async_commit();
         };
@@ -369,6 +388,8 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
             const uint32_t st = base + (uint32_t)(i % kStages) * G::kStage;
             const int tok0 = s.first + (tile0 + i * kWarps + warp) * kTile;
 
+            auto tile = [&](auto masked) {
+            constexpr bool MASKED = decltype(masked)::value;  // some row does not see every token
             // scores: sc[n][j] of row g, tokens 8 (j / 2) + 2 t4 + j % 2
             float sc[NT][8];
 #pragma unroll
@@ -423,15 +444,13 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
                 for (int k = 0; k < DB / 2; ++k) m = max(m, max(own[k] & 0x7C00u, (own[k] >> 16) & 0x7C00u));
                 e_run = max(e_run, (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 15);
             }
-            const bool inside = tok0 >= all_lo && tok0 >= s.lo && tok0 + kTile <= all_end;  // no token is masked
             bool moved = false;
             float keep[NT];
             uint32_t seen[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                seen[n] = 0xFFu;
-                if (!inside) {
-                    seen[n] = 0u;
+                seen[n] = 0u;
+                if constexpr (MASKED) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int t = tok0 + 8 * (j / 2) + 2 * t4 + j % 2;
@@ -469,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sc[n][j] = ex2(fmaf(sc[n][j], factor[n], -ref[n]));
-                    if (!inside && !(seen[n] >> j & 1u)) sc[n][j] = 0.f;  // also where the query is not finite
+                    if (MASKED && !(seen[n] >> j & 1u)) sc[n][j] = 0.f;  // also where the query is not finite
                     l[n] += sc[n][j];
                 }
             }
@@ -490,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float2 y = __fmul2_rn(make_float2(sc[n][2 * j], sc[n][2 * j + 1]), d);
-                        if (!inside) {  // a masked token's scale may be anything
+                        if constexpr (MASKED) {  // a masked token's scale may be anything
                             if (!(seen[n] >> (2 * j) & 1u)) y.x = 0.f;
                             if (!(seen[n] >> (2 * j + 1) & 1u)) y.y = 0.f;
                         }
@@ -518,6 +537,9 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
                     }
                 }
             }
+            };
+            if (tok0 >= all_lo && tok0 >= s.lo && tok0 + kTile <= all_end) tile(std::false_type());
+            else tile(std::true_type());
         }
         cp_async_wait<0>();
         bad = __any_sync(0xffffffffu, bad) != 0;
@@ -548,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
         if (bad && lane == 0) atomicOr(a.fault, s.bad ? (unsigned)kFaultBadLength : (unsigned)kFaultBadPage);
         __syncthreads();
         const bool whole = count == s.tiles;
-        const int slot = at == begin ? 0 : 1;
+        const int slot = item_at + kItemCost <= begin ? 0 : 1;  // an item that began before is this CTA's first
         float* part = p.part + ((long long)blockIdx.x * 2 + slot) * (ROWS * (D + 2));
         for (int idx = threadIdx.x; idx < ROWS * (D / 4); idx += kThreads) {
             const int r = idx / (D / 4), d4 = idx % (D / 4);
@@ -578,11 +600,9 @@ __global__ void __launch_bounds__(kThreads, Geo<DB>::kCtas) kv4_attention_kernel
         }
         if (threadIdx.x == 0 && tile0 == 0 && !whole) {
             // the item begins here: a join starts from this CTA
-            const long long item_end = at + s.tiles;
-            p.desc[blockIdx.x] = make_int4(b, item, (int)((item_end - 1) / share), slot);
+            p.desc[blockIdx.x] = make_int4(b, item, (int)((item_at + cost - 1) / share), slot);
         }
         __syncthreads();  // the join's memory is free for the next stages
-        at += count;
     }
 }
 
