@@ -370,15 +370,23 @@ class KV4Cache:
         return cls(*made)
 
 
-def _rows(t: torch.Tensor, heads: int, D: int, dtype: torch.dtype, device, name: str):
-    """(address, elements from one token to the next) of a tensor of token rows [..., heads, D]."""
-    if t.dtype != dtype:
+# These calls take a few microseconds on the device, so the checks below are written to cost the host as little: one
+# pass over each tensor's properties, and the stream's handle without a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _rows(t: torch.Tensor, heads: int, D: int, dtype: torch.dtype, dev: int, name: str):
+    """(address, elements from one token to the next) of a tensor of token rows [..., heads, D] on device `dev`."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    shape, st = t.shape, t.stride()
-    if len(shape) < 3 or shape[-2] != heads or shape[-1] != D:
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on device {dev}, got {t.device}")
+    shape = t.shape
+    if len(shape) < 3 or shape[-1] != D or shape[-2] != heads:
         raise ValueError(f"{name}: expected [..., {heads}, {D}], got {list(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * D
+    st = t.stride()
     if st[-1] != 1 or (heads > 1 and st[-2] != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     # token axes must lie evenly: the outer ones follow from the innermost that has more than one token
@@ -393,47 +401,44 @@ def _rows(t: torch.Tensor, heads: int, D: int, dtype: torch.dtype, device, name:
     return t.data_ptr(), step if n > 1 else heads * D
 
 
-def _index(t: torch.Tensor, device, name: str, shape: tuple) -> int:
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name}: expected torch.int32, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _floats(t: torch.Tensor | None, device, name: str, numel: int) -> int | None:
-    if t is None:
-        return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+def _flat(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str, numel: int) -> int:
+    """Address of a contiguous tensor of `numel` values on device `dev`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on device {dev}, got {t.device}")
     if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {numel} contiguous values")
+        raise ValueError(f"{name}: expected {numel} contiguous values, got {list(t.shape)}")
     return t.data_ptr()
 
 
 def _act(t: torch.Tensor, name: str):
-    """(C code of the activation type, device) of a call, from its first activation."""
+    """(C code of the activation type, device index) of a call, from its first activation."""
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    return code, t.device
+    return code, dev
 
 
-def _call(fn, device, stream, *args) -> None:
-    """Call a C entry on the tensors' device (made current if it is not) and the given or current stream of it."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+def _stream_on(dev: int, stream) -> int:
+    """Handle of the given stream, or of the current stream of device `dev`."""
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(fn, dev: int, *args) -> None:
+    """Call a C entry with the tensors' device current."""
+    if dev == torch.cuda.current_device():
+        rc = fn(*args)
     else:
-        _check(fn(*args, _stream(stream)))
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc:
+        _check(rc)
 
 
 def qk_norm_rope(q_out, k_out, q, k, q_gamma, k_gamma, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False,
@@ -442,39 +447,42 @@ def qk_norm_rope(q_out, k_out, q, k, q_gamma, k_gamma, cos_sin, positions, eps: 
     rotation of the first ``cos_sin.shape[1]`` elements by the table row cos_sin[positions[t]] (cos, then sin; None: no
     rotation). The outputs may be the inputs."""
     code, dev = _act(q, "q")
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    shape, k_shape, dt = q.shape, k.shape, q.dtype
+    if len(shape) != 3 or len(k_shape) != 3 or shape[0] != k_shape[0] or shape[2] != k_shape[2]:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    if q_out.shape != shape or k_out.shape != k_shape:
         raise ValueError("q_out must be [T, Hq, D] and k_out [T, Hkv, D]")
+    T, Hq, D = shape
+    Hkv = k_shape[1]
     max_pos = rot = 0
     table = where = None
     if cos_sin is not None:
         max_pos, rot = cos_sin.shape
-        table = _floats(cos_sin, dev, "cos_sin", max_pos * rot)
-        where = _index(positions, dev, "positions", (T,))
-    qp, qs = _rows(q, Hq, D, q.dtype, dev, "q")
-    kp, ks = _rows(k, Hkv, D, q.dtype, dev, "k")
-    qop, qos = _rows(q_out, Hq, D, q.dtype, dev, "q_out")
-    kop, kos = _rows(k_out, Hkv, D, q.dtype, dev, "k_out")
-    _call(load().qk_norm_rope, dev, stream, qop, kop, qp, kp, _floats(q_gamma, dev, "q_gamma", D),
-          _floats(k_gamma, dev, "k_gamma", D), eps, table, where, T, Hq, Hkv, D, rot, max_pos, 1 if interleaved else 0, qs,
-          ks, qos, kos, code)
+        table = _flat(cos_sin, torch.float32, dev, "cos_sin", max_pos * rot)
+        where = _flat(positions, torch.int32, dev, "positions", T)
+    qp, qs = _rows(q, Hq, D, dt, dev, "q")
+    kp, ks = _rows(k, Hkv, D, dt, dev, "k")
+    qop, qos = _rows(q_out, Hq, D, dt, dev, "q_out")
+    kop, kos = _rows(k_out, Hkv, D, dt, dev, "k_out")
+    _call(load().qk_norm_rope, dev, qop, kop, qp, kp,
+          None if q_gamma is None else _flat(q_gamma, torch.float32, dev, "q_gamma", D),
+          None if k_gamma is None else _flat(k_gamma, torch.float32, dev, "k_gamma", D), eps, table, where, T, Hq, Hkv, D, rot,
+          max_pos, 1 if interleaved else 0, qs, ks, qos, kos, code, _stream_on(dev, stream))
 
 
 def kv4_write(cache: KV4Cache, k, v, slots, stream=None) -> None:
     """Quantise k and v [T, num_kv_heads, head_dim] into the cache's slots (int32 [T]; negative: skipped; the others
     distinct)."""
     code, dev = _act(k, "k")
-    T, H, D = k.shape[0], cache.num_kv_heads, cache.head_dim
-    if k.dim() != 3 or v.shape != k.shape:
+    shape, dt, H, D = k.shape, k.dtype, cache.num_kv_heads, cache.head_dim
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must be [T, num_kv_heads, head_dim]")
-    if dev != cache.device:
-        raise ValueError(f"k: expected a tensor on {cache.device}, got {dev}")
-    kp, ks = _rows(k, H, D, k.dtype, dev, "k")
-    vp, vs = _rows(v, H, D, k.dtype, dev, "v")
-    _call(load().kv4_write, dev, stream, cache._ref, kp, vp, _index(slots, dev, "slots", (T,)), T, ks, vs, code)
+    if dev != cache.device.index:
+        raise ValueError(f"k: expected a tensor on {cache.device}, got {k.device}")
+    kp, ks = _rows(k, H, D, dt, dev, "k")
+    vp, vs = _rows(v, H, D, dt, dev, "v")
+    _call(load().kv4_write, dev, cache._ref, kp, vp, _flat(slots, torch.int32, dev, "slots", shape[0]), shape[0], ks, vs, code,
+          _stream_on(dev, stream))
 
 
 def kv4_read(k_out, v_out, cache: KV4Cache, slots, stream=None) -> None:
@@ -484,25 +492,27 @@ def kv4_read(k_out, v_out, cache: KV4Cache, slots, stream=None) -> None:
     if first is None:
         raise ValueError("k_out and v_out cannot both be None")
     code, dev = _act(first, "k_out" if k_out is not None else "v_out")
-    T, H, D = first.shape[0], cache.num_kv_heads, cache.head_dim
-    if first.dim() != 3 or (v_out is not None and v_out.shape != first.shape):
+    shape, dt, H, D = first.shape, first.dtype, cache.num_kv_heads, cache.head_dim
+    if len(shape) != 3 or (v_out is not None and v_out.shape != shape):
         raise ValueError("k_out and v_out must be [T, num_kv_heads, head_dim]")
-    if dev != cache.device:
-        raise ValueError(f"k_out: expected a tensor on {cache.device}, got {dev}")
-    kp, ks = (None, 0) if k_out is None else _rows(k_out, H, D, first.dtype, dev, "k_out")
-    vp, vs = (None, 0) if v_out is None else _rows(v_out, H, D, first.dtype, dev, "v_out")
-    _call(load().kv4_read, dev, stream, kp, vp, cache._ref, _index(slots, dev, "slots", (T,)), T, ks, vs, code)
+    if dev != cache.device.index:
+        raise ValueError(f"k_out: expected a tensor on {cache.device}, got {first.device}")
+    kp, ks = (None, 0) if k_out is None else _rows(k_out, H, D, dt, dev, "k_out")
+    vp, vs = (None, 0) if v_out is None else _rows(v_out, H, D, dt, dev, "v_out")
+    _call(load().kv4_read, dev, kp, vp, cache._ref, _flat(slots, torch.int32, dev, "slots", shape[0]), shape[0], ks, vs, code,
+          _stream_on(dev, stream))
 
 
 def kv4_attention_workspace(q, cache: KV4Cache) -> torch.Tensor:
     """Workspace for kv4_attention calls with q's [..., M, Hq, D] and type over `cache` (any batch and lengths). Calls that
     may run at the same time (other streams, other graphs) need one each."""
     code, dev = _act(q, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, M, Hq, D] or [B, Hq, D]")
     M, Hq = (1, q.shape[1]) if q.dim() == 3 else q.shape[1:3]
     need = ctypes.c_size_t(0)
-    with torch.cuda.device(dev):
-        _check(load().kv4_attention_workspace(ctypes.byref(need), M, Hq, cache.num_kv_heads, cache.head_dim, code))
-    return torch.empty(max(16, need.value), dtype=torch.uint8, device=dev)
+    _call(load().kv4_attention_workspace, dev, ctypes.byref(need), M, Hq, cache.num_kv_heads, cache.head_dim, code)
+    return torch.empty(max(16, need.value), dtype=torch.uint8, device=q.device)
 
 
 def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float | None = None, window: int = 0, lse=None,
@@ -512,29 +522,35 @@ def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float |
     tokens, lse float32 [B, M, Hq] or None. workspace: from kv4_attention_workspace, kept between calls; None: allocated
     for this call."""
     code, dev = _act(q, "q")
-    if q.dim() not in (3, 4) or out.shape != q.shape:
-        raise ValueError("q and out must be [B, M, Hq, D] or [B, Hq, D]")
-    B, Hq, D = q.shape[0], q.shape[-2], cache.head_dim
-    M = q.shape[1] if q.dim() == 4 else 1
-    if dev != cache.device:
-        raise ValueError(f"q: expected a tensor on {cache.device}, got {dev}")
-    if block_table.dim() != 2:
+    shape, dt, D = q.shape, q.dtype, cache.head_dim
+    if len(shape) == 4:
+        B, M, Hq, _ = shape
+    elif len(shape) == 3:
+        B, Hq, _ = shape
+        M = 1
+    else:
+        raise ValueError("q must be [B, M, Hq, D] or [B, Hq, D]")
+    if out.shape != shape:
+        raise ValueError("out must have q's shape")
+    if dev != cache.device.index:
+        raise ValueError(f"q: expected a tensor on {cache.device}, got {q.device}")
+    table_shape = block_table.shape
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    qp, qs = _rows(q, Hq, D, q.dtype, dev, "q")
-    op, os_ = _rows(out, Hq, D, q.dtype, dev, "out")
-    max_pages = block_table.shape[1]
+    qp, qs = _rows(q, Hq, D, dt, dev, "q")
+    op, os_ = _rows(out, Hq, D, dt, dev, "out")
     if workspace is None:
         # on the stream that uses it, so that the allocator hands it on only to work behind this call
         s = torch.cuda.current_stream(dev) if stream is None else (
             stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev))
         with torch.cuda.stream(s):
             workspace = kv4_attention_workspace(q, cache)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
-    _call(load().kv4_attention, dev, stream, op, _floats(lse, dev, "lse", B * M * Hq), qp, cache._ref,
-          _index(block_table, dev, "block_table", (B, max_pages)), _index(seq_lens, dev, "seq_lens", (B,)), B, M, Hq,
-          max_pages, qs, os_, D ** -0.5 if scale is None else scale, window, code, _ptr(workspace, torch.uint8, "workspace"),
-          workspace.numel())
+    size = workspace.numel()
+    _call(load().kv4_attention, dev, op, None if lse is None else _flat(lse, torch.float32, dev, "lse", B * M * Hq), qp,
+          cache._ref, _flat(block_table, torch.int32, dev, "block_table", B * table_shape[1]),
+          _flat(seq_lens, torch.int32, dev, "seq_lens", B), B, M, Hq, table_shape[1], qs, os_,
+          D ** -0.5 if scale is None else scale, window, code, _flat(workspace, torch.uint8, dev, "workspace", size), size,
+          _stream_on(dev, stream))
 
 
 def q4_device_faults() -> int:

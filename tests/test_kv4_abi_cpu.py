@@ -127,7 +127,7 @@ def test_the_binding_refuses_before_it_calls():
 
 
 def test_token_rows():
-    rows = lambda t, H, D: q4._rows(t, H, D, torch.float32, t.device, "t")[1]  # noqa: E731
+    rows = lambda t, H, D: q4._rows(t, H, D, torch.float32, -1, "t")[1]  # noqa: E731
     base = torch.zeros(4, 3, 10, 32)
     assert rows(base, 10, 32) == 320 and rows(base[:, :, 2:7], 5, 32) == 320
     assert rows(base[:, :1], 10, 32) == 960 and rows(base[:1, :1], 10, 32) == 320
@@ -136,4 +136,4 @@ def test_token_rows():
         with pytest.raises(ValueError):
             rows(bad, bad.shape[-2], bad.shape[-1] if bad.shape[-1] != 16 else 32)
     with pytest.raises(TypeError):
-        q4._rows(base, 10, 32, torch.float16, base.device, "t")
+        q4._rows(base, 10, 32, torch.float16, -1, "t")
