@@ -25,6 +25,8 @@
 //     the lengths. A warp walks its piece without meeting another warp, its copies running ahead across items; it writes
 //     the outputs of items that it holds whole, and parts of the others, which a second kernel joins in a fixed order.
 //   - whole items: one CTA per item, its warps' tiles interleaved and joined through shared memory; one launch.
+#include <algorithm>
+
 #include "kv_common.cuh"
 
 namespace q4 {
@@ -55,7 +57,8 @@ struct Params {
     int4* desc;   // [warps]: the item that begins in a warp's piece and ends in a later one's: (sequence, head * chunks +
                   // chunk, last warp, slot of the first part); -1: none
     int R, group, chunks, lp;  // rows per key head, query heads per key head, chunks of 8 NT rows, log2(page size)
-    int warps;                 // streaming warps
+    int warps;                 // streaming warps; 0: whole or split items
+    int splits;                // CTAs of an item
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -556,14 +559,18 @@ __global__ void __launch_bounds__(kItemWarps * 32, Geo<DB>::kItemCtas) kv4_atten
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const int chunk = blockIdx.x % p.chunks, h = blockIdx.x / p.chunks, b = blockIdx.y, row0 = chunk * ROWS;
+    const int item = blockIdx.x / p.splits, split = blockIdx.x - item * p.splits;
+    const int h = item / p.chunks, b = blockIdx.y, row0 = (item - h * p.chunks) * ROWS;
     const Span s = span_of(a, a.seq_lens[b]);
     const int* table = a.block_table + (long long)b * a.max_pages;
     bool bad = s.bad;
-    const int mine = (s.tiles - warp + kItemWarps - 1) / kItemWarps;
-    int ahead = s.first + warp * kTile + w.lane;  // this lane's token of the next tile to look up
+    // this CTA's tiles of the item, and where they end
+    const int tile0 = (int)((long long)s.tiles * split / p.splits), tile1 = (int)((long long)s.tiles * (split + 1) / p.splits);
+    const int mine = max(tile1 - tile0 - warp + kItemWarps - 1, 0) / kItemWarps;
+    const int first = s.first + tile0 * kTile, end = min(s.n, s.first + tile1 * kTile);
+    int ahead = first + warp * kTile + w.lane;  // this lane's token of the next tile to look up
     auto lookup = [&] {
-        const int row = row_of(p, table, h, ahead, s.lo, s.n);
+        const int row = row_of(p, table, h, ahead, s.lo, end);
         ahead += kItemWarps * kTile;
         return row;
     };
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(kItemWarps * 32, Geo<DB>::kItemCtas) kv4_atten
         }
         ring.filled();
         next = lookup();
-        w.take(ring.out, s.first + (i * kItemWarps + warp) * kTile);
+        w.take(ring.out, first + (i * kItemWarps + warp) * kTile);
         ring.used();
     }
     cp_async_wait<0>();
@@ -606,6 +613,7 @@ __global__ void __launch_bounds__(kItemWarps * 32, Geo<DB>::kItemCtas) kv4_atten
         *reinterpret_cast<float2*>(jo + (warp * ROWS + 8 * n + 2 * w.t4 + i) * G::kJoinRow + e) = v;
     });
     __syncthreads();
+    float* part = p.part + ((long long)b * gridDim.x + blockIdx.x) * (ROWS * (D + 2));
     for (int idx = threadIdx.x; idx < ROWS * (D / 4); idx += kItemWarps * 32) {
         const int r = idx / (D / 4), d4 = idx % (D / 4);
         if (row0 + r >= p.R) continue;
@@ -623,9 +631,14 @@ __global__ void __launch_bounds__(kItemWarps * 32, Geo<DB>::kItemCtas) kv4_atten
                 v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
             }
         }
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        store_out4(a, out_at(p, b, h, row0 + r, D) + 4 * d4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-        if (a.lse && d4 == 0) a.lse[lse_at(p, b, h, row0 + r)] = lse_of(rt, lt);
+        if (p.splits == 1) {
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;
+            store_out4(a, out_at(p, b, h, row0 + r, D) + 4 * d4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            if (a.lse && d4 == 0) a.lse[lse_at(p, b, h, row0 + r)] = lse_of(rt, lt);
+        } else {
+            *reinterpret_cast<float4*>(part + r * D + 4 * d4) = v;
+            if (d4 == 0) part[ROWS * D + r] = rt, part[ROWS * D + ROWS + r] = lt;
+        }
     }
 }
 
@@ -824,58 +837,88 @@ __global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams
     cp_async_wait<0>();
 }
 
-// Joins the parts of the items that were divided between warps: block (w, y) rows y, y + gridDim.y, ... of the item that
-// begins in warp w's piece. Every warp of the block sums every fourth part, and the four sums are added in order.
-constexpr int kJoinWarps = 4;
-template <int DB, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv4_attention_join_kernel(const Params p) {
-    constexpr int D = DB * 32, ROWS = 8 * NT;
-    __shared__ float so[kJoinWarps][D], sl[kJoinWarps], sm[kJoinWarps];
+// Joins the parts of an item that was divided: block x the item that begins in piece x (streams) or item x, ROWS / gridDim.y
+// of its rows. A block's threads stand over rows, parts and groups of four elements; every sum has a fixed order.
+constexpr int kJoinThreads = 256;
+template <int DB, int NT, int RPB>  // RPB: rows a block
+__global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const Params p) {
+    constexpr int D = DB * 32, ROWS = 8 * NT, D4 = D / 4;
+    constexpr int RT = RPB * D4 <= kJoinThreads ? RPB : kJoinThreads / D4;  // rows at a time
+    constexpr int PT = kJoinThreads / (RT * D4);                            // parts at a time
+    __shared__ float4 so[PT][RT][D4];
+    __shared__ float sl[PT][RT], sm[PT][RT];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int4 ds = p.desc[blockIdx.x];
-    if (ds.x < 0) return;
-    const int h = ds.y / p.chunks, row0 = (ds.y - h * p.chunks) * ROWS;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = blockIdx.x, n = ds.z - c0 + 1;
-    auto part = [&](int i) { return p.part + ((long long)(c0 + i) * 2 + (i == 0 ? ds.w : 0)) * (ROWS * (D + 2)); };
-    for (int r = blockIdx.y; r < ROWS && row0 + r < p.R; r += gridDim.y) {
+    int b, item, n;
+    const float* part0;  // the first part; the others follow, two slots apart in streams
+    const int stride = ROWS * (D + 2);
+    long long step;
+    if (p.warps) {
+        const int4 ds = p.desc[blockIdx.x];
+        if (ds.x < 0) return;
+        b = ds.x, item = ds.y, n = ds.z - (int)blockIdx.x + 1;
+        part0 = p.part + ((long long)blockIdx.x * 2 + ds.w) * stride;
+        step = 2 * stride - ds.w * stride;  // to slot 0 of the next piece
+    } else {
+        const int items = p.a.c.num_kv_heads * p.chunks;
+        b = blockIdx.x / items, item = blockIdx.x - b * items, n = p.splits;
+        part0 = p.part + (long long)blockIdx.x * n * stride;
+        step = stride;
+    }
+    const int h = item / p.chunks, row0 = (item - h * p.chunks) * ROWS;
+    auto part = [&](int i) { return i == 0 ? part0 : part0 + step + (long long)(i - 1) * (p.warps ? 2 * stride : stride); };
+    const int d4 = threadIdx.x % D4, rt = threadIdx.x / D4 % RT, pt = threadIdx.x / (D4 * RT);
+    for (int r0 = blockIdx.y * RPB; r0 < (int)(blockIdx.y + 1) * RPB; r0 += RT) {
+        const int r = r0 + rt;
+        if (row0 + r0 >= p.R) break;  // the same for the whole block
+        // the largest reference: a thread's share of the parts, then over the threads of its row
         float top = -INFINITY;
-        for (int i = threadIdx.x; i < n; i += kJoinWarps * 32) top = fmaxf(top, part(i)[ROWS * D + r]);
+        for (int i = pt * D4 + d4; i < n; i += PT * D4) top = fmaxf(top, part(i)[ROWS * D + r]);
 #pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        if (lane == 0) sm[warp] = top;
-        __syncthreads();
+        for (int x = (D4 < 32 ? D4 : 32) / 2; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        if constexpr (D4 > 32) {  // a row's elements take two warps
+            __shared__ float halves[kJoinThreads / 32];
+            if ((threadIdx.x & 31) == 0) halves[threadIdx.x / 32] = top;
+            __syncthreads();
+            top = fmaxf(top, halves[(threadIdx.x / 32) ^ 1]);
+        }
+        if constexpr (PT > 1) {
+            if (d4 == 0) sm[pt][rt] = top;
+            __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kJoinWarps; ++u) top = fmaxf(top, sm[u]);
-        float v[DB] = {}, l = 0.f;
+            for (int u = 0; u < PT; ++u) top = fmaxf(top, sm[u][rt]);
+        }
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
         if (top != -INFINITY) {
 #pragma unroll 8
-            for (int i = warp; i < n; i += kJoinWarps) {
+            for (int i = pt; i < n; i += PT) {
                 const float* x = part(i);
-                const float f = ex2(x[ROWS * D + r] - top);  // 0 for a part that saw nothing (reference -infinity)
-                l = fmaf(x[ROWS * D + ROWS + r], f, l);
-#pragma unroll
-                for (int k = 0; k < DB; ++k) v[k] = fmaf(x[r * D + 32 * k + lane], f, v[k]);
+                const float4 o = *reinterpret_cast<const float4*>(x + r * D + 4 * d4);
+                const float ref = x[ROWS * D + r], pl = x[ROWS * D + ROWS + r];
+                if (ref == -INFINITY) continue;  // saw nothing; its elements were not computed
+                const float f = ex2(ref - top);
+                l = fmaf(pl, f, l);
+                v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
             }
         }
+        if constexpr (PT > 1) {
+            so[pt][rt][d4] = v;
+            if (d4 == 0) sl[pt][rt] = l;
+            __syncthreads();
+            if (pt == 0) {
 #pragma unroll
-        for (int k = 0; k < DB; ++k) so[warp][32 * k + lane] = v[k];
-        if (lane == 0) sl[warp] = l;
-        __syncthreads();
-        float lt = 0.f;
-#pragma unroll
-        for (int u = 0; u < kJoinWarps; ++u) lt += sl[u];
-        for (int d4 = threadIdx.x; d4 < D / 4; d4 += kJoinWarps * 32) {
-            float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int u = 0; u < kJoinWarps; ++u) {
-                const float4 x = *reinterpret_cast<const float4*>(&so[u][4 * d4]);
-                t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+                for (int u = 1; u < PT; ++u) {
+                    const float4 o = so[u][rt][d4];
+                    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                    l += sl[u][rt];
+                }
             }
-            const float inv = lt == 0.f ? 0.f : 1.f / lt;
-            store_out4(p.a, out_at(p, ds.x, h, row0 + r, D) + 4 * d4, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
-            if (p.a.lse && d4 == 0) p.a.lse[lse_at(p, ds.x, h, row0 + r)] = lse_of(top, lt);
+        }
+        if (pt == 0 && row0 + r < p.R) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            store_out4(p.a, out_at(p, b, h, row0 + r, D) + 4 * d4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            if (p.a.lse && d4 == 0) p.a.lse[lse_at(p, b, h, row0 + r)] = lse_of(top, l);
         }
         __syncthreads();
     }
@@ -932,22 +975,30 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
         p.R = group * a.M;
         p.group = group;
         p.chunks = (p.R + 8 * NT - 1) / (8 * NT);
+        p.splits = 1;
         p.lp = 0;
         while ((1 << p.lp) < a.c.page_size) ++p.lp;
         const int items = a.c.num_kv_heads * p.chunks;
-        if ((long long)a.max_pages * a.c.page_size <= kItemTokens) {
+        auto join = [&](unsigned blocks, bool few) {  // few items: a row a block
+            // It may be scheduled while the parts are computed, whatever the overlap setting: both are this call's own.
+            return few ? launch_grid(kv4_attention_join_kernel<DB, NT, 1>, dim3(blocks, 8 * NT), dim3(kJoinThreads), 0, s, true, p)
+                       : launch_grid(kv4_attention_join_kernel<DB, NT, 8 * NT>, dim3(blocks), dim3(kJoinThreads), 0, s, true, p);
+        };
+        const long long most = (long long)a.max_pages * a.c.page_size;
+        if (most <= kItemTokens || a.B == 1) {
             constexpr int kRing = kItemWarps * G::kStages * G::kStage;
             static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
-            return launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT>, dim3((unsigned)items, (unsigned)a.B),
-                                    kItemWarps * 32, kRing, s, p);
+            p.warps = 0;
+            if (most > kItemTokens)
+                p.splits = (int)std::max(1LL, std::min<long long>(sm_count * G::kItemCtas / items, most / (kTile * kItemWarps)));
+            cudaError_t e = launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT>, dim3((unsigned)(items * p.splits), (unsigned)a.B),
+                                             kItemWarps * 32, kRing, s, p);
+            if (e == cudaSuccess && p.splits > 1) e = join((unsigned)items, true);
+            return e;
         }
         cudaError_t e = launch_with_ring(kv4_attention_streams_kernel<DB, NT, SPLIT>, dim3((unsigned)sm_count), G::kWarps * 32,
                                          G::kWarps * G::kStages * G::kStage, s, p);
-        // the join may be scheduled while the streams end, whatever the overlap setting: both are this call's own. A row a
-        // block where the items are few and their parts many.
-        if (e == cudaSuccess)
-            e = launch_grid(kv4_attention_join_kernel<DB, NT>, dim3((unsigned)p.warps, items * a.B <= 64 ? 8 * NT : 1),
-                            dim3(kJoinWarps * 32), 0, s, true, p);
+        if (e == cudaSuccess) e = join((unsigned)p.warps, items * a.B <= 64);
         return e;
     });
 }
