@@ -491,7 +491,7 @@ int kv4_attention_workspace(size_t* bytes, int M, int Hq, int Hkv, int D, int dt
     Q4_TRY(check_attention_sizes(what, M, Hq, Hkv, D, dtype));
     DeviceInfo di;
     Q4_TRY(check_device(what, &di));
-    *bytes = kv4_attention_workspace_bytes(M, Hq / Hkv, D, dtype, di.sm_count);
+    *bytes = kv4_attention_workspace_bytes(M, Hq / Hkv, Hkv, D, dtype, di.sm_count);
     return finish(what, cudaSuccess);
 }
 
@@ -516,7 +516,7 @@ int kv4_attention(void* out, float* lse, const void* q, const kv4_cache* cache, 
     KvAttnArgs a = {*cache, out, lse, q, block_table, seq_lens, B, M, Hq, max_pages, q_stride, out_stride, scale, window,
                     dtype, nullptr};
     Q4_TRY(check_device_faults(what, &di, &a.fault));
-    const size_t need = kv4_attention_workspace_bytes(M, Hq / cache->num_kv_heads, cache->head_dim, dtype, di.sm_count);
+    const size_t need = kv4_attention_workspace_bytes(M, Hq / cache->num_kv_heads, cache->num_kv_heads, cache->head_dim, dtype, di.sm_count);
     if (need) {
         if (!workspace) return fail(Q4_EINVAL, "%s: null workspace", what);
         if (!aligned(workspace, 16)) return fail(Q4_EALIGN, "%s: workspace must be 16-byte aligned", what);

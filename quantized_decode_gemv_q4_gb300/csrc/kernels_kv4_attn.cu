@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kTile = 32;       // tokens a warp takes at a time
 constexpr int kMaxB = 1024;     // sequences of a call
-constexpr int kItemCost = 2;    // what starting on an item costs a streaming warp, in tiles
+constexpr int kItemCost = 4;    // what starting on an item costs a streaming warp, in tiles
 constexpr int kItemWarps = 4;   // warps of a CTA that takes whole items
 
 template <int DB>
@@ -45,17 +45,22 @@ struct Geo {
     static constexpr int kCodes = kTile * kRow;            // of a tile
     static constexpr int kScales = kTile * DB * 2;
     static constexpr int kStage = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
-    static constexpr int kStages = DB == 2 ? 5 : 3;        // tiles of a warp in flight or in use
-    static constexpr int kWarps = DB == 8 ? 8 : 12;        // streaming warps of an SM, all in one CTA
-    static constexpr int kItemCtas = DB == 8 ? 2 : 3;      // CTAs of whole items per SM
     static constexpr int kJoinRow = D + 4;                 // floats; the pad spreads the joining stores over the banks
+};
+
+// Warps and stages (tiles of a warp in flight or in use), by registers: 12 warps of up to 168 or 8 of up to 255 on an SM.
+template <int DB, int NT, bool SPLIT>
+struct Plan {
+    static constexpr bool kTwelve = DB == 2 || (DB == 4 && NT == 1);
+    static constexpr int kWarps = kTwelve ? 12 : 8;       // streaming warps of an SM, all in one CTA
+    static constexpr int kItemCtas = kTwelve ? 3 : 2;     // CTAs of whole items per SM
+    static constexpr int kStages = DB == 2 ? 5 : DB == 4 && !kTwelve ? 4 : 3;
 };
 
 struct Params {
     KvAttnArgs a;
     float* part;  // [warps][2][8 NT * (D + 2)]
-    int4* desc;   // [warps]: the item that begins in a warp's piece and ends in a later one's: (sequence, head * chunks +
-                  // chunk, last warp, slot of the first part); -1: none
+    int2* desc;   // [B * items]: the parts of an item (1: it was whole), the first one's warp * 2 + slot
     int R, group, chunks, lp;  // rows per key head, query heads per key head, chunks of 8 NT rows, log2(page size)
     int warps;                 // streaming warps; 0: whole or split items
     int splits;                // CTAs of an item
@@ -226,8 +231,6 @@ struct Rows {
     __device__ __forceinline__ void start(const Params& p, int b, int h, int row0, const Span& s) {
         const KvAttnArgs& a = p.a;
 #pragma unroll
-        for (int i = 0; i < MT * DB * 2 * 4; ++i) (&qa[0][0][0][0])[i] = 0u;
-#pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = row0 + n * 8 + g;
             const bool there = r < p.R;
@@ -275,7 +278,8 @@ struct Rows {
                 for (int i = 0; i < 2; ++i) {
                     qa[mt][k][i][hi] = pack_half2(xh[i], xh[i + 2]);
                     qa[mt][k][i][2 + hi] = pack_half2(xh[4 + i], xh[6 + i]);
-                    if constexpr (SPLIT) {
+                    // (of 16-bit queries the low parts are zeros, which fill rows that a single group of 8 leaves free)
+                    if constexpr (SPLIT || NT == 1) {
                         qa[mt][k][i][1] = pack_half2(xl[i], xl[i + 2]);
                         qa[mt][k][i][3] = pack_half2(xl[4 + i], xl[6 + i]);
                     }
@@ -307,27 +311,31 @@ struct Rows {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 8; ++j) sc[n][j] = 0.f;
-        uint32_t kd[4][DB];
+        uint32_t kd[4][DB], kw[DB][4];
+#pragma unroll
+        for (int k = 0; k < DB; ++k) ldsm4(codes ^ (uint32_t)(16 * k), kw[k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) lds_words<DB>(scales + (uint32_t)(8 * j * DB * 2), kd[j]);
 #pragma unroll
-        for (int k = 0; k < DB; ++k) {
-            uint32_t w[4];
-            ldsm4(codes ^ (uint32_t)(16 * k), w);
+        for (int kk = 0; kk < DB; kk += 2) {
+            uint32_t x[8][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 da = to_float2(kd[j][k / 2]), db = to_float2(kd[j][DB / 2 + k / 2]);
-                const float2 d = make_float2(k % 2 ? da.y : da.x, k % 2 ? db.y : db.x);
-                uint32_t x[4];
-                codes_of(w[j], k1024, x);
+            for (int j = 0; j < 8; ++j) codes_of(kw[kk + j / 4][j % 4], k1024, x[j]);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                    float c[4];
-                    mma(c, qa[mt][k][0], x[0], x[1], zero);
-                    mma(c, qa[mt][k][1], x[2], x[3], c);
+            for (int mt = 0; mt < MT; ++mt) {
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                float c[8][4];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mma(c[j], qa[mt][kk + j / 4][0], x[j][0], x[j][1], zero);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mma(c[j], qa[mt][kk + j / 4][1], x[j][2], x[j][3], c[j]);
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj) {
+                    const int j = jj % 4, k = kk + jj / 4;
+                    const float2 da = to_float2(kd[j][k / 2]), db = to_float2(kd[j][DB / 2 + k / 2]);
+                    const float2 d = make_float2(k % 2 ? da.y : da.x, k % 2 ? db.y : db.x);
                     if constexpr (SPLIT) {
-                        const float2 both = fadd2(make_float2(c[0], c[1]), make_float2(c[2], c[3]));
+                        const float2 both = fadd2(make_float2(c[jj][0], c[jj][1]), make_float2(c[jj][2], c[jj][3]));
                         const float2 y = ffma2(both, d, make_float2(sc[mt][2 * j], sc[mt][2 * j + 1]));
                         sc[mt][2 * j] = y.x, sc[mt][2 * j + 1] = y.y;
                     } else {
@@ -335,7 +343,7 @@ struct Rows {
                         for (int u = 0; u < 2; ++u) {
                             const int n = 2 * mt + u;
                             if (n < NT) {
-                                const float2 y = ffma2(make_float2(c[2 * u], c[2 * u + 1]), d,
+                                const float2 y = ffma2(make_float2(c[jj][2 * u], c[jj][2 * u + 1]), d,
                                                        make_float2(sc[n][2 * j], sc[n][2 * j + 1]));
                                 sc[n][2 * j] = y.x, sc[n][2 * j + 1] = y.y;
                             }
@@ -409,8 +417,10 @@ struct Rows {
         for (int j = 0; j < 4; ++j) lds_words<DB>(scales + (uint32_t)(G::kScales + 8 * j * DB * 2), vd[j]);
 #pragma unroll
         for (int k = 0; k < DB; ++k) {
-            uint32_t w[4];
+            uint32_t w[4], x[4][4];
             ldsm4_trans((codes ^ (uint32_t)(16 * k)) + G::kCodes, w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) codes_of(w[u], k1024, x[u]);
             uint32_t hi[NT][4], lo[SPLIT ? NT : 1][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -432,10 +442,8 @@ struct Rows {
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint32_t x[4], y[4];
-                codes_of(w[2 * u], k1024, x);
-                codes_of(w[2 * u + 1], k1024, y);
-                const uint32_t a0[4] = {x[0], x[1], y[0], y[1]}, a1[4] = {x[2], x[3], y[2], y[3]};
+                const uint32_t a0[4] = {x[2 * u][0], x[2 * u][1], x[2 * u + 1][0], x[2 * u + 1][1]};
+                const uint32_t a1[4] = {x[2 * u][2], x[2 * u][3], x[2 * u + 1][2], x[2 * u + 1][3]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     mma(o[n][k][0], a0, hi[n][2 * u], hi[n][2 * u + 1], o[n][k][0]);
@@ -478,7 +486,7 @@ struct Rows {
 };
 
 // A warp's ring of stages, and its copies into it.
-template <int DB>
+template <int DB, int STAGES>
 struct Ring {
     using G = Geo<DB>;
     uint32_t base, in, out;  // shared addresses: of the ring, of the stage to fill next, of the stage to use next
@@ -492,7 +500,7 @@ struct Ring {
     }
     static __device__ __forceinline__ uint32_t after(uint32_t st, uint32_t base) {
         st += G::kStage;
-        return st == base + G::kStages * G::kStage ? base : st;
+        return st == base + STAGES * G::kStage ? base : st;
     }
     // The 32 tokens' rows of the cache (row: this lane's token's; negative: zeros): chunk lane % DB of every (32 / DB)-th
     // token, and the scales of token `lane`.
@@ -524,7 +532,7 @@ struct Ring {
         in = after(in, base);
     }
     __device__ __forceinline__ void wait() {  // for the oldest stage
-        cp_async_wait<G::kStages - 2>();
+        cp_async_wait<STAGES - 2>();
         __syncwarp();
     }
     __device__ __forceinline__ void used() { out = after(out, base); }
@@ -545,17 +553,18 @@ __device__ __forceinline__ int row_of(const Params& p, const int* table, int h, 
 // ------------------------------------------------------------------------------------------------
 
 template <int DB, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kItemWarps * 32, Geo<DB>::kItemCtas) kv4_attention_items_kernel(const Params p) {
+__global__ void __launch_bounds__(kItemWarps * 32, Plan<DB, NT, SPLIT>::kItemCtas) kv4_attention_items_kernel(const Params p) {
     using G = Geo<DB>;
+    using L = Plan<DB, NT, SPLIT>;
     constexpr int D = G::D, ROWS = 8 * NT;
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ float join_ref[kItemWarps][ROWS], join_l[kItemWarps][ROWS];
     const KvAttnArgs& a = p.a;
     const int warp = threadIdx.x >> 5;
     Rows<DB, NT, SPLIT> w;
-    Ring<DB> ring;
+    Ring<DB, L::kStages> ring;
     w.init();
-    ring.init(smem_addr(ring_memory) + (uint32_t)(warp * G::kStages * G::kStage), a.c);
+    ring.init(smem_addr(ring_memory) + (uint32_t)(warp * L::kStages * G::kStage), a.c);
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -574,23 +583,23 @@ __global__ void __launch_bounds__(kItemWarps * 32, Geo<DB>::kItemCtas) kv4_atten
         ahead += kItemWarps * kTile;
         return row;
     };
-    int rows[G::kStages];
+    int rows[L::kStages];
 #pragma unroll
-    for (int i = 0; i < G::kStages; ++i) rows[i] = lookup();
+    for (int i = 0; i < L::kStages; ++i) rows[i] = lookup();
 #pragma unroll
-    for (int i = 0; i < G::kStages - 1; ++i) {
+    for (int i = 0; i < L::kStages - 1; ++i) {
         if (i < mine) {
             bad = bad || rows[i] == kBadPage;
             ring.copy(a.c, rows[i]);
         }
         ring.filled();
     }
-    int next = rows[G::kStages - 1];
+    int next = rows[L::kStages - 1];
     w.start(p, b, h, row0, s);
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
         ring.wait();
-        if (i + G::kStages - 1 < mine) {
+        if (i + L::kStages - 1 < mine) {
             bad = bad || next == kBadPage;
             ring.copy(a.c, next);
         }
@@ -674,81 +683,89 @@ __device__ __forceinline__ void scan_cost(const KvAttnArgs& a, long long* prefix
     __syncthreads();
 }
 
-// The part of an item that lies in a warp's piece of the line: `count` tiles from tile0 on.
+// The part of an item that lies in a warp's piece of the line: `count` tiles from tile0 on. A warp keeps its parts in
+// shared memory (all lanes write the same values), because they are looked at only where an item begins or ends.
 struct Part {
-    int b, item;        // sequence, head * chunks + chunk
-    Span s;
     long long item_at;  // where the item begins on the line: its start's cost, then its tiles
+    int b, item;        // sequence, head * chunks + chunk
     int tile0, count;
-
-    __device__ __forceinline__ void cut(const KvAttnArgs& a, long long begin, long long end) {
-        s = span_of(a, a.seq_lens[b]);
-        tile0 = (int)max(begin - item_at - kItemCost, 0LL);
-        count = (int)min(end - item_at - kItemCost, (long long)s.tiles) - tile0;
-    }
-    // The first part of the piece [begin, end); count <= 0: none (the piece ends in an item's start).
-    __device__ __forceinline__ void first(const KvAttnArgs& a, const long long* prefix, int items, long long begin, long long end) {
-        b = 0;
-        for (int step = kMaxB / 2; step > 0; step >>= 1)
-            if (b + step < a.B && prefix[b + step] * items <= begin) b += step;
-        const int cost = (int)(prefix[b + 1] - prefix[b]);
-        const long long rem = begin - prefix[b] * items;
-        item = (int)(rem / cost);
-        item_at = begin - (rem - (long long)item * cost);
-        cut(a, begin, end);
-    }
-    __device__ __forceinline__ void next(const KvAttnArgs& a, int items, long long end) {
-        item_at += s.tiles + kItemCost;
-        count = 0;
-        if (item_at >= end) return;
-        if (++item == items) item = 0, ++b;
-        cut(a, item_at, end);
-    }
+    Span s;
 };
 
+__device__ __forceinline__ void cut(Part& part, const KvAttnArgs& a, int b, int item, long long item_at, long long begin, long long end) {
+    const Span s = span_of(a, a.seq_lens[b]);
+    part.b = b, part.item = item, part.item_at = item_at, part.s = s;
+    part.tile0 = (int)max(begin - item_at - kItemCost, 0LL);
+    part.count = (int)min(end - item_at - kItemCost, (long long)s.tiles) - part.tile0;
+}
+// The first part of the piece [begin, end); count <= 0: none (the piece ends in an item's start).
+__device__ __forceinline__ void first_part(Part& part, const KvAttnArgs& a, const long long* prefix, int items, long long begin, long long end) {
+    int b = 0;
+    for (int step = kMaxB / 2; step > 0; step >>= 1)
+        if (b + step < a.B && prefix[b + step] * items <= begin) b += step;
+    const int cost = (int)(prefix[b + 1] - prefix[b]);
+    const long long rem = begin - prefix[b] * items;
+    const int item = (int)(rem / cost);
+    cut(part, a, b, item, begin - (rem - (long long)item * cost), begin, end);
+}
+__device__ __forceinline__ void next_part(Part& part, const KvAttnArgs& a, int items, long long end) {
+    const long long at = part.item_at + part.s.tiles + kItemCost;
+    int b = part.b, item = part.item + 1;
+    if (item == items) item = 0, ++b;
+    __syncwarp();  // every lane has read the part
+    if (at >= end) part.count = 0;
+    else cut(part, a, b, item, at, at, end);
+    __syncwarp();
+}
+
 template <int DB, int NT, bool SPLIT>
-__global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams_kernel(const Params p) {
+__global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_attention_streams_kernel(const Params p) {
     using G = Geo<DB>;
+    using L = Plan<DB, NT, SPLIT>;
     constexpr int D = G::D, ROWS = 8 * NT;
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ long long prefix[kMaxB + 1];
+    __shared__ Part parts[L::kWarps][2];
+    __shared__ long long ends[L::kWarps];
     const KvAttnArgs& a = p.a;
     const int warp = threadIdx.x >> 5;
     // warps of one SM take pieces that are far apart: an SM that gets a stretch of short items gets others too
     const int stream = warp * (int)gridDim.x + (int)blockIdx.x;
     Rows<DB, NT, SPLIT> w;
-    Ring<DB> ring;
+    Ring<DB, L::kStages> ring;
     w.init();
-    ring.init(smem_addr(ring_memory) + (uint32_t)(warp * G::kStages * G::kStage), a.c);
+    ring.init(smem_addr(ring_memory) + (uint32_t)(warp * L::kStages * G::kStage), a.c);
     grid_dependency_wait();
     grid_launch_dependents();
-    scan_cost<G::kWarps * 32>(a, prefix);
+    scan_cost<L::kWarps * 32>(a, prefix);
 
     const int items = a.c.num_kv_heads * p.chunks;
     const long long total = prefix[a.B] * items;
     // an even share of the cost, no less than an item of one tile
     const long long share = max((total + p.warps - 1) / (long long)p.warps, (long long)(1 + kItemCost));
-    const long long begin = min(total, share * stream), end = min(total, begin + share);
-    if (w.lane == 0) p.desc[stream] = make_int4(-1, 0, 0, 0);
-    if (begin >= end) return;
-
-    Part use, fill;  // of the tile to use next, and of the tile to look up next
-    use.first(a, prefix, items, begin, end);
-    if (use.count <= 0) return;
-    fill = use;
-    int left = fill.count, ahead = fill.s.first + fill.tile0 * kTile + w.lane;
+    Part &use = parts[warp][0], &fill = parts[warp][1];  // of the tile to use next, and of the tile to look up next
+    {
+        const long long begin = min(total, share * stream), end = min(total, begin + share);
+        if (begin >= end) return;
+        first_part(use, a, prefix, items, begin, end);
+        fill = use;
+        ends[warp] = end;
+        __syncwarp();
+        if (use.count <= 0) return;
+    }
+    int left = fill.count, ahead = fill.s.first + fill.tile0 * kTile + w.lane, ahead_lo = fill.s.lo, ahead_end = fill.s.n;
     const int* table = a.block_table + (long long)fill.b * a.max_pages;
     int fill_h = fill.item / p.chunks;
     auto lookup = [&](bool& some) {  // the row of this lane's token of the next tile of the piece; some: there is a tile
         some = left > 0;
         if (!some) return (int)kSkip;
-        const int row = row_of(p, table, fill_h, ahead, fill.s.lo, fill.s.n);
+        const int row = row_of(p, table, fill_h, ahead, ahead_lo, ahead_end);
         ahead += kTile;
         if (--left == 0) {
-            fill.next(a, items, end);
+            next_part(fill, a, items, ends[warp]);
             left = max(fill.count, 0);
             if (left > 0) {
-                ahead = fill.s.first + fill.tile0 * kTile + w.lane;
+                ahead = fill.s.first + fill.tile0 * kTile + w.lane, ahead_lo = fill.s.lo, ahead_end = fill.s.n;
                 table = a.block_table + (long long)fill.b * a.max_pages;
                 fill_h = fill.item / p.chunks;
             }
@@ -761,32 +778,34 @@ __global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams
         bad_stages = bad_stages << 1 | (some && row == kBadPage ? 1u : 0u);
         ring.filled();
     };
-    int rows[G::kStages];
-    bool some[G::kStages];
+    int rows[L::kStages];
+    bool some[L::kStages];
 #pragma unroll
-    for (int i = 0; i < G::kStages; ++i) rows[i] = lookup(some[i]);
+    for (int i = 0; i < L::kStages; ++i) rows[i] = lookup(some[i]);
 #pragma unroll
-    for (int i = 0; i < G::kStages - 1; ++i) copy(some[i], rows[i]);
-    int next_row = rows[G::kStages - 1];
-    bool next_some = some[G::kStages - 1];
+    for (int i = 0; i < L::kStages - 1; ++i) copy(some[i], rows[i]);
+    int next_row = rows[L::kStages - 1];
+    bool next_some = some[L::kStages - 1];
 
-    int slot = use.item_at + kItemCost < begin ? 0 : 1;  // a part of an item that began before goes to slot 0
 #pragma unroll 1
     for (;;) {
-        const int h = use.item / p.chunks, row0 = (use.item - h * p.chunks) * ROWS;
         bool bad = use.s.bad;
-        w.start(p, use.b, h, row0, use.s);
+        {
+            const int h = use.item / p.chunks;
+            w.start(p, use.b, h, (use.item - h * p.chunks) * ROWS, use.s);
+        }
         int tok0 = use.s.first + use.tile0 * kTile;
+        const int last = tok0 + use.count * kTile;
 #pragma unroll 1
-        for (int i = 0; i < use.count; ++i) {
+        for (; tok0 != last; tok0 += kTile) {
             ring.wait();
-            bad = bad || (bad_stages >> (G::kStages - 2) & 1u);
+            bad = bad || (bad_stages >> (L::kStages - 2) & 1u);
             copy(next_some, next_row);
             next_row = lookup(next_some);
             w.take(ring.out, tok0);
             ring.used();
-            tok0 += kTile;
         }
+        const int b = use.b, h = use.item / p.chunks, row0 = (use.item - h * p.chunks) * ROWS;
         bad = __any_sync(0xffffffffu, bad) != 0;
         w.finish(bad);
         if (bad && w.lane == 0) atomicOr(a.fault, use.s.bad ? (unsigned)kFaultBadLength : (unsigned)kFaultBadPage);
@@ -795,7 +814,7 @@ __global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams
             for (int n = 0; n < NT; ++n) {
                 const float inv = w.l[n] == 0.f ? 0.f : 1.f / w.l[n];
                 const int r = row0 + 8 * n + w.g;
-                if (a.lse && w.t4 == 0 && r < p.R) a.lse[lse_at(p, use.b, h, r)] = lse_of(w.ref[n], w.l[n]);
+                if (a.lse && w.t4 == 0 && r < p.R) a.lse[lse_at(p, b, h, r)] = lse_of(w.ref[n], w.l[n]);
                 w.l[n] = inv;
             }
             long long to[NT][2];
@@ -806,7 +825,7 @@ __global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams
                 for (int i = 0; i < 2; ++i) {
                     const int r = row0 + 8 * n + 2 * w.t4 + i;
                     inv[n][i] = __shfl_sync(0xffffffffu, w.l[n], 8 * w.t4 + 4 * i);
-                    to[n][i] = r < p.R ? out_at(p, use.b, h, r, D) : -1;
+                    to[n][i] = r < p.R ? out_at(p, b, h, r, D) : -1;
                 }
             w.each_pair([&](int n, int i, int e, float2 v) {
                 if (to[n][i] < 0) return;
@@ -816,7 +835,10 @@ __global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams
                 else if (a.dtype == Q4_F16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack2(v.x, v.y, __half());
                 else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack2(v.x, v.y, __nv_bfloat16());
             });
+            if (w.lane == 0) p.desc[b * items + use.item] = make_int2(1, 0);
         } else {
+            // a part of an item that began before goes to slot 0
+            const int slot = use.item_at + kItemCost < share * stream ? 0 : 1;
             float* part = p.part + ((long long)stream * 2 + slot) * (ROWS * (D + 2));
             if (w.t4 == 0) {
 #pragma unroll
@@ -828,17 +850,15 @@ __global__ void __launch_bounds__(Geo<DB>::kWarps * 32, 1) kv4_attention_streams
                 if (row0 + r < p.R) *reinterpret_cast<float2*>(part + r * D + e) = v;
             });
             if (use.tile0 == 0 && w.lane == 0)  // the item begins here: its join starts from this warp
-                p.desc[stream] = make_int4(use.b, use.item, (int)((use.item_at + use.s.tiles + kItemCost - 1) / share), slot);
+                p.desc[b * items + use.item] = make_int2((int)((use.item_at + use.s.tiles + kItemCost - 1) / share) - stream + 1, stream * 2 + slot);
         }
-        slot = 1;
-        use.next(a, items, end);
+        next_part(use, a, items, ends[warp]);
         if (use.count <= 0) break;
     }
     cp_async_wait<0>();
 }
 
-// Joins the parts of an item that was divided: block x the item that begins in piece x (streams) or item x, ROWS / gridDim.y
-// of its rows. A block's threads stand over rows, parts and groups of four elements; every sum has a fixed order.
+// Joins the parts of an item that was divided: block x item x of the call, ROWS / gridDim.y of its rows. A block's threads stand over rows, parts and groups of four elements; every sum has a fixed order.
 constexpr int kJoinThreads = 256;
 template <int DB, int NT, int RPB>  // RPB: rows a block
 __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const Params p) {
@@ -849,24 +869,18 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const 
     __shared__ float sl[PT][RT], sm[PT][RT];
     grid_dependency_wait();
     grid_launch_dependents();
-    int b, item, n;
-    const float* part0;  // the first part; the others follow, two slots apart in streams
-    const int stride = ROWS * (D + 2);
-    long long step;
-    if (p.warps) {
-        const int4 ds = p.desc[blockIdx.x];
-        if (ds.x < 0) return;
-        b = ds.x, item = ds.y, n = ds.z - (int)blockIdx.x + 1;
-        part0 = p.part + ((long long)blockIdx.x * 2 + ds.w) * stride;
-        step = 2 * stride - ds.w * stride;  // to slot 0 of the next piece
-    } else {
-        const int items = p.a.c.num_kv_heads * p.chunks;
-        b = blockIdx.x / items, item = blockIdx.x - b * items, n = p.splits;
-        part0 = p.part + (long long)blockIdx.x * n * stride;
-        step = stride;
-    }
+    const int items = p.a.c.num_kv_heads * p.chunks, stride = ROWS * (D + 2);
+    const int b = blockIdx.x / items, item = blockIdx.x - b * items;
     const int h = item / p.chunks, row0 = (item - h * p.chunks) * ROWS;
-    auto part = [&](int i) { return i == 0 ? part0 : part0 + step + (long long)(i - 1) * (p.warps ? 2 * stride : stride); };
+    int n = p.splits, slot = 0;
+    const float* part0 = p.part + (long long)blockIdx.x * n * stride;  // split items: their parts follow each other
+    if (p.warps) {  // streams: a slot of the first piece, then slot 0 of the next pieces
+        const int2 ds = p.desc[blockIdx.x];
+        n = ds.x, slot = ds.y & 1;
+        if (n <= 1) return;
+        part0 = p.part + (long long)ds.y * stride;
+    }
+    auto part = [&](int i) { return part0 + (long long)(p.warps ? (i == 0 ? 0 : 2 * i - slot) : i) * stride; };
     const int d4 = threadIdx.x % D4, rt = threadIdx.x / D4 % RT, pt = threadIdx.x / (D4 * RT);
     for (int r0 = blockIdx.y * RPB; r0 < (int)(blockIdx.y + 1) * RPB; r0 += RT) {
         const int r = r0 + rt;
@@ -952,12 +966,13 @@ cudaError_t launch_with_ring(Kernel kernel, dim3 grid, int threads, uint32_t rin
 
 }  // namespace
 
-size_t kv4_attention_workspace_bytes(int M, int group, int D, int dtype, int sm_count) {
+size_t kv4_attention_workspace_bytes(int M, int group, int heads, int D, int dtype, int sm_count) {
     const int nt = row_groups(M, group, D);
-    return with_plan(D, nt, dtype == Q4_F32, [&](auto db, auto n, auto) {
+    return with_plan(D, nt, dtype == Q4_F32, [&](auto db, auto n, auto split) {
         constexpr int DB = decltype(db)::value, NT = decltype(n)::value;
-        const size_t warps = (size_t)sm_count * Geo<DB>::kWarps;
-        return warps * (sizeof(int4) + 2 * 8 * NT * (DB * 32 + 2) * sizeof(float));
+        const size_t warps = (size_t)sm_count * Plan<DB, NT, decltype(split)::value>::kWarps;
+        const size_t items = (size_t)heads * ((M * group + 8 * NT - 1) / (8 * NT));
+        return warps * 2 * 8 * NT * (DB * 32 + 2) * sizeof(float) + kMaxB * items * sizeof(int2);
     });
 }
 
@@ -967,11 +982,12 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
         constexpr int DB = decltype(db)::value, NT = decltype(n)::value;
         constexpr bool SPLIT = decltype(split)::value;
         using G = Geo<DB>;
+        using L = Plan<DB, NT, SPLIT>;
         Params p;
         p.a = a;
-        p.warps = sm_count * G::kWarps;
-        p.desc = static_cast<int4*>(workspace);
-        p.part = reinterpret_cast<float*>(p.desc + p.warps);
+        p.warps = sm_count * L::kWarps;
+        p.part = static_cast<float*>(workspace);
+        p.desc = reinterpret_cast<int2*>(p.part + (size_t)p.warps * 2 * 8 * NT * (DB * 32 + 2));
         p.R = group * a.M;
         p.group = group;
         p.chunks = (p.R + 8 * NT - 1) / (8 * NT);
@@ -986,19 +1002,19 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
         };
         const long long most = (long long)a.max_pages * a.c.page_size;
         if (most <= kItemTokens || a.B == 1) {
-            constexpr int kRing = kItemWarps * G::kStages * G::kStage;
+            constexpr int kRing = kItemWarps * L::kStages * G::kStage;
             static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
             p.warps = 0;
             if (most > kItemTokens)
-                p.splits = (int)std::max(1LL, std::min<long long>(sm_count * G::kItemCtas / items, most / (kTile * kItemWarps)));
+                p.splits = (int)std::max(1LL, std::min<long long>(sm_count * L::kItemCtas / items, most / (kTile * kItemWarps)));
             cudaError_t e = launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT>, dim3((unsigned)(items * p.splits), (unsigned)a.B),
                                              kItemWarps * 32, kRing, s, p);
             if (e == cudaSuccess && p.splits > 1) e = join((unsigned)items, true);
             return e;
         }
-        cudaError_t e = launch_with_ring(kv4_attention_streams_kernel<DB, NT, SPLIT>, dim3((unsigned)sm_count), G::kWarps * 32,
-                                         G::kWarps * G::kStages * G::kStage, s, p);
-        if (e == cudaSuccess) e = join((unsigned)p.warps, items * a.B <= 64);
+        cudaError_t e = launch_with_ring(kv4_attention_streams_kernel<DB, NT, SPLIT>, dim3((unsigned)sm_count), L::kWarps * 32,
+                                         L::kWarps * L::kStages * G::kStage, s, p);
+        if (e == cudaSuccess) e = join((unsigned)(items * a.B), items * a.B <= 64);
         return e;
     });
 }
