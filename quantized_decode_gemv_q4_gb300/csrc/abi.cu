@@ -396,6 +396,12 @@ static int check_cache(const char* what, const kv4_cache* c) {
     return Q4_OK;
 }
 
+static int log2_of(int n) {  // of a power of two
+    int l = 0;
+    while ((1 << l) < n) ++l;
+    return l;
+}
+
 static int check_index(const char* what, const char* name, const int32_t* p) {
     if (!p) return fail(Q4_EINVAL, "%s: null %s", what, name);
     if (!aligned(p, 4)) return fail(Q4_EALIGN, "%s: %s must be 4-byte aligned", what, name);
@@ -419,6 +425,7 @@ int qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, const f
     Q4_TRY(check_dtype(what, dtype));
     Q4_TRY(check_heads(what, Hkv, D));
     if (Hq <= 0 || Hq > 65535 || Hkv > 65535) return fail(Q4_EINVAL, "%s: 1 to 65535 heads are taken", what);
+    if ((long long)T * (Hq + Hkv) > 0x7fffffffLL) return fail(Q4_EINVAL, "%s: T * heads exceeds 2^31-1", what);
     Q4_TRY(check_rows(what, "q", q, q_stride, (long long)Hq * D, dtype));
     Q4_TRY(check_rows(what, "k", k, k_stride, (long long)Hkv * D, dtype));
     Q4_TRY(check_rows(what, "q_out", q_out, q_out_stride, (long long)Hq * D, dtype));
@@ -435,8 +442,9 @@ int qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, const f
     }
     DeviceInfo di;
     RopeArgs a = {q_out, k_out, q, k, q_gamma, k_gamma, cos_sin, positions, eps, T, Hq, Hkv, D, rot_dim, max_pos,
-                  interleaved != 0, q_stride, k_stride, q_out_stride, k_out_stride, nullptr};
+                  interleaved != 0, q_stride, k_stride, q_out_stride, k_out_stride, nullptr, 0};
     Q4_TRY(check_device_faults(what, &di, &a.fault));
+    a.sm_count = di.sm_count;
     return finish(what, launch_qk_norm_rope(a, dtype, (cudaStream_t)stream));
 }
 
@@ -451,7 +459,7 @@ int kv4_write(const kv4_cache* cache, const void* k, const void* v, const int32_
     Q4_TRY(check_rows(what, "v", v, v_stride, width, dtype));
     Q4_TRY(check_index(what, "slots", slots));
     DeviceInfo di;
-    KvRowsArgs a = {*cache, const_cast<void*>(k), const_cast<void*>(v), slots, T, k_stride, v_stride, nullptr};
+    KvRowsArgs a = {*cache, const_cast<void*>(k), const_cast<void*>(v), slots, T, k_stride, v_stride, nullptr, log2_of(cache->page_size)};
     Q4_TRY(check_device_faults(what, &di, &a.fault));
     return finish(what, launch_kv4_write(a, dtype, (cudaStream_t)stream));
 }
@@ -468,7 +476,7 @@ int kv4_read(void* k_out, void* v_out, const kv4_cache* cache, const int32_t* sl
     if (v_out) Q4_TRY(check_rows(what, "v_out", v_out, v_stride, width, dtype));
     Q4_TRY(check_index(what, "slots", slots));
     DeviceInfo di;
-    KvRowsArgs a = {*cache, k_out, v_out, slots, T, k_stride, v_stride, nullptr};
+    KvRowsArgs a = {*cache, k_out, v_out, slots, T, k_stride, v_stride, nullptr, log2_of(cache->page_size)};
     Q4_TRY(check_device_faults(what, &di, &a.fault));
     return finish(what, launch_kv4_read(a, dtype, (cudaStream_t)stream));
 }

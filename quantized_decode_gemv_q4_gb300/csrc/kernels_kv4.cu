@@ -12,6 +12,30 @@ namespace q4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
+constexpr int kTokens = 4;                       // tokens of a thread where there are many pieces
+constexpr long long kManyPieces = 1LL << 20;     // three for each resident thread of the device
+
+// A thread holds 16 elements of a 32-element block, those of 8 code bytes: elements 8 s .. 8 s + 7 (low nibbles) and
+// 16 + 8 s .. (high nibbles) of side s = 0, 1; so a block's two threads write whole 32-byte sectors of values, and their
+// only exchange is the block's maximum. A token's Hkv * D / 8 pieces run over its K heads, then its V heads. A thread
+// takes the same piece of U tokens, all of whose loads are in flight at once.
+struct Piece {
+    bool v;
+    int el;          // first low element in the token's row
+    int head, blk, side;
+};
+__device__ __forceinline__ Piece piece_of(const kv4_cache& c, int u) {
+    Piece q;
+    const int half = c.num_kv_heads * c.head_dim / 16;  // pieces of K, and of V
+    q.v = u >= half;
+    const int in = q.v ? u - half : u, per_head = c.head_dim / 16;
+    q.head = in / per_head;
+    const int in_row = in - q.head * per_head;
+    q.blk = in_row >> 1, q.side = in_row & 1;
+    q.el = q.head * c.head_dim + 32 * q.blk + 8 * q.side;
+    return q;
+}
 
 // nearest(x / d) for d an f16 value > 0, ties to even, exactly: r = rint(x * (1 / d)) is the nearest or next to it,
 // and x - r d is exact in fp32 (r d has 15 bits, and the difference is below 2^24 units of the smaller operand's
@@ -25,123 +49,184 @@ __device__ __forceinline__ float nearest_quotient(float x, float d, float inv) {
     return fminf(fmaxf(r, -7.f), 7.f);
 }
 
-// One thread holds 8 elements, four threads a block; the threads of a token run over its K heads, then its V heads.
+// The eight code bytes (8 + r_lo) + 16 (8 + r_hi) of a thread's elements with nearest_quotient, one after the other from
+// memory: rarely needed, so kept small.
 template <typename T>
-__global__ void kv4_write_kernel(const KvRowsArgs p) {
+__device__ __noinline__ uint2 exact_bytes(const T* src, float d) {
+    unsigned long long w = 0ull;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        const float a = nearest_quotient((float)src[j], d, 1.f / d), b = nearest_quotient((float)src[16 + j], d, 1.f / d);
+        w |= (unsigned long long)(136 + __float2int_rn(a) + 16 * __float2int_rn(b)) << (8 * j);
+    }
+    return make_uint2((uint32_t)w, (uint32_t)(w >> 32));
+}
+
+// The same from low elements lo and high elements hi in registers. Adding 1.5 * 2^23 leaves the rounded quotient as a float
+// (and, the second time, the byte in the low bits): four operations an element instead of fifteen. exact_bytes is left to
+// a thread that met a quotient within 2^-18 of a border (the approximate reciprocal moves none further) or a scale that
+// leaves quotients past 7.5 (below f16's normal range, or capped).
+template <typename T>
+__device__ __forceinline__ uint2 code_bytes(const float (&lo)[8], const float (&hi)[8], float top, float d, const T* src) {
+    constexpr float kMagic = 12582912.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+    float off = 0.f;
+    uint32_t byte[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = fmaf(lo[j], inv, kMagic) - kMagic, b = fmaf(hi[j], inv, kMagic) - kMagic;
+        off = fmaxf(off, fmaxf(fabsf(fmaf(-a, d, lo[j])), fabsf(fmaf(-b, d, hi[j]))));
+        byte[j] = __float_as_uint(fmaf(b, 16.f, a) + (kMagic + 136.f));
+    }
+    if (off >= 0.5f * d * (1.f - 0x1p-18f) || d < 0x1p-14f || top > 7.f * 65504.f) return exact_bytes(src, d);
+    uint2 w;
+    w.x = __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
+    w.y = __byte_perm(__byte_perm(byte[4], byte[5], 0x0040), __byte_perm(byte[6], byte[7], 0x0040), 0x5410);
+    return w;
+}
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+template <typename T, int U>
+__global__ void __launch_bounds__(kMaxThreads) kv4_write_kernel(const KvRowsArgs p) {
+    const int pieces = p.c.num_kv_heads * p.c.head_dim / 8;
+    const int t0 = ((int)blockIdx.x * (int)blockDim.y + (int)threadIdx.y) * U, slots = p.c.num_pages * p.c.page_size;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int t = (int)blockIdx.x * blockDim.y + threadIdx.y;
-    const int per = p.c.num_kv_heads * p.c.head_dim / 8;  // threads' worth of work in K, and in V
-    int slot = -1;
-    if (t < p.T) slot = p.slots[t];
-    if (slot >= p.c.num_pages * p.c.page_size) {
-        if (threadIdx.x == 0) atomicOr(p.fault, (unsigned)kFaultBadSlot);
-        slot = -1;
+    int slot[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) slot[i] = t0 + i < p.T ? p.slots[t0 + i] : -1;
+    for (int u0 = 0; u0 < pieces; u0 += (int)blockDim.x) {  // every thread of a warp takes part in the shuffles
+        const int u = u0 + (int)threadIdx.x;
+        const bool active = u < pieces;
+        const Piece q = piece_of(p.c, active ? u : 0);
+        const T* src = static_cast<const T*>(q.v ? p.v : p.k) + q.el;
+        const long long stride = q.v ? p.v_stride : p.k_stride;
+        float lo[U][8], hi[U][8];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) lo[i][j] = hi[i][j] = 0.f;
+            if (active && t0 + i < p.T) {
+                load_floats(src + (t0 + i) * stride, lo[i]);
+                load_floats(src + (t0 + i) * stride + 16, hi[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max_or_nan(top, max_or_nan(fabsf(lo[i][j]), fabsf(hi[i][j])));
+            top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const bool finite = top < INFINITY;
+            const __half dh = __float2half_rn(fminf(__fdiv_rn(top, 7.f), 65504.f));
+            const float d = __half2float(dh);
+            const uint2 w = finite && d > 0.f ? code_bytes(lo[i], hi[i], top, d, src + (t0 + i) * stride)
+                                              : make_uint2(0x88888888u, 0x88888888u);
+            if (active && slot[i] >= 0 && slot[i] < slots) {
+                const int page = slot[i] >> p.lp, off = slot[i] & (p.c.page_size - 1);
+                const long long row = cache_row(p.c, page, q.head, off);
+                *reinterpret_cast<uint2*>((q.v ? p.c.v_qs : p.c.k_qs) + row * (p.c.head_dim / 2) + q.blk * 16 + q.side * 8) = w;
+                if (q.side == 0)
+                    (q.v ? p.c.v_d : p.c.k_d)[row * (p.c.head_dim / 32) + q.blk] = finite ? __half_as_ushort(dh) : (unsigned short)0x7E00u;
+            }
+        }
     }
-    const int page = slot / p.c.page_size, off = slot - page * p.c.page_size;
-    const int rounds = (2 * per + (int)blockDim.x - 1) / (int)blockDim.x;
-    for (int i = 0; i < rounds; ++i) {  // every thread of a warp takes part in the shuffles
-        const int u = i * (int)blockDim.x + threadIdx.x;
-        const bool active = slot >= 0 && u < 2 * per;
-        const bool is_v = u >= per;
-        const int el = (is_v ? u - per : u) * 8;
-        float x[8] = {};
-        if (active) {
-            const T* src = is_v ? static_cast<const T*>(p.v) + t * p.v_stride : static_cast<const T*>(p.k) + t * p.k_stride;
-            load_floats(src + el, x);
-        }
-        uint32_t top = 0u;  // the largest magnitude's bits: NaN and infinity rank above every finite value
+    if (threadIdx.x == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const __half dh = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top), 7.f), 65504.f));
-        const float d = __half2float(dh);
-        const bool finite = top < 0x7F800000u;
-        const bool codes = finite && d > 0.f;
-        const float inv = 1.f / d;
-        uint32_t w[2] = {0x08080808u, 0x08080808u};
-        if (codes) {
-            w[0] = w[1] = 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                w[j / 4] |= (uint32_t)(8 + __float2int_rn(nearest_quotient(x[j], d, inv))) << (8 * (j % 4));
-        }
-        // thread q of a block holds elements 8q .. 8q + 7: bytes 8 (q % 2) .. + 7, low nibbles from q < 2
-        const int q = threadIdx.x & 3;
-        const uint32_t o0 = __shfl_xor_sync(0xffffffffu, w[0], 2), o1 = __shfl_xor_sync(0xffffffffu, w[1], 2);
-        const uint32_t word = q < 2 ? (w[0] | (o0 << 4)) : (o1 | (w[1] << 4));
-        if (active) {
-            const int h = el / p.c.head_dim, in_row = el - h * p.c.head_dim;
-            const long long row = cache_row(p.c, page, h, off);
-            uint8_t* qs = (is_v ? p.c.v_qs : p.c.k_qs) + row * (p.c.head_dim / 2);
-            uint16_t* ds = (is_v ? p.c.v_d : p.c.k_d) + row * (p.c.head_dim / 32);
-            *reinterpret_cast<uint32_t*>(qs + (in_row / 32) * 16 + (q & 1) * 8 + (q >> 1) * 4) = word;
-            if (q == 0) ds[in_row / 32] = finite ? __half_as_ushort(dh) : (unsigned short)0x7E00u;
-        }
+        for (int i = 0; i < U; ++i)
+            if (slot[i] >= slots) atomicOr(p.fault, (unsigned)kFaultBadSlot);
     }
 }
 
-template <typename T>
-__global__ void kv4_read_kernel(const KvRowsArgs p) {
+template <typename T, int U>
+__global__ void __launch_bounds__(kMaxThreads) kv4_read_kernel(const KvRowsArgs p) {
+    const int pieces = p.c.num_kv_heads * p.c.head_dim / 8;
+    const int t0 = ((int)blockIdx.x * (int)blockDim.y + (int)threadIdx.y) * U, slots = p.c.num_pages * p.c.page_size;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int t = (int)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.T) return;
-    const int per = p.c.num_kv_heads * p.c.head_dim / 8;
-    const int slot = p.slots[t];
-    if (slot < 0) return;
-    const bool bad = slot >= p.c.num_pages * p.c.page_size;
-    if (bad && threadIdx.x == 0) atomicOr(p.fault, (unsigned)kFaultBadSlot);
-    const int page = bad ? 0 : slot / p.c.page_size, off = bad ? 0 : slot - page * p.c.page_size;
-    for (int u = threadIdx.x; u < 2 * per; u += blockDim.x) {
-        const bool is_v = u >= per;
-        const int el = (is_v ? u - per : u) * 8;
-        T* dst = static_cast<T*>(is_v ? p.v : p.k);
+    int slot[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) slot[i] = t0 + i < p.T ? p.slots[t0 + i] : -1;
+    for (int u = (int)threadIdx.x; u < pieces; u += (int)blockDim.x) {
+        const Piece q = piece_of(p.c, u);
+        T* dst = static_cast<T*>(q.v ? p.v : p.k);
         if (!dst) continue;
-        dst += t * (is_v ? p.v_stride : p.k_stride) + el;
-        const int h = el / p.c.head_dim, in_row = el - h * p.c.head_dim;
-        const long long row = cache_row(p.c, page, h, off);
-        const int q = (in_row / 8) & 3;
-        const uint2 w = *reinterpret_cast<const uint2*>((is_v ? p.c.v_qs : p.c.k_qs) + row * (p.c.head_dim / 2) +
-                                                        (in_row / 32) * 16 + (q & 1) * 8);
-        float d = f16_bits_to_f32((is_v ? p.c.v_d : p.c.k_d)[row * (p.c.head_dim / 32) + in_row / 32]);
-        if (bad) d = qnan();
-        float x[8];
+        dst += q.el;
+        const long long stride = q.v ? p.v_stride : p.k_stride;
+        uint2 w[U];
+        float d[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t code = ((j < 4 ? w.x : w.y) >> (8 * (j % 4) + 4 * (q >> 1))) & 15u;
-            x[j] = (float)((int)code - 8) * d;
+        for (int i = 0; i < U; ++i) {
+            const bool there = slot[i] >= 0 && slot[i] < slots;
+            const int at = there ? slot[i] : 0, page = at >> p.lp, off = at & (p.c.page_size - 1);
+            const long long row = cache_row(p.c, page, q.head, off);
+            w[i] = *reinterpret_cast<const uint2*>((q.v ? p.c.v_qs : p.c.k_qs) + row * (p.c.head_dim / 2) + q.blk * 16 + q.side * 8);
+            d[i] = f16_bits_to_f32((q.v ? p.c.v_d : p.c.k_d)[row * (p.c.head_dim / 32) + q.blk]);
+            if (!there) d[i] = qnan();
         }
-        store_floats(dst, x);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (slot[i] < 0) continue;
+            float lo[8], hi[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c = ((j < 4 ? w[i].x : w[i].y) >> (8 * (j % 4))) & 255u;
+                lo[j] = (float)((int)(c & 15u) - 8) * d[i];
+                hi[j] = (float)((int)(c >> 4) - 8) * d[i];
+            }
+            store_floats(dst + (t0 + i) * stride, lo);
+            store_floats(dst + (t0 + i) * stride + 16, hi);
+        }
+    }
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (slot[i] >= slots) atomicOr(p.fault, (unsigned)kFaultBadSlot);
     }
 }
 
-// A block's threads: x over a token's 2 * Hkv * D / 8 eight-element pieces (a multiple of 8), y over tokens so that
-// short tokens share a block; a whole number of warps.
-dim3 rows_block(const KvRowsArgs& a) {
-    const int pieces = 2 * a.c.num_kv_heads * a.c.head_dim / 8;
+// A block's threads: x over a token's pieces (a multiple of 4), y over groups of U tokens so that short tokens share a
+// block; a whole number of warps, at most kMaxThreads.
+dim3 rows_block(int pieces) {
     if (pieces >= kThreads) return dim3(kThreads);
+    if (pieces >= 64) {
+        const int x = (pieces + 31) / 32 * 32;
+        return dim3((unsigned)x, (unsigned)(kThreads / x));
+    }
     int y = kThreads / pieces;
-    if (pieces % 32) y = (y + 3) / 4 * 4;
+    if (pieces % 32) y = (y + 7) / 8 * 8;
     return dim3((unsigned)pieces, (unsigned)y);
+}
+
+template <int N, typename F1, typename F4>
+cudaError_t launch_rows(const KvRowsArgs& a, cudaStream_t s, F1 one, F4 four) {
+    const int pieces = a.c.num_kv_heads * a.c.head_dim / 8;
+    const dim3 block = rows_block(pieces);
+    const bool many = (long long)a.T * pieces >= kManyPieces;
+    const int tokens = (int)block.y * (many ? N : 1);
+    const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
+    return many ? launch_grid(four, grid, block, 0, s, launch_overlap(), a) : launch_grid(one, grid, block, 0, s, launch_overlap(), a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_write(const KvRowsArgs& a, int dtype, cudaStream_t s) {
-    const dim3 block = rows_block(a);
-    const dim3 grid((unsigned)((a.T + (int)block.y - 1) / (int)block.y));
     return with_dtype(dtype, [&](auto tag) {
-        return launch_grid(kv4_write_kernel<decltype(tag)>, grid, block, 0, s, launch_overlap(), a);
+        using T = decltype(tag);
+        return launch_rows<kTokens>(a, s, kv4_write_kernel<T, 1>, kv4_write_kernel<T, kTokens>);
     });
 }
 
 cudaError_t launch_kv4_read(const KvRowsArgs& a, int dtype, cudaStream_t s) {
-    const dim3 block = rows_block(a);
-    const dim3 grid((unsigned)((a.T + (int)block.y - 1) / (int)block.y));
     return with_dtype(dtype, [&](auto tag) {
-        return launch_grid(kv4_read_kernel<decltype(tag)>, grid, block, 0, s, launch_overlap(), a);
+        using T = decltype(tag);
+        return launch_rows<kTokens>(a, s, kv4_read_kernel<T, 1>, kv4_read_kernel<T, kTokens>);
     });
 }
 

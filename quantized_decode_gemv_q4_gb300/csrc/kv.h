@@ -33,6 +33,7 @@ struct RopeArgs {
     int T, Hq, Hkv, D, rot, max_pos, interleaved;
     long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements from one token to the next
     unsigned* fault;
+    int sm_count;
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int dtype, cudaStream_t s);
 
@@ -43,6 +44,7 @@ struct KvRowsArgs {
     int T;
     long long k_stride, v_stride;
     unsigned* fault;
+    int lp;  // log2(page size)
 };
 cudaError_t launch_kv4_write(const KvRowsArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_kv4_read(const KvRowsArgs& a, int dtype, cudaStream_t s);
