@@ -13,8 +13,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxThreads = 512;
-constexpr int kTokens = 4;                       // tokens of a thread where there are many pieces
-constexpr long long kManyPieces = 1LL << 20;     // three for each resident thread of the device
+// Tokens of a thread where there are many pieces (three for each resident thread of the device, so that fewer threads with
+// more in flight still fill it): 16384 bf16 tokens of 8 heads of 128, write and read back, take 48 us with one token a
+// thread, 37 us with four; the read of 50001 tokens 58 and 46 us (of its 39 us for the bytes).
+template <typename T>
+constexpr int kTokens = 8 / (int)sizeof(T);
+constexpr long long kManyPieces = 1LL << 20;
 
 // A thread holds 16 elements of a 32-element block, those of 8 code bytes: elements 8 s .. 8 s + 7 (low nibbles) and
 // 16 + 8 s .. (high nibbles) of side s = 0, 1; so a block's two threads write whole 32-byte sectors of values, and their
@@ -62,10 +66,14 @@ __device__ __noinline__ uint2 exact_bytes(const T* src, float d) {
     return make_uint2((uint32_t)w, (uint32_t)(w >> 32));
 }
 
-// The same from low elements lo and high elements hi in registers. Adding 1.5 * 2^23 leaves the rounded quotient as a float
-// (and, the second time, the byte in the low bits): four operations an element instead of fifteen. exact_bytes is left to
-// a thread that met a quotient within 2^-18 of a border (the approximate reciprocal moves none further) or a scale that
-// leaves quotients past 7.5 (below f16's normal range, or capped).
+// The same from low elements lo and high elements hi in registers. Adding 1.5 * 2^23 leaves a rounded quotient as a float
+// (and, the second time, the byte in the low bits).
+//   fp32: the quotient by an approximate reciprocal; exact_bytes is left to a thread that met a value within 2^-18 of a
+//   border, which random values are once in 2^18.
+//   16-bit types: a value of at most 11 bits lies on a border (k + 1/2) d of at most 15 bits, or 2^-16 away. One Newton
+//   step gives the quotient to 2^-22, and exactly where it lies on a border, which is common (one block in 25: the scale
+//   of a bf16 maximum divisible by 7 is exact).
+// Either way exact_bytes takes the blocks whose scale leaves quotients past 7.5 (below f16's normal range, or capped).
 template <typename T>
 __device__ __forceinline__ uint2 code_bytes(const float (&lo)[8], const float (&hi)[8], float top, float d, const T* src) {
     constexpr float kMagic = 12582912.f;
@@ -75,8 +83,15 @@ __device__ __forceinline__ uint2 code_bytes(const float (&lo)[8], const float (&
     uint32_t byte[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float a = fmaf(lo[j], inv, kMagic) - kMagic, b = fmaf(hi[j], inv, kMagic) - kMagic;
-        off = fmaxf(off, fmaxf(fabsf(fmaf(-a, d, lo[j])), fabsf(fmaf(-b, d, hi[j]))));
+        float a, b;
+        if constexpr (sizeof(T) == 4) {
+            a = fmaf(lo[j], inv, kMagic) - kMagic, b = fmaf(hi[j], inv, kMagic) - kMagic;
+            off = fmaxf(off, fmaxf(fabsf(fmaf(-a, d, lo[j])), fabsf(fmaf(-b, d, hi[j]))));
+        } else {
+            const float x = lo[j] * inv, y = hi[j] * inv;
+            a = (fmaf(fmaf(-x, d, lo[j]), inv, x) + kMagic) - kMagic;
+            b = (fmaf(fmaf(-y, d, hi[j]), inv, y) + kMagic) - kMagic;
+        }
         byte[j] = __float_as_uint(fmaf(b, 16.f, a) + (kMagic + 136.f));
     }
     if (off >= 0.5f * d * (1.f - 0x1p-18f) || d < 0x1p-14f || top > 7.f * 65504.f) return exact_bytes(src, d);
@@ -90,6 +105,22 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+
+// Eight elements from the 16-byte words that they were loaded in.
+__device__ __forceinline__ void widen8(const uint4* w, float (&x)[8], float) {
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]);
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4* w, float (&x)[8], T tag) {
+    const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2(v[i], tag);
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
 }
 
 template <typename T, int U>
@@ -107,26 +138,31 @@ __global__ void __launch_bounds__(kMaxThreads) kv4_write_kernel(const KvRowsArgs
         const Piece q = piece_of(p.c, active ? u : 0);
         const T* src = static_cast<const T*>(q.v ? p.v : p.k) + q.el;
         const long long stride = q.v ? p.v_stride : p.k_stride;
-        float lo[U][8], hi[U][8];
+        constexpr int W = (int)sizeof(T) / 2;  // 16-byte words of 8 elements
+        uint4 raw[U][2 * W];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
+            const bool read = active && t0 + i < p.T;
+            const uint4 *lo = reinterpret_cast<const uint4*>(src + (t0 + i) * stride), *hi = reinterpret_cast<const uint4*>(src + (t0 + i) * stride + 16);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lo[i][j] = hi[i][j] = 0.f;
-            if (active && t0 + i < p.T) {
-                load_floats(src + (t0 + i) * stride, lo[i]);
-                load_floats(src + (t0 + i) * stride + 16, hi[i]);
+            for (int j = 0; j < W; ++j) {
+                raw[i][j] = read ? lo[j] : make_uint4(0u, 0u, 0u, 0u);
+                raw[i][W + j] = read ? hi[j] : make_uint4(0u, 0u, 0u, 0u);
             }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
+            float lo[8], hi[8];
+            widen8(&raw[i][0], lo, T());
+            widen8(&raw[i][W], hi, T());
             float top = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max_or_nan(top, max_or_nan(fabsf(lo[i][j]), fabsf(hi[i][j])));
+            for (int j = 0; j < 8; ++j) top = max_or_nan(top, max_or_nan(fabsf(lo[j]), fabsf(hi[j])));
             top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
             const bool finite = top < INFINITY;
             const __half dh = __float2half_rn(fminf(__fdiv_rn(top, 7.f), 65504.f));
             const float d = __half2float(dh);
-            const uint2 w = finite && d > 0.f ? code_bytes(lo[i], hi[i], top, d, src + (t0 + i) * stride)
+            const uint2 w = finite && d > 0.f ? code_bytes(lo, hi, top, d, src + (t0 + i) * stride)
                                               : make_uint2(0x88888888u, 0x88888888u);
             if (active && slot[i] >= 0 && slot[i] < slots) {
                 const int page = slot[i] >> p.lp, off = slot[i] & (p.c.page_size - 1);
@@ -219,14 +255,14 @@ cudaError_t launch_rows(const KvRowsArgs& a, cudaStream_t s, F1 one, F4 four) {
 cudaError_t launch_kv4_write(const KvRowsArgs& a, int dtype, cudaStream_t s) {
     return with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
-        return launch_rows<kTokens>(a, s, kv4_write_kernel<T, 1>, kv4_write_kernel<T, kTokens>);
+        return launch_rows<kTokens<T>>(a, s, kv4_write_kernel<T, 1>, kv4_write_kernel<T, kTokens<T>>);
     });
 }
 
 cudaError_t launch_kv4_read(const KvRowsArgs& a, int dtype, cudaStream_t s) {
     return with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
-        return launch_rows<kTokens>(a, s, kv4_read_kernel<T, 1>, kv4_read_kernel<T, kTokens>);
+        return launch_rows<kTokens<T>>(a, s, kv4_read_kernel<T, 1>, kv4_read_kernel<T, kTokens<T>>);
     });
 }
 

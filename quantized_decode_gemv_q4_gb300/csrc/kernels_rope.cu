@@ -17,9 +17,13 @@ namespace q4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;                     // heads of a lane where there are many rows
-constexpr int kBlocks = 2;                    // resident blocks of an SM where there are many rows
-constexpr long long kManyLanes = 1LL << 20;   // three for each resident thread of the device
+// Where there are many rows (three for each resident thread of the device) a lane takes 4 heads and the resident blocks
+// walk over the tokens, else a lane takes a head. 8191 bf16 tokens of 32 + 8 heads of 128: 42 us with a head a lane, 37 us
+// with 4 heads a lane and a block for every 256 lanes, 32 us so (26 us for the bytes). What is left is the latency of the
+// table row behind the position, one round ahead.
+constexpr int kHeads = 4;
+constexpr int kBlocks = 2;  // resident blocks of an SM
+constexpr long long kManyLanes = 1LL << 20;
 
 // 16 bytes of activations as they lie in memory, and as floats.
 __device__ __forceinline__ void widen(uint4 w, float (&x)[4], float) {
