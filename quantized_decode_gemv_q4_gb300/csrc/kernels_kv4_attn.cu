@@ -941,8 +941,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const 
 // Groups of 8 rows that a warp holds: two where there are more than 8 rows and the outputs fit the registers.
 int row_groups(int M, int group, int D) { return M * group > 8 && D < 256 ? 2 : 1; }
 
-// Whole items where no sequence of the call can be longer than this: one launch instead of two.
-constexpr long long kItemTokens = 512;
+// Items (whole, or split evenly over up to two CTAs an SM, each with two tiles a warp at least) where the page table admits
+// no sequence longer than kItemTokens, for a single sequence, and for few items of up to kSplitTokens; streams otherwise.
+// The streams' scan, their second launch and its join cost 8 us more than a launch of whole items (8 sequences of 100
+// tokens, 8 key heads of 128: 6.3 and 14.9 us; of 1500 tokens, split in 4: 12 and 17.5 us), and do not mind the lengths:
+// a CTA with the longest of ragged items is waited for, 25 us for 8192 tokens split in two.
+constexpr long long kItemTokens = 1024;
+constexpr long long kSplitTokens = 8192;
 
 template <typename F>
 auto with_plan(int D, int nt, bool split, F fn) {
@@ -1000,21 +1005,20 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
             return few ? launch_grid(kv4_attention_join_kernel<DB, NT, 1>, dim3(blocks, 8 * NT), dim3(kJoinThreads), 0, s, true, p)
                        : launch_grid(kv4_attention_join_kernel<DB, NT, 8 * NT>, dim3(blocks), dim3(kJoinThreads), 0, s, true, p);
         };
-        const long long most = (long long)a.max_pages * a.c.page_size;
-        if (most <= kItemTokens || a.B == 1) {
+        const long long most = (long long)a.max_pages * a.c.page_size, call_items = (long long)items * a.B;
+        if (most <= kItemTokens || a.B == 1 || (most <= kSplitTokens && call_items <= sm_count)) {
             constexpr int kRing = kItemWarps * L::kStages * G::kStage;
             static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
             p.warps = 0;
-            if (most > kItemTokens)
-                p.splits = (int)std::max(1LL, std::min<long long>(sm_count * L::kItemCtas / items, most / (kTile * kItemWarps)));
+            p.splits = (int)std::max(1LL, std::min(2LL * sm_count / call_items, most / (2 * kTile * kItemWarps)));
             cudaError_t e = launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT>, dim3((unsigned)(items * p.splits), (unsigned)a.B),
                                              kItemWarps * 32, kRing, s, p);
-            if (e == cudaSuccess && p.splits > 1) e = join((unsigned)items, true);
+            if (e == cudaSuccess && p.splits > 1) e = join((unsigned)call_items, true);
             return e;
         }
         cudaError_t e = launch_with_ring(kv4_attention_streams_kernel<DB, NT, SPLIT>, dim3((unsigned)sm_count), L::kWarps * 32,
                                          L::kWarps * L::kStages * G::kStage, s, p);
-        if (e == cudaSuccess) e = join((unsigned)(items * a.B), items * a.B <= 64);
+        if (e == cudaSuccess) e = join((unsigned)call_items, call_items <= 64);
         return e;
     });
 }
