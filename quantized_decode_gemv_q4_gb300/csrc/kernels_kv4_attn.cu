@@ -48,13 +48,13 @@ struct Geo {
     static constexpr int kJoinRow = D + 4;                 // floats; the pad spreads the joining stores over the banks
 };
 
-// Warps and stages (tiles of a warp in flight or in use), by registers: 12 warps of up to 168 or 8 of up to 255 on an SM.
+// Warps and stages (tiles of a warp in flight or in use), by registers and shared memory.
 template <int DB, int NT, bool SPLIT>
 struct Plan {
     static constexpr bool kTwelve = DB == 2 || (DB == 4 && NT == 1);
-    static constexpr int kWarps = kTwelve ? 12 : 8;       // streaming warps of an SM, all in one CTA
-    static constexpr int kItemCtas = kTwelve ? 3 : 2;     // CTAs of whole items per SM
-    static constexpr int kStages = DB == 2 ? 5 : DB == 4 && !kTwelve ? 4 : 3;
+    static constexpr int kWarps = kTwelve ? 12 : 8;    // streaming warps of an SM, all in one CTA
+    static constexpr int kItemCtas = kTwelve ? 3 : 2;  // CTAs of whole items per SM
+    static constexpr int kStages = DB == 2 ? 5 : DB == 4 && NT == 1 ? 3 : DB == 4 ? 4 : 2;
 };
 
 struct Params {
@@ -99,6 +99,21 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(SIZE), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ void lds_floats(uint32_t addr, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3])
+                     : "r"(addr + 4u * i)
+                     : "memory");
+}
+__device__ __forceinline__ void sts_word(uint32_t addr, uint32_t w) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts_quad(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 template <int WORDS>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[WORDS]) {
     if constexpr (WORDS == 2) {
@@ -112,6 +127,18 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[WORDS]) {
                          : "memory");
     }
 }
+
+// A token's scales: one, two or four words.
+template <int WORDS>
+__device__ __forceinline__ void lds_own(uint32_t addr, uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    else lds_words<WORDS>(addr, w);
+}
+
+// Token t of a tile lies in row place(t) of its stage: matrix j of ldmatrix reads rows 8 j .. 8 j + 7, and column c of it
+// becomes token 8 (c / 2) + 2 j + c % 2, so that a lane's eight tokens (columns 2 t4 and 2 t4 + 1 of four matrices) are
+// the consecutive ones 8 t4 .. 8 t4 + 7.
+__device__ __forceinline__ int place(int t) { return 8 * (t >> 1 & 3) + 2 * (t >> 3) + (t & 1); }
 
 // A row's 16-byte chunk c sits at chunk c ^ swizzle(row), so that eight rows of one chunk cover all banks.
 template <int DB>
@@ -215,7 +242,7 @@ struct Rows {
     static constexpr int D = G::D, MT = SPLIT ? NT : (NT + 1) / 2, ROWS = 8 * NT;
     int lane, g, t4;
     uint32_t k1024;             // see codes_of
-    uint32_t qa[MT][DB][2][4];  // queries in the layout of the row operand
+    uint32_t queries;           // shared address of this lane's row operands: [MT][DB][2] of 16 bytes, 512 apart
     float factor[NT];           // row g: score * log2(e) = factor * accumulated sum
     int seen_end[NT], seen_lo[NT];  // row g sees the tokens seen_lo .. seen_end - 1
     int all_end, all_lo;        // tokens that every row sees, so that only tiles outside look at each token
@@ -223,8 +250,11 @@ struct Rows {
     float top[NT], ref[NT], l[NT];  // row g: running maximum, reference, the lane's part of the sum
     int e_run;                  // the largest exponent of a value scale so far
 
-    __device__ __forceinline__ void init() {
+    static constexpr uint32_t kQueries = MT * DB * 2 * 512;  // bytes of a warp's row operands
+
+    __device__ __forceinline__ void init(uint32_t at) {
         lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+        queries = at + (uint32_t)lane * 16u;
         asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
     }
 
@@ -274,14 +304,19 @@ struct Rows {
                     xh[j] = __half2float(__float2half_rn(y));
                     xl[j] = y - xh[j];
                 }
+                // words 0 and 2: row g, words 1 and 3: row g + 8 (the low parts of fp32 queries; of 16-bit queries the next
+                // group's rows, or nothing)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    qa[mt][k][i][hi] = pack_half2(xh[i], xh[i + 2]);
-                    qa[mt][k][i][2 + hi] = pack_half2(xh[4 + i], xh[6 + i]);
-                    // (of 16-bit queries the low parts are zeros, which fill rows that a single group of 8 leaves free)
-                    if constexpr (SPLIT || NT == 1) {
-                        qa[mt][k][i][1] = pack_half2(xl[i], xl[i + 2]);
-                        qa[mt][k][i][3] = pack_half2(xl[4 + i], xl[6 + i]);
+                    const uint32_t at = queries + (uint32_t)(((mt * DB + k) * 2 + i) * 512);
+                    const uint32_t a0 = pack_half2(xh[i], xh[i + 2]), a2 = pack_half2(xh[4 + i], xh[6 + i]);
+                    if constexpr (SPLIT) {
+                        sts_quad(at, a0, pack_half2(xl[i], xl[i + 2]), a2, pack_half2(xl[4 + i], xl[6 + i]));
+                    } else if constexpr (NT == 1) {
+                        sts_quad(at, a0, 0u, a2, 0u);
+                    } else {
+                        sts_word(at + 4u * hi, a0);
+                        sts_word(at + 8u + 4u * hi, a2);
                     }
                 }
             }
@@ -304,36 +339,64 @@ struct Rows {
     template <bool MASKED>  // some row does not see every token
     __device__ __forceinline__ void tile(uint32_t st, int tok0) {
         const uint32_t codes = st + (uint32_t)(lane * G::kRow + swizzle<DB>(lane) * 16);  // chunk k: codes ^ (16 k)
-        const uint32_t scales = st + (uint32_t)(2 * G::kCodes + 2 * t4 * DB * 2);
-        // scores: sc[n][j] of row g, tokens 8 (j / 2) + 2 t4 + j % 2
+        uint32_t kw[DB][4];
+#pragma unroll
+        for (int k = 0; k < DB; ++k) ldsm4(codes ^ (uint32_t)(16 * k), kw[k]);
+        // This lane's token's scales become fp32 [K, V][block][token] in the place of the keys' codes, which are in
+        // registers now: a lane then reads those of its eight tokens as they are used (converting them where they are used
+        // would take 64 conversions, eight lanes the same ones). Their largest exponent is noted on the way (zeros stand
+        // where nothing was read).
+        {
+            uint32_t own[2][DB / 2], m = 0u;
+            const uint32_t at = st + (uint32_t)(2 * G::kCodes + lane * DB * 2);
+            lds_own<DB / 2>(at, own[0]);
+            lds_own<DB / 2>(at + G::kScales, own[1]);
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int k = 0; k < DB / 2; ++k) {
+                    const float2 d = to_float2(own[v][k]);
+                    const uint32_t to = st + (uint32_t)(((v * DB + 2 * k) * 32 + lane) * 4);
+                    sts_word(to, __float_as_uint(d.x));
+                    sts_word(to + 128u, __float_as_uint(d.y));
+                    if (v) m = max(m, max(own[v][k] & 0x7C00u, (own[v][k] >> 16) & 0x7C00u));
+                }
+            e_run = max(e_run, (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 15);
+            __syncwarp();
+        }
+        const uint32_t scales = st + (uint32_t)(8 * t4 * 4);  // of block k: + 128 k, of the values' blocks + 128 (DB + k)
+        // scores: sc[n][j] of row g, token 8 t4 + j
         float sc[NT][8];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 8; ++j) sc[n][j] = 0.f;
-        uint32_t kd[4][DB], kw[DB][4];
+        constexpr int KB = 1;  // blocks at a time
 #pragma unroll
-        for (int k = 0; k < DB; ++k) ldsm4(codes ^ (uint32_t)(16 * k), kw[k]);
+        for (int kk = 0; kk < DB; kk += KB) {
+            uint32_t x[4 * KB][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) lds_words<DB>(scales + (uint32_t)(8 * j * DB * 2), kd[j]);
-#pragma unroll
-        for (int kk = 0; kk < DB; kk += 2) {
-            uint32_t x[8][4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) codes_of(kw[kk + j / 4][j % 4], k1024, x[j]);
+            for (int j = 0; j < 4 * KB; ++j) codes_of(kw[kk + j / 4][j % 4], k1024, x[j]);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                float c[8][4];
+                float c[4 * KB][4];
+                uint32_t q[KB][2][4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mma(c[j], qa[mt][kk + j / 4][0], x[j][0], x[j][1], zero);
+                for (int k = 0; k < KB; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mma(c[j], qa[mt][kk + j / 4][1], x[j][2], x[j][3], c[j]);
+                    for (int i = 0; i < 2; ++i) lds_words<4>(queries + (uint32_t)(((mt * DB + kk + k) * 2 + i) * 512), q[k][i]);
 #pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
-                    const int j = jj % 4, k = kk + jj / 4;
-                    const float2 da = to_float2(kd[j][k / 2]), db = to_float2(kd[j][DB / 2 + k / 2]);
-                    const float2 d = make_float2(k % 2 ? da.y : da.x, k % 2 ? db.y : db.x);
+                for (int j = 0; j < 4 * KB; ++j) mma(c[j], q[j / 4][0], x[j][0], x[j][1], zero);
+#pragma unroll
+                for (int j = 0; j < 4 * KB; ++j) mma(c[j], q[j / 4][1], x[j][2], x[j][3], c[j]);
+                float kd[KB][8];
+#pragma unroll
+                for (int k = 0; k < KB; ++k) lds_floats(scales + (uint32_t)(128 * (kk + k)), kd[k]);
+#pragma unroll
+                for (int jj = 0; jj < 4 * KB; ++jj) {
+                    const int j = jj % 4;
+                    const float2 d = make_float2(kd[jj / 4][2 * j], kd[jj / 4][2 * j + 1]);
                     if constexpr (SPLIT) {
                         const float2 both = fadd2(make_float2(c[jj][0], c[jj][1]), make_float2(c[jj][2], c[jj][3]));
                         const float2 y = ffma2(both, d, make_float2(sc[mt][2 * j], sc[mt][2 * j + 1]));
@@ -353,16 +416,6 @@ struct Rows {
             }
         }
 
-        // the largest exponent of a value scale, so far (zeros stand where nothing was read)
-        {
-            const uint32_t at = st + (uint32_t)(2 * G::kCodes + G::kScales + lane * DB * 2);
-            uint32_t own[DB / 2], m = 0u;
-            if constexpr (DB == 2) own[0] = lds32(at);
-            else lds_words<DB / 2>(at, own);
-#pragma unroll
-            for (int k = 0; k < DB / 2; ++k) m = max(m, max(own[k] & 0x7C00u, (own[k] >> 16) & 0x7C00u));
-            e_run = max(e_run, (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 15);
-        }
         bool moved = false;
         float keep[NT];
         uint32_t seen[NT];
@@ -372,7 +425,7 @@ struct Rows {
             if constexpr (MASKED) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int t = tok0 + 8 * (j / 2) + 2 * t4 + j % 2;
+                    const int t = tok0 + 8 * t4 + j;
                     if (t >= seen_lo[n] && t < seen_end[n]) seen[n] |= 1u << j;
                     else sc[n][j] = -INFINITY;
                 }
@@ -404,28 +457,31 @@ struct Rows {
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sc[n][j] = ex2(fmaf(sc[n][j], factor[n], -ref[n]));
-                if (MASKED && !(seen[n] >> j & 1u)) sc[n][j] = 0.f;  // also where the query is not finite
-                l[n] += sc[n][j];
+            for (int j = 0; j < 8; j += 2) {
+                float2 y = ffma2(make_float2(sc[n][j], sc[n][j + 1]), make_float2(factor[n], factor[n]), make_float2(-ref[n], -ref[n]));
+                y.x = ex2(y.x), y.y = ex2(y.y);
+                if (MASKED && !(seen[n] >> j & 1u)) y.x = 0.f;  // also where the query is not finite
+                if (MASKED && !(seen[n] >> (j + 1) & 1u)) y.y = 0.f;
+                sc[n][j] = y.x, sc[n][j + 1] = y.y;
+                sum = fadd2(sum, y);
             }
+            l[n] += sum.x + sum.y;
         }
 
-        uint32_t vd[4][DB];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) lds_words<DB>(scales + (uint32_t)(G::kScales + 8 * j * DB * 2), vd[j]);
 #pragma unroll
         for (int k = 0; k < DB; ++k) {
             uint32_t w[4], x[4][4];
             ldsm4_trans((codes ^ (uint32_t)(16 * k)) + G::kCodes, w);
 #pragma unroll
             for (int u = 0; u < 4; ++u) codes_of(w[u], k1024, x[u]);
+            float vd[8];
+            lds_floats(scales + (uint32_t)(128 * (DB + k)), vd);
             uint32_t hi[NT][4], lo[SPLIT ? NT : 1][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 da = to_float2(vd[j][k / 2]), db = to_float2(vd[j][DB / 2 + k / 2]);
-                const float2 d = make_float2(k % 2 ? da.y : da.x, k % 2 ? db.y : db.x);
+                const float2 d = make_float2(vd[2 * j], vd[2 * j + 1]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float2 y = __fmul2_rn(make_float2(sc[n][2 * j], sc[n][2 * j + 1]), d);
@@ -510,11 +566,10 @@ struct Ring {
             constexpr bool ALL = decltype(all)::value;
 #pragma unroll
             for (int j = 0; j < DB; ++j) {
-                const int lo = lane / DB, tok = j * (32 / DB) + lo;
+                const int tok = j * (32 / DB) + lane / DB, at = place(tok);
                 const int r = __shfl_sync(0xffffffffu, row, tok);
                 const long long off = (long long)(ALL ? r : max(r, 0)) * G::kRow;
-                const uint32_t dst = in + (uint32_t)(lo * G::kRow + ((lane % DB) ^ swizzle<DB>(lo + j * (32 / DB) % 8)) * 16) +
-                                     (uint32_t)(j * (32 / DB) * G::kRow);
+                const uint32_t dst = in + (uint32_t)(at * G::kRow + ((lane % DB) ^ swizzle<DB>(at)) * 16);
                 const uint32_t bytes = ALL || r >= 0 ? 16u : 0u;
                 copy_async<16>(dst, k_src + off, bytes);
                 copy_async<16>(dst + G::kCodes, v_src + off, bytes);
@@ -540,13 +595,26 @@ struct Ring {
 
 enum : int { kSkip = -1, kBadPage = -2 };
 
-// The cache row of token t, kSkip outside [lo, end), kBadPage where its page is none.
-__device__ __forceinline__ int row_of(const Params& p, const int* table, int h, int t, int lo, int end) {
-    if (t < lo || t >= end) return kSkip;
-    const int page = table[t >> p.lp];
-    if ((unsigned)page >= (unsigned)p.a.c.num_pages) return kBadPage;
-    return ((page * p.a.c.num_kv_heads + h) << p.lp) + (t & (p.a.c.page_size - 1));  // below 2^31
-}
+// A token to copy: its page as the page table has it. It is looked up a tile ahead, and nothing is made of the loaded page
+// before the next tile's copies (row()), so that nobody waits for the load.
+struct Lookup {
+    int page, h, t;  // t < 0: none is read
+
+    __device__ __forceinline__ void token(const Params& p, const int* table, int head, int tok, int lo, int end) {
+        const bool read = tok >= lo && tok < end;
+        h = head;
+        t = read ? tok : -1;
+        page = 0;
+        if (read) page = table[tok >> p.lp];
+    }
+    __device__ __forceinline__ void none() { page = h = 0, t = -1; }
+    // The token's cache row, kSkip where none is read, kBadPage where its page is none.
+    __device__ __forceinline__ int row(const Params& p) const {
+        if (t < 0) return kSkip;
+        if ((unsigned)page >= (unsigned)p.a.c.num_pages) return kBadPage;
+        return ((page * p.a.c.num_kv_heads + h) << p.lp) + (t & (p.a.c.page_size - 1));  // below 2^31
+    }
+};
 
 // ------------------------------------------------------------------------------------------------
 // Whole items
@@ -563,8 +631,10 @@ __global__ void __launch_bounds__(kItemWarps * 32, Plan<DB, NT, SPLIT>::kItemCta
     const int warp = threadIdx.x >> 5;
     Rows<DB, NT, SPLIT> w;
     Ring<DB, L::kStages> ring;
-    w.init();
-    ring.init(smem_addr(ring_memory) + (uint32_t)(warp * L::kStages * G::kStage), a.c);
+    constexpr uint32_t kWarpBytes = L::kStages * G::kStage + Rows<DB, NT, SPLIT>::kQueries;
+    const uint32_t mine_at = smem_addr(ring_memory) + (uint32_t)warp * kWarpBytes;
+    ring.init(mine_at, a.c);
+    w.init(mine_at + L::kStages * G::kStage);
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -579,30 +649,30 @@ __global__ void __launch_bounds__(kItemWarps * 32, Plan<DB, NT, SPLIT>::kItemCta
     const int first = s.first + tile0 * kTile, end = min(s.n, s.first + tile1 * kTile);
     int ahead = first + warp * kTile + w.lane;  // this lane's token of the next tile to look up
     auto lookup = [&] {
-        const int row = row_of(p, table, h, ahead, s.lo, end);
+        Lookup x;
+        x.token(p, table, h, ahead, s.lo, end);
         ahead += kItemWarps * kTile;
-        return row;
+        return x;
     };
-    int rows[L::kStages];
+    auto copy = [&](const Lookup& x) {
+        const int row = x.row(p);
+        bad = bad || row == kBadPage;
+        ring.copy(a.c, row);
+    };
+    Lookup ups[L::kStages];
 #pragma unroll
-    for (int i = 0; i < L::kStages; ++i) rows[i] = lookup();
+    for (int i = 0; i < L::kStages; ++i) ups[i] = lookup();
 #pragma unroll
     for (int i = 0; i < L::kStages - 1; ++i) {
-        if (i < mine) {
-            bad = bad || rows[i] == kBadPage;
-            ring.copy(a.c, rows[i]);
-        }
+        if (i < mine) copy(ups[i]);
         ring.filled();
     }
-    int next = rows[L::kStages - 1];
+    Lookup next = ups[L::kStages - 1];
     w.start(p, b, h, row0, s);
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
         ring.wait();
-        if (i + L::kStages - 1 < mine) {
-            bad = bad || next == kBadPage;
-            ring.copy(a.c, next);
-        }
+        if (i + L::kStages - 1 < mine) copy(next);
         ring.filled();
         next = lookup();
         w.take(ring.out, first + (i * kItemWarps + warp) * kTile);
@@ -733,8 +803,10 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
     const int stream = warp * (int)gridDim.x + (int)blockIdx.x;
     Rows<DB, NT, SPLIT> w;
     Ring<DB, L::kStages> ring;
-    w.init();
-    ring.init(smem_addr(ring_memory) + (uint32_t)(warp * L::kStages * G::kStage), a.c);
+    constexpr uint32_t kWarpBytes = L::kStages * G::kStage + Rows<DB, NT, SPLIT>::kQueries;
+    const uint32_t mine_at = smem_addr(ring_memory) + (uint32_t)warp * kWarpBytes;
+    ring.init(mine_at, a.c);
+    w.init(mine_at + L::kStages * G::kStage);
     grid_dependency_wait();
     grid_launch_dependents();
     scan_cost<L::kWarps * 32>(a, prefix);
@@ -756,10 +828,12 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
     int left = fill.count, ahead = fill.s.first + fill.tile0 * kTile + w.lane, ahead_lo = fill.s.lo, ahead_end = fill.s.n;
     const int* table = a.block_table + (long long)fill.b * a.max_pages;
     int fill_h = fill.item / p.chunks;
-    auto lookup = [&](bool& some) {  // the row of this lane's token of the next tile of the piece; some: there is a tile
+    auto lookup = [&](bool& some) {  // this lane's token of the next tile of the piece; some: there is a tile
+        Lookup x;
+        x.none();
         some = left > 0;
-        if (!some) return (int)kSkip;
-        const int row = row_of(p, table, fill_h, ahead, ahead_lo, ahead_end);
+        if (!some) return x;
+        x.token(p, table, fill_h, ahead, ahead_lo, ahead_end);
         ahead += kTile;
         if (--left == 0) {
             next_part(fill, a, items, ends[warp]);
@@ -770,21 +844,22 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
                 fill_h = fill.item / p.chunks;
             }
         }
-        return row;
+        return x;
     };
     uint32_t bad_stages = 0u;  // bit i: the tile copied i tiles before the newest met a bad page
-    auto copy = [&](bool some, int row) {
+    auto copy = [&](bool some, const Lookup& x) {
+        const int row = x.row(p);
         if (some) ring.copy(a.c, row);
         bad_stages = bad_stages << 1 | (some && row == kBadPage ? 1u : 0u);
         ring.filled();
     };
-    int rows[L::kStages];
+    Lookup ups[L::kStages];
     bool some[L::kStages];
 #pragma unroll
-    for (int i = 0; i < L::kStages; ++i) rows[i] = lookup(some[i]);
+    for (int i = 0; i < L::kStages; ++i) ups[i] = lookup(some[i]);
 #pragma unroll
-    for (int i = 0; i < L::kStages - 1; ++i) copy(some[i], rows[i]);
-    int next_row = rows[L::kStages - 1];
+    for (int i = 0; i < L::kStages - 1; ++i) copy(some[i], ups[i]);
+    Lookup next = ups[L::kStages - 1];
     bool next_some = some[L::kStages - 1];
 
 #pragma unroll 1
@@ -800,8 +875,8 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
         for (; tok0 != last; tok0 += kTile) {
             ring.wait();
             bad = bad || (bad_stages >> (L::kStages - 2) & 1u);
-            copy(next_some, next_row);
-            next_row = lookup(next_some);
+            copy(next_some, next);
+            next = lookup(next_some);
             w.take(ring.out, tok0);
             ring.used();
         }
@@ -1007,7 +1082,7 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
         };
         const long long most = (long long)a.max_pages * a.c.page_size, call_items = (long long)items * a.B;
         if (most <= kItemTokens || a.B == 1 || (most <= kSplitTokens && call_items <= sm_count)) {
-            constexpr int kRing = kItemWarps * L::kStages * G::kStage;
+            constexpr int kWarpBytes = L::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries, kRing = kItemWarps * kWarpBytes;
             static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
             p.warps = 0;
             p.splits = (int)std::max(1LL, std::min(2LL * sm_count / call_items, most / (2 * kTile * kItemWarps)));
@@ -1017,7 +1092,7 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
             return e;
         }
         cudaError_t e = launch_with_ring(kv4_attention_streams_kernel<DB, NT, SPLIT>, dim3((unsigned)sm_count), L::kWarps * 32,
-                                         L::kWarps * L::kStages * G::kStage, s, p);
+                                         L::kWarps * (L::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries), s, p);
         if (e == cudaSuccess) e = join((unsigned)call_items, call_items <= 64);
         return e;
     });
