@@ -960,47 +960,58 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const 
     for (int r0 = blockIdx.y * RPB; r0 < (int)(blockIdx.y + 1) * RPB; r0 += RT) {
         const int r = r0 + rt;
         if (row0 + r0 >= p.R) break;  // the same for the whole block
-        // the largest reference: a thread's share of the parts, then over the threads of its row
-        float top = -INFINITY;
-        for (int i = pt * D4 + d4; i < n; i += PT * D4) top = fmaxf(top, part(i)[ROWS * D + r]);
-#pragma unroll
-        for (int x = (D4 < 32 ? D4 : 32) / 2; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        if constexpr (D4 > 32) {  // a row's elements take two warps
-            __shared__ float halves[kJoinThreads / 32];
-            if ((threadIdx.x & 31) == 0) halves[threadIdx.x / 32] = top;
-            __syncthreads();
-            top = fmaxf(top, halves[(threadIdx.x / 32) ^ 1]);
-        }
-        if constexpr (PT > 1) {
-            if (d4 == 0) sm[pt][rt] = top;
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < PT; ++u) top = fmaxf(top, sm[u][rt]);
-        }
+        // a thread's share of the parts, eight in flight, each under the largest reference so far (a part that saw nothing
+        // has reference -infinity and weighs 0)
+        float top = -INFINITY, l = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        if (top != -INFINITY) {
-#pragma unroll 8
-            for (int i = pt; i < n; i += PT) {
-                const float* x = part(i);
-                const float4 o = *reinterpret_cast<const float4*>(x + r * D + 4 * d4);
-                const float ref = x[ROWS * D + r], pl = x[ROWS * D + ROWS + r];
-                if (ref == -INFINITY) continue;  // saw nothing; its elements were not computed
-                const float f = ex2(ref - top);
-                l = fmaf(pl, f, l);
-                v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+        constexpr int kAhead = 8;
+        for (int i0 = pt; i0 < n; i0 += PT * kAhead) {
+            float4 o[kAhead];
+            float ref[kAhead], pl[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * PT;
+                ref[u] = -INFINITY, pl[u] = 0.f, o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    const float* x = part(i);
+                    o[u] = *reinterpret_cast<const float4*>(x + r * D + 4 * d4);
+                    ref[u] = x[ROWS * D + r], pl[u] = x[ROWS * D + ROWS + r];
+                }
+            }
+            float nt = top;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) nt = fmaxf(nt, ref[u]);
+            if (nt != -INFINITY) {
+                const float keep = ex2(top - nt);
+                l *= keep, v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const float f = ex2(ref[u] - nt);
+                    l = fmaf(pl[u], f, l);
+                    v.x = fmaf(o[u].x, f, v.x), v.y = fmaf(o[u].y, f, v.y), v.z = fmaf(o[u].z, f, v.z), v.w = fmaf(o[u].w, f, v.w);
+                }
+                top = nt;
             }
         }
         if constexpr (PT > 1) {
             so[pt][rt][d4] = v;
-            if (d4 == 0) sl[pt][rt] = l;
+            if (d4 == 0) sl[pt][rt] = l, sm[pt][rt] = top;
             __syncthreads();
             if (pt == 0) {
+                float all = top;
 #pragma unroll
-                for (int u = 1; u < PT; ++u) {
-                    const float4 o = so[u][rt][d4];
-                    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-                    l += sl[u][rt];
+                for (int u = 1; u < PT; ++u) all = fmaxf(all, sm[u][rt]);
+                if (all != -INFINITY) {
+                    const float keep = ex2(top - all);
+                    l *= keep, v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+#pragma unroll
+                    for (int u = 1; u < PT; ++u) {
+                        const float4 o = so[u][rt][d4];
+                        const float f = ex2(sm[u][rt] - all);
+                        l = fmaf(sl[u][rt], f, l);
+                        v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+                    }
+                    top = all;
                 }
             }
         }
