@@ -50,11 +50,15 @@ struct Geo {
 
 // Warps and stages (tiles of a warp in flight or in use), by registers and shared memory.
 template <int DB, int NT, bool SPLIT>
-struct Plan {
+struct Plan {  // streams
     static constexpr bool kTwelve = DB == 2 || (DB == 4 && NT == 1);
-    static constexpr int kWarps = kTwelve ? 12 : 8;    // streaming warps of an SM, all in one CTA
-    static constexpr int kItemCtas = kTwelve ? 3 : 2;  // CTAs of whole items per SM
+    static constexpr int kWarps = kTwelve ? 12 : 8;  // warps of an SM, all in one CTA
     static constexpr int kStages = DB == 2 ? 5 : DB == 4 && NT == 1 ? 3 : DB == 4 ? 4 : 2;
+};
+template <int DB, int NT, bool SPLIT, bool MANY>
+struct ItemPlan {  // items: MANY CTAs, which hide each other's starts, or few
+    static constexpr int kCtas = MANY ? 4 : 2;  // CTAs of an SM
+    static constexpr int kStages = MANY ? (DB == 2 ? 4 : 2) : DB == 8 ? 2 : 4;
 };
 
 struct Params {
@@ -620,10 +624,10 @@ struct Lookup {
 // Whole items
 // ------------------------------------------------------------------------------------------------
 
-template <int DB, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kItemWarps * 32, Plan<DB, NT, SPLIT>::kItemCtas) kv4_attention_items_kernel(const Params p) {
+template <int DB, int NT, bool SPLIT, bool MANY>
+__global__ void __launch_bounds__(kItemWarps * 32, ItemPlan<DB, NT, SPLIT, MANY>::kCtas) kv4_attention_items_kernel(const Params p) {
     using G = Geo<DB>;
-    using L = Plan<DB, NT, SPLIT>;
+    using L = ItemPlan<DB, NT, SPLIT, MANY>;
     constexpr int D = G::D, ROWS = 8 * NT;
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ float join_ref[kItemWarps][ROWS], join_l[kItemWarps][ROWS];
@@ -1093,12 +1097,19 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
         };
         const long long most = (long long)a.max_pages * a.c.page_size, call_items = (long long)items * a.B;
         if (most <= kItemTokens || a.B == 1 || (most <= kSplitTokens && call_items <= sm_count)) {
-            constexpr int kWarpBytes = L::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries, kRing = kItemWarps * kWarpBytes;
-            static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
             p.warps = 0;
             p.splits = (int)std::max(1LL, std::min(2LL * sm_count / call_items, most / (2 * kTile * kItemWarps)));
-            cudaError_t e = launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT>, dim3((unsigned)(items * p.splits), (unsigned)a.B),
-                                             kItemWarps * 32, kRing, s, p);
+            auto go = [&](auto many) {
+                constexpr bool MANY = decltype(many)::value;
+                constexpr int kWarpBytes = ItemPlan<DB, NT, SPLIT, MANY>::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries;
+                constexpr int kRing = kItemWarps * kWarpBytes;
+                static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
+                return launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT, MANY>, dim3((unsigned)(items * p.splits), (unsigned)a.B),
+                                        kItemWarps * 32, kRing, s, p);
+            };
+            // more CTAs than two an SM: four of them fit where 128 registers do
+            constexpr bool kFour = DB == 2 || (DB == 4 && NT == 1);
+            cudaError_t e = call_items * p.splits > 2LL * sm_count && kFour ? go(std::integral_constant<bool, kFour>()) : go(std::false_type());
             if (e == cudaSuccess && p.splits > 1) e = join((unsigned)call_items, true);
             return e;
         }
