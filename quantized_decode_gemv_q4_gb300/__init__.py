@@ -375,19 +375,17 @@ class KV4Cache:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t: torch.Tensor, heads: int, D: int, dtype: torch.dtype, dev: int, name: str):
-    """(address, elements from one token to the next) of a tensor of token rows [..., heads, D] on device `dev`."""
+def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, dev: int, name: str):
+    """(address, elements from one token to the next) of token rows [..., heads, D] on device `dev`, width = heads * D (the
+    caller has checked the shape)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on device {dev}, got {t.device}")
-    shape = t.shape
-    if len(shape) < 3 or shape[-1] != D or shape[-2] != heads:
-        raise ValueError(f"{name}: expected [..., {heads}, {D}], got {list(shape)}")
     if t.is_contiguous():
-        return t.data_ptr(), heads * D
-    st = t.stride()
-    if st[-1] != 1 or (heads > 1 and st[-2] != D):
+        return t.data_ptr(), width
+    shape, st = t.shape, t.stride()
+    if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     # token axes must lie evenly: the outer ones follow from the innermost that has more than one token
     step, n = 0, 1
@@ -398,7 +396,7 @@ def _rows(t: torch.Tensor, heads: int, D: int, dtype: torch.dtype, dev: int, nam
             elif s != step * n:
                 raise ValueError(f"{name}: the token rows must be evenly spaced")
             n *= size
-    return t.data_ptr(), step if n > 1 else heads * D
+    return t.data_ptr(), step if n > 1 else width
 
 
 def _flat(t: torch.Tensor, dtype: torch.dtype, dev: int, name: str, numel: int) -> int:
@@ -448,22 +446,25 @@ def qk_norm_rope(q_out, k_out, q, k, q_gamma, k_gamma, cos_sin, positions, eps: 
     rotation). The outputs may be the inputs."""
     code, dev = _act(q, "q")
     shape, k_shape, dt = q.shape, k.shape, q.dtype
-    if len(shape) != 3 or len(k_shape) != 3 or shape[0] != k_shape[0] or shape[2] != k_shape[2]:
-        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
     if q_out.shape != shape or k_out.shape != k_shape:
         raise ValueError("q_out must be [T, Hq, D] and k_out [T, Hkv, D]")
-    T, Hq, D = shape
-    Hkv = k_shape[1]
+    try:
+        T, Hq, D = shape
+        k_T, Hkv, k_D = k_shape
+    except ValueError:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]") from None
+    if T != k_T or D != k_D:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
     max_pos = rot = 0
     table = where = None
     if cos_sin is not None:
         max_pos, rot = cos_sin.shape
         table = _flat(cos_sin, torch.float32, dev, "cos_sin", max_pos * rot)
         where = _flat(positions, torch.int32, dev, "positions", T)
-    qp, qs = _rows(q, Hq, D, dt, dev, "q")
-    kp, ks = _rows(k, Hkv, D, dt, dev, "k")
-    qop, qos = _rows(q_out, Hq, D, dt, dev, "q_out")
-    kop, kos = _rows(k_out, Hkv, D, dt, dev, "k_out")
+    qp, qs = _rows(q, Hq * D, dt, dev, "q")
+    kp, ks = _rows(k, Hkv * D, dt, dev, "k")
+    qop, qos = _rows(q_out, Hq * D, dt, dev, "q_out")
+    kop, kos = _rows(k_out, Hkv * D, dt, dev, "k_out")
     _call(load().qk_norm_rope, dev, qop, kop, qp, kp,
           None if q_gamma is None else _flat(q_gamma, torch.float32, dev, "q_gamma", D),
           None if k_gamma is None else _flat(k_gamma, torch.float32, dev, "k_gamma", D), eps, table, where, T, Hq, Hkv, D, rot,
@@ -475,13 +476,14 @@ def kv4_write(cache: KV4Cache, k, v, slots, stream=None) -> None:
     distinct)."""
     code, dev = _act(k, "k")
     shape, dt, H, D = k.shape, k.dtype, cache.num_kv_heads, cache.head_dim
-    if len(shape) != 3 or v.shape != shape:
-        raise ValueError("k and v must be [T, num_kv_heads, head_dim]")
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or v.shape != shape:
+        raise ValueError(f"k and v must be [T, {H}, {D}], got {list(shape)} and {list(v.shape)}")
     if dev != cache.device.index:
         raise ValueError(f"k: expected a tensor on {cache.device}, got {k.device}")
-    kp, ks = _rows(k, H, D, dt, dev, "k")
-    vp, vs = _rows(v, H, D, dt, dev, "v")
-    _call(load().kv4_write, dev, cache._ref, kp, vp, _flat(slots, torch.int32, dev, "slots", shape[0]), shape[0], ks, vs, code,
+    T = shape[0]
+    kp, ks = _rows(k, H * D, dt, dev, "k")
+    vp, vs = _rows(v, H * D, dt, dev, "v")
+    _call(load().kv4_write, dev, cache._ref, kp, vp, _flat(slots, torch.int32, dev, "slots", T), T, ks, vs, code,
           _stream_on(dev, stream))
 
 
@@ -493,13 +495,14 @@ def kv4_read(k_out, v_out, cache: KV4Cache, slots, stream=None) -> None:
         raise ValueError("k_out and v_out cannot both be None")
     code, dev = _act(first, "k_out" if k_out is not None else "v_out")
     shape, dt, H, D = first.shape, first.dtype, cache.num_kv_heads, cache.head_dim
-    if len(shape) != 3 or (v_out is not None and v_out.shape != shape):
-        raise ValueError("k_out and v_out must be [T, num_kv_heads, head_dim]")
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or (v_out is not None and v_out.shape != shape):
+        raise ValueError(f"k_out and v_out must be [T, {H}, {D}]")
     if dev != cache.device.index:
         raise ValueError(f"k_out: expected a tensor on {cache.device}, got {first.device}")
-    kp, ks = (None, 0) if k_out is None else _rows(k_out, H, D, dt, dev, "k_out")
-    vp, vs = (None, 0) if v_out is None else _rows(v_out, H, D, dt, dev, "v_out")
-    _call(load().kv4_read, dev, kp, vp, cache._ref, _flat(slots, torch.int32, dev, "slots", shape[0]), shape[0], ks, vs, code,
+    T = shape[0]
+    kp, ks = (None, 0) if k_out is None else _rows(k_out, H * D, dt, dev, "k_out")
+    vp, vs = (None, 0) if v_out is None else _rows(v_out, H * D, dt, dev, "v_out")
+    _call(load().kv4_read, dev, kp, vp, cache._ref, _flat(slots, torch.int32, dev, "slots", T), T, ks, vs, code,
           _stream_on(dev, stream))
 
 
@@ -530,15 +533,15 @@ def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float |
         M = 1
     else:
         raise ValueError("q must be [B, M, Hq, D] or [B, Hq, D]")
-    if out.shape != shape:
-        raise ValueError("out must have q's shape")
+    if out.shape != shape or shape[-1] != D:
+        raise ValueError(f"q and out must be [B, M, Hq, {D}] or [B, Hq, {D}], got {list(shape)} and {list(out.shape)}")
     if dev != cache.device.index:
         raise ValueError(f"q: expected a tensor on {cache.device}, got {q.device}")
     table_shape = block_table.shape
     if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    qp, qs = _rows(q, Hq, D, dt, dev, "q")
-    op, os_ = _rows(out, Hq, D, dt, dev, "out")
+    qp, qs = _rows(q, Hq * D, dt, dev, "q")
+    op, os_ = _rows(out, Hq * D, dt, dev, "out")
     if workspace is None:
         # on the stream that uses it, so that the allocator hands it on only to work behind this call
         s = torch.cuda.current_stream(dev) if stream is None else (

@@ -375,34 +375,31 @@ struct Rows {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 8; ++j) sc[n][j] = 0.f;
-        constexpr int KB = 1;  // blocks at a time
 #pragma unroll
-        for (int kk = 0; kk < DB; kk += KB) {
-            uint32_t x[4 * KB][4];
+        for (int k = 0; k < DB; ++k) {
+            uint32_t x[4][4];
 #pragma unroll
-            for (int j = 0; j < 4 * KB; ++j) codes_of(kw[kk + j / 4][j % 4], k1024, x[j]);
+            for (int j = 0; j < 4; ++j) codes_of(kw[k][j], k1024, x[j]);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                float c[4 * KB][4];
-                uint32_t q[KB][2][4];
+                float c[4][4], kd[8];
+                uint32_t q[2][4];
 #pragma unroll
-                for (int k = 0; k < KB; ++k)
+                for (int i = 0; i < 2; ++i) lds_words<4>(queries + (uint32_t)(((mt * DB + k) * 2 + i) * 512), q[i]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) lds_words<4>(queries + (uint32_t)(((mt * DB + kk + k) * 2 + i) * 512), q[k][i]);
+                for (int j = 0; j < 4; ++j) mma(c[j], q[0], x[j][0], x[j][1], zero);
 #pragma unroll
-                for (int j = 0; j < 4 * KB; ++j) mma(c[j], q[j / 4][0], x[j][0], x[j][1], zero);
+                for (int j = 0; j < 4; ++j) mma(c[j], q[1], x[j][2], x[j][3], c[j]);
+                lds_floats(scales + (uint32_t)(128 * k), kd);
+                __syncwarp();  // keeps the blocks' instructions apart: without it registers spill (B = 64 ragged 77 us, not 74)
 #pragma unroll
-                for (int j = 0; j < 4 * KB; ++j) mma(c[j], q[j / 4][1], x[j][2], x[j][3], c[j]);
-                float kd[KB][8];
-#pragma unroll
-                for (int k = 0; k < KB; ++k) lds_floats(scales + (uint32_t)(128 * (kk + k)), kd[k]);
-#pragma unroll
-                for (int jj = 0; jj < 4 * KB; ++jj) {
-                    const int j = jj % 4;
-                    const float2 d = make_float2(kd[jj / 4][2 * j], kd[jj / 4][2 * j + 1]);
-                    if constexpr (SPLIT) {
-                        const float2 both = fadd2(make_float2(c[jj][0], c[jj][1]), make_float2(c[jj][2], c[jj][3]));
+                for (int j = 0; j < 4; ++j) {
+                    const float2 d = make_float2(kd[2 * j], kd[2 * j + 1]);
+                    // (where 16-bit queries leave rows 8 .. 15 empty this adds zeros; taking the first half alone makes the
+                    // compiler spill: 64 sequences of 1000 tokens 35 us, not 26)
+                    if constexpr (SPLIT || NT == 1) {
+                        const float2 both = fadd2(make_float2(c[j][0], c[j][1]), make_float2(c[j][2], c[j][3]));
                         const float2 y = ffma2(both, d, make_float2(sc[mt][2 * j], sc[mt][2 * j + 1]));
                         sc[mt][2 * j] = y.x, sc[mt][2 * j + 1] = y.y;
                     } else {
@@ -410,7 +407,7 @@ struct Rows {
                         for (int u = 0; u < 2; ++u) {
                             const int n = 2 * mt + u;
                             if (n < NT) {
-                                const float2 y = ffma2(make_float2(c[jj][2 * u], c[jj][2 * u + 1]), d,
+                                const float2 y = ffma2(make_float2(c[j][2 * u], c[j][2 * u + 1]), d,
                                                        make_float2(sc[n][2 * j], sc[n][2 * j + 1]));
                                 sc[n][2 * j] = y.x, sc[n][2 * j + 1] = y.y;
                             }

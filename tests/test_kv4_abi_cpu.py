@@ -127,13 +127,13 @@ def test_the_binding_refuses_before_it_calls():
 
 
 def test_token_rows():
-    rows = lambda t, H, D: q4._rows(t, H, D, torch.float32, -1, "t")[1]  # noqa: E731
+    rows = lambda t: q4._rows(t, t.shape[-2] * t.shape[-1], torch.float32, -1, "t")[1]  # noqa: E731
     base = torch.zeros(4, 3, 10, 32)
-    assert rows(base, 10, 32) == 320 and rows(base[:, :, 2:7], 5, 32) == 320
-    assert rows(base[:, :1], 10, 32) == 960 and rows(base[:1, :1], 10, 32) == 320
-    assert rows(base[0], 10, 32) == 320 and rows(base[:, 0, :4], 4, 32) == 960
+    assert rows(base) == 320 and rows(base[:, :, 2:7]) == 320
+    assert rows(base[:, :1]) == 960 and rows(base[:1, :1]) == 320
+    assert rows(base[0]) == 320 and rows(base[:, 0, :4]) == 960
     for bad in (base[:, :2], base[..., ::2, :], base.transpose(-1, -2), base[..., :16]):
         with pytest.raises(ValueError):
-            rows(bad, bad.shape[-2], bad.shape[-1] if bad.shape[-1] != 16 else 32)
+            rows(bad)
     with pytest.raises(TypeError):
-        q4._rows(base, 10, 32, torch.float16, -1, "t")
+        q4._rows(base, 320, torch.float16, -1, "t")
