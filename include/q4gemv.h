@@ -208,7 +208,7 @@ enum { Q4_F32 = 0, Q4_F16 = 1, Q4_BF16 = 2 };
  *   q, q_out [T][Hq][D], k, k_out [T][Hkv][D]; an output may be its input (same pointer and stride) or must not overlap
  *   any input; q_gamma, k_gamma float[D] or NULL; cos_sin float[max_pos][rot_dim]: row p holds cos for the rot_dim / 2
  *   pairs, then sin; positions int32[T] (device). gamma and cos_sin 16-byte aligned.
- *   D a multiple of 32 up to 256; rot_dim a multiple of 16, 0..D (0: no rotation, cos_sin and positions unused).
+ *   D a multiple of 32 up to 256; T * (Hq + Hkv) < 2^31; rot_dim a multiple of 16, 0..D (0: no rotation, cos_sin and positions unused).
  *   A token whose position is outside [0, max_pos) gets NaN heads and Q4_FAULT_BAD_POSITION is recorded.
  */
 int qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k, const float *q_gamma, const float *k_gamma,
@@ -237,7 +237,7 @@ typedef struct {
  *   d = binary16(min(max|x| / 7, 65504)), code = 8 + clamp(nearest(x / d), -7, 7) with ties to even (d = 0: codes 8);
  *   the nearest is exact, so equal inputs give equal bytes whatever the type they come in. A block that holds a NaN or
  *   an infinity is stored as d = NaN, codes 8 (it reads back as NaN).
- *   k, v [T][num_kv_heads][head_dim]; slots int32[T] (device). A token whose slot is negative is skipped; one whose slot
+ *   k, v [T][num_kv_heads][head_dim], T <= 2^30; slots int32[T] (device). A token whose slot is negative is skipped; one whose slot
  *   is past the cache is skipped and Q4_FAULT_BAD_SLOT recorded. The slots >= 0 of one call must be distinct (a slot
  *   given twice ends up with a mixture of the two rows).
  * kv4_read: the rows at T slots as values (code - 8) * d.
@@ -259,7 +259,7 @@ int kv4_read(void *k_out, void *v_out, const kv4_cache *cache, const int32_t *sl
  * are not read, and what a query does not see does not enter its result, whatever bits it holds.
  *   q, out [B*M][Hq][head_dim] (token rows with strides as above); lse float[B*M][Hq]; block_table
  *   int32[B][max_pages], seq_lens int32[B] (device). 1 <= M <= 16; 1 <= B <= 1024; head_dim 64, 128 or 256;
- *   Hq a multiple of num_kv_heads; scale finite and > 0; max_pages * page_size <= 2^30.
+ *   Hq a multiple of num_kv_heads; 0 < scale <= 1e30; max_pages * page_size <= 2^30.
  *   A sequence whose length is outside [0, max_pages * page_size], or that reads a page id outside [0, num_pages), gets
  *   NaN rows, and Q4_FAULT_BAD_LENGTH or Q4_FAULT_BAD_PAGE is recorded. A query row that holds a NaN or an infinity
  *   gives NaN.

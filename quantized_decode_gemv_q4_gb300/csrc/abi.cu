@@ -452,7 +452,7 @@ int kv4_write(const kv4_cache* cache, const void* k, const void* v, const int32_
               long long v_stride, int dtype, q4_stream_t stream) {
     const char* what = "kv4_write";
     Q4_TRY(check_cache(what, cache));
-    if (T <= 0) return fail(Q4_EINVAL, "%s: T must be >= 1 (got %d)", what, T);
+    if (T <= 0 || T > (1 << 30)) return fail(Q4_EINVAL, "%s: T must be in 1..2^30 (got %d)", what, T);
     Q4_TRY(check_dtype(what, dtype));
     const long long width = (long long)cache->num_kv_heads * cache->head_dim;
     Q4_TRY(check_rows(what, "k", k, k_stride, width, dtype));
@@ -468,7 +468,7 @@ int kv4_read(void* k_out, void* v_out, const kv4_cache* cache, const int32_t* sl
              long long v_stride, int dtype, q4_stream_t stream) {
     const char* what = "kv4_read";
     Q4_TRY(check_cache(what, cache));
-    if (T <= 0) return fail(Q4_EINVAL, "%s: T must be >= 1 (got %d)", what, T);
+    if (T <= 0 || T > (1 << 30)) return fail(Q4_EINVAL, "%s: T must be in 1..2^30 (got %d)", what, T);
     Q4_TRY(check_dtype(what, dtype));
     if (!k_out && !v_out) return fail(Q4_EINVAL, "%s: null k_out and v_out", what);
     const long long width = (long long)cache->num_kv_heads * cache->head_dim;
@@ -518,8 +518,9 @@ int kv4_attention(void* out, float* lse, const void* q, const kv4_cache* cache, 
     Q4_TRY(check_index(what, "seq_lens", seq_lens));
     if (max_pages <= 0 || (long long)max_pages * cache->page_size > (1LL << 30))
         return fail(Q4_EINVAL, "%s: max_pages must be >= 1 and hold up to 2^30 tokens (got %d)", what, max_pages);
-    if (!(scale > 0.f) || !std::isfinite(scale)) return fail(Q4_EINVAL, "%s: scale must be finite and > 0", what);
+    if (!(scale > 0.f) || !(scale <= 1e30f)) return fail(Q4_EINVAL, "%s: scale must be > 0 and at most 1e30", what);
     if (window < 0) return fail(Q4_EINVAL, "%s: window must be >= 0 (got %d)", what, window);
+    if ((long long)window >= (long long)max_pages * cache->page_size) window = 0;  // it reaches past every sequence
     DeviceInfo di;
     KvAttnArgs a = {*cache, out, lse, q, block_table, seq_lens, B, M, Hq, max_pages, q_stride, out_stride, scale, window,
                     dtype, nullptr};

@@ -199,6 +199,25 @@ def test_bad_pages_and_lengths_are_recorded(spare):
     c.check(out, lse, rows=[1, 3])
 
 
+@pytest.mark.parametrize("spare", [1, 800])
+def test_windows_past_every_sequence_are_none(spare):
+    c = Case([1, 40, 0, 9], 16, 2, 1, 64, 16, F32, spare=spare)
+    out, lse = c.run()
+    c.check(out, lse)
+    for window in (c.table.shape[1] * c.page, 2 ** 30, 2 ** 31 - 1):
+        c.window = window
+        again, lse2 = c.run()
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+def test_many_heads_and_rows():
+    """More query heads than a CTA's rows many times over, and a key head for each query head."""
+    c = Case([70, 3], 2, 192, 2, 64, 16, BF16)
+    c.check(*c.run())
+    c = Case([45], 1, 96, 96, 64, 16, F16)
+    c.check(*c.run())
+
+
 def test_strided_queries_and_one_token_form():
     c = Case([130, 7], 1, 8, 2, 64, 16, BF16)
     out, _ = c.run()

@@ -55,7 +55,7 @@ def refused(lib, name, base, code, text, **kw):
 def test_rope_refusals(lib):
     for kw, code, text in [
             (dict(q=None), q4.Q4_EINVAL, "null q"), (dict(k_out=None), q4.Q4_EINVAL, "null k_out"),
-            (dict(T=0), q4.Q4_EINVAL, "T must"), (dict(D=48), q4.Q4_EINVAL, "multiple of 32"),
+            (dict(T=0), q4.Q4_EINVAL, "T must"), (dict(T=1 << 30), q4.Q4_EINVAL, "2^31-1"), (dict(D=48), q4.Q4_EINVAL, "multiple of 32"),
             (dict(D=288, qs=2000, ks=2000, qos=2000, kos=2000), q4.Q4_EINVAL, "up to 256"),
             (dict(Hq=0), q4.Q4_EINVAL, "heads"), (dict(Hkv=0), q4.Q4_EINVAL, "key heads"),
             (dict(Hq=70000), q4.Q4_EINVAL, "heads"), (dict(rot=24), q4.Q4_EINVAL, "multiple of 16"),
@@ -82,6 +82,7 @@ def test_cache_refusals(lib):
             refused(lib, name, base, code, text, cache=cache(**kw))
     for name, base in (("kv4_write", WRITE), ("kv4_read", READ)):
         refused(lib, name, base, q4.Q4_EINVAL, "T must", T=0)
+        refused(lib, name, base, q4.Q4_EINVAL, "T must", T=(1 << 30) + 1)
         refused(lib, name, base, q4.Q4_EINVAL, "null slots", slots=None)
         refused(lib, name, base, q4.Q4_EALIGN, "slots", slots=A + 2)
         refused(lib, name, base, q4.Q4_EINVAL, "token stride", ks=127)
@@ -98,7 +99,7 @@ def test_attention_refusals(lib):
             (dict(Hq=5), q4.Q4_EINVAL, "multiple of the key heads"), (dict(Hq=0), q4.Q4_EINVAL, "multiple of the key heads"),
             (dict(max_pages=0), q4.Q4_EINVAL, "max_pages"), (dict(max_pages=1 << 28), q4.Q4_EINVAL, "2^30"),
             (dict(scale=0.0), q4.Q4_EINVAL, "scale"), (dict(scale=float("inf")), q4.Q4_EINVAL, "scale"),
-            (dict(scale=float("nan")), q4.Q4_EINVAL, "scale"), (dict(window=-1), q4.Q4_EINVAL, "window"),
+            (dict(scale=float("nan")), q4.Q4_EINVAL, "scale"), (dict(scale=2e30), q4.Q4_EINVAL, "scale"), (dict(window=-1), q4.Q4_EINVAL, "window"),
             (dict(q=None), q4.Q4_EINVAL, "null q"), (dict(out=None), q4.Q4_EINVAL, "null out"),
             (dict(out=A + 8), q4.Q4_EALIGN, "row of out"), (dict(lse=A + 2), q4.Q4_EALIGN, "lse"),
             (dict(table=None), q4.Q4_EINVAL, "null block_table"), (dict(lens=None), q4.Q4_EINVAL, "null seq_lens"),
