@@ -180,6 +180,19 @@ __global__ void __launch_bounds__(kMaxThreads) kv4_write_kernel(const KvRowsArgs
     }
 }
 
+// The four low and four high elements of a word of codes. A code at bits p .. p + 3 (p <= 16) under the pattern of 2^23 is
+// 2^23 + code * 2^p, so a difference leaves (code - 8) * 2^p exactly and a product with d * 2^-p, exact as well (15 bits),
+// the value: no shift and no conversion from integers, which cost the reader more than its bytes did.
+__device__ __forceinline__ void value_words(uint32_t w, float d, float* lo, float* hi) {
+    const uint32_t s = w >> 12;
+    auto value = [&](uint32_t v, int p) {
+        const float x = __uint_as_float((v & (15u << p)) | 0x4B000000u) - (8388608.f + (float)(8 << p));
+        return x * (d * __int_as_float((127 - p) << 23));
+    };
+    lo[0] = value(w, 0), lo[1] = value(w, 8), lo[2] = value(w, 16), lo[3] = value(s, 12);
+    hi[0] = value(w, 4), hi[1] = value(w, 12), hi[2] = value(s, 8), hi[3] = value(s, 16);
+}
+
 template <typename T, int U>
 __global__ void __launch_bounds__(kMaxThreads) kv4_read_kernel(const KvRowsArgs p) {
     const int pieces = p.c.num_kv_heads * p.c.head_dim / 8;
@@ -210,12 +223,8 @@ __global__ void __launch_bounds__(kMaxThreads) kv4_read_kernel(const KvRowsArgs 
         for (int i = 0; i < U; ++i) {
             if (slot[i] < 0) continue;
             float lo[8], hi[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t c = ((j < 4 ? w[i].x : w[i].y) >> (8 * (j % 4))) & 255u;
-                lo[j] = (float)((int)(c & 15u) - 8) * d[i];
-                hi[j] = (float)((int)(c >> 4) - 8) * d[i];
-            }
+            value_words(w[i].x, d[i], &lo[0], &hi[0]);
+            value_words(w[i].y, d[i], &lo[4], &hi[4]);
             store_floats(dst + (t0 + i) * stride, lo);
             store_floats(dst + (t0 + i) * stride + 16, hi);
         }
