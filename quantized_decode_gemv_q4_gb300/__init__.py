@@ -373,6 +373,7 @@ class KV4Cache:
 # These calls take a few microseconds on the device, so the checks below are written to cost the host as little: one
 # pass over each tensor's properties, and the stream's handle without a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, dev: int, name: str):
@@ -385,6 +386,8 @@ def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, dev: int, name: str):
     if t.is_contiguous():
         return t.data_ptr(), width
     shape, st = t.shape, t.stride()
+    if len(st) == 3 and st[2] == 1 and st[1] == shape[2]:  # columns of a wider tensor
+        return t.data_ptr(), st[0]
     if st[-1] != 1 or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     # token axes must lie evenly: the outer ones follow from the innermost that has more than one token
@@ -430,7 +433,7 @@ def _stream_on(dev: int, stream) -> int:
 
 def _call(fn, dev: int, *args) -> None:
     """Call a C entry with the tensors' device current."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
