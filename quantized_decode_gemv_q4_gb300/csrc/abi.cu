@@ -532,7 +532,7 @@ int kv4_attention(void* out, float* lse, const void* q, const kv4_cache* cache, 
         if (workspace_bytes < need)
             return fail(Q4_EINVAL, "%s: the workspace holds %zu bytes, %zu are needed", what, workspace_bytes, need);
     }
-    return finish(what, launch_kv4_attention(a, workspace, di.sm_count, (cudaStream_t)stream));
+    return finish(what, launch_kv4_attention(a, workspace, di, (cudaStream_t)stream));
 }
 
 const char* q4_last_error(void) { return g_last_error.c_str(); }

@@ -26,6 +26,7 @@
 //     the outputs of items that it holds whole, and parts of the others, which a second kernel joins in a fixed order.
 //   - whole items: one CTA per item, its warps' tiles interleaved and joined through shared memory; one launch.
 #include <algorithm>
+#include <atomic>
 
 #include "kv_common.cuh"
 
@@ -1049,11 +1050,16 @@ auto with_plan(int D, int nt, bool split, F fn) {
     return by_split(std::integral_constant<int, 8>(), one());
 }
 
-template <typename Kernel>
-cudaError_t launch_with_ring(Kernel kernel, dim3 grid, int threads, uint32_t ring, cudaStream_t s, const Params& p) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
-    if (e == cudaSuccess) e = launch_grid(kernel, grid, dim3((unsigned)threads), ring, s, launch_overlap(), p);
-    return e;
+// Launches a kernel with `ring` bytes of dynamic shared memory, which it is allowed once on each device.
+template <auto kKernel>
+cudaError_t launch_with_ring(dim3 grid, int threads, uint32_t ring, const DeviceInfo& di, cudaStream_t s, const Params& p) {
+    static std::atomic<bool> allowed[64];
+    if (!allowed[di.device & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+        if (e != cudaSuccess) return e;
+        allowed[di.device & 63].store(true, std::memory_order_relaxed);
+    }
+    return launch_grid(kKernel, grid, dim3((unsigned)threads), ring, s, launch_overlap(), p);
 }
 
 }  // namespace
@@ -1068,7 +1074,8 @@ size_t kv4_attention_workspace_bytes(int M, int group, int heads, int D, int dty
     });
 }
 
-cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_count, cudaStream_t s) {
+cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, const DeviceInfo& di, cudaStream_t s) {
+    const int sm_count = di.sm_count;
     const int group = a.Hq / a.c.num_kv_heads, nt = row_groups(a.M, group, a.c.head_dim);
     return with_plan(a.c.head_dim, nt, a.dtype == Q4_F32, [&](auto db, auto n, auto split) {
         constexpr int DB = decltype(db)::value, NT = decltype(n)::value;
@@ -1101,8 +1108,8 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
                 constexpr int kWarpBytes = ItemPlan<DB, NT, SPLIT, MANY>::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries;
                 constexpr int kRing = kItemWarps * kWarpBytes;
                 static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
-                return launch_with_ring(kv4_attention_items_kernel<DB, NT, SPLIT, MANY>, dim3((unsigned)(items * p.splits), (unsigned)a.B),
-                                        kItemWarps * 32, kRing, s, p);
+                return launch_with_ring<kv4_attention_items_kernel<DB, NT, SPLIT, MANY>>(
+                    dim3((unsigned)(items * p.splits), (unsigned)a.B), kItemWarps * 32, kRing, di, s, p);
             };
             // more CTAs than two an SM: four of them fit where 128 registers do
             constexpr bool kFour = DB == 2 || (DB == 4 && NT == 1);
@@ -1110,8 +1117,8 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_co
             if (e == cudaSuccess && p.splits > 1) e = join((unsigned)call_items, true);
             return e;
         }
-        cudaError_t e = launch_with_ring(kv4_attention_streams_kernel<DB, NT, SPLIT>, dim3((unsigned)sm_count), L::kWarps * 32,
-                                         L::kWarps * (L::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries), s, p);
+        cudaError_t e = launch_with_ring<kv4_attention_streams_kernel<DB, NT, SPLIT>>(
+            dim3((unsigned)sm_count), L::kWarps * 32, L::kWarps * (L::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries), di, s, p);
         if (e == cudaSuccess) e = join((unsigned)call_items, call_items <= 64);
         return e;
     });

@@ -64,6 +64,6 @@ struct KvAttnArgs {
 };
 // Bytes of workspace that launch_kv4_attention needs for these sizes on a device of sm_count SMs.
 size_t kv4_attention_workspace_bytes(int M, int group, int heads, int D, int dtype, int sm_count);
-cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, int sm_count, cudaStream_t s);
+cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, const DeviceInfo& di, cudaStream_t s);
 
 }  // namespace q4
