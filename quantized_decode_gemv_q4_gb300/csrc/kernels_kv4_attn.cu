@@ -37,7 +37,6 @@ namespace {
 constexpr int kTile = 32;       // tokens a warp takes at a time
 constexpr int kMaxB = 1024;     // sequences of a call
 constexpr int kItemCost = 4;    // what starting on an item costs a streaming warp, in tiles
-constexpr int kItemWarps = 4;   // warps of a CTA that takes whole items
 
 template <int DB>
 struct Geo {
@@ -56,10 +55,12 @@ struct Plan {  // streams
     static constexpr int kWarps = kTwelve ? 12 : 8;  // warps of an SM, all in one CTA
     static constexpr int kStages = DB == 2 ? 5 : DB == 4 && NT == 1 ? 3 : DB == 4 ? 4 : 2;
 };
-template <int DB, int NT, bool SPLIT, bool MANY>
-struct ItemPlan {  // items: MANY CTAs, which hide each other's starts, or few
-    static constexpr int kCtas = MANY ? 4 : 2;  // CTAs of an SM
-    static constexpr int kStages = MANY ? (DB == 2 ? 4 : 2) : DB == 8 ? 2 : 4;
+enum : int { kFew, kMany, kCrowd };  // CTAs of an items launch
+template <int DB, int NT, bool SPLIT, int COUNT>
+struct ItemPlan {  // items: CTAs that hide each other's starts, or few; a crowd has one start a warp less
+    static constexpr int kWarps = COUNT == kCrowd ? 2 : 4;                   // warps of a CTA
+    static constexpr int kCtas = COUNT == kFew ? 2 : COUNT == kMany ? 4 : 8;  // CTAs of an SM
+    static constexpr int kStages = COUNT != kFew ? (DB == 2 ? 4 : 2) : DB == 8 ? 2 : 4;
 };
 
 struct Params {
@@ -622,11 +623,12 @@ struct Lookup {
 // Whole items
 // ------------------------------------------------------------------------------------------------
 
-template <int DB, int NT, bool SPLIT, bool MANY>
-__global__ void __launch_bounds__(kItemWarps * 32, ItemPlan<DB, NT, SPLIT, MANY>::kCtas) kv4_attention_items_kernel(const Params p) {
+template <int DB, int NT, bool SPLIT, int COUNT>
+__global__ void __launch_bounds__(ItemPlan<DB, NT, SPLIT, COUNT>::kWarps * 32, ItemPlan<DB, NT, SPLIT, COUNT>::kCtas)
+kv4_attention_items_kernel(const Params p) {
     using G = Geo<DB>;
-    using L = ItemPlan<DB, NT, SPLIT, MANY>;
-    constexpr int D = G::D, ROWS = 8 * NT;
+    using L = ItemPlan<DB, NT, SPLIT, COUNT>;
+    constexpr int D = G::D, ROWS = 8 * NT, kItemWarps = L::kWarps;
     extern __shared__ __align__(128) unsigned char ring_memory[];
     __shared__ float join_ref[kItemWarps][ROWS], join_l[kItemWarps][ROWS];
     const KvAttnArgs& a = p.a;
@@ -1102,18 +1104,24 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, const Dev
         const long long most = (long long)a.max_pages * a.c.page_size, call_items = (long long)items * a.B;
         if (most <= kItemTokens || a.B == 1 || (most <= kSplitTokens && call_items <= sm_count)) {
             p.warps = 0;
-            p.splits = (int)std::max(1LL, std::min(2LL * sm_count / call_items, most / (2 * kTile * kItemWarps)));
-            auto go = [&](auto many) {
-                constexpr bool MANY = decltype(many)::value;
-                constexpr int kWarpBytes = ItemPlan<DB, NT, SPLIT, MANY>::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries;
-                constexpr int kRing = kItemWarps * kWarpBytes;
-                static_assert(kRing >= kItemWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
-                return launch_with_ring<kv4_attention_items_kernel<DB, NT, SPLIT, MANY>>(
-                    dim3((unsigned)(items * p.splits), (unsigned)a.B), kItemWarps * 32, kRing, di, s, p);
+            p.splits = (int)std::max(1LL, std::min(2LL * sm_count / call_items, most / (8 * kTile)));
+            auto go = [&](auto count) {
+                constexpr int COUNT = decltype(count)::value;
+                using I = ItemPlan<DB, NT, SPLIT, COUNT>;
+                constexpr int kRing = I::kWarps * (I::kStages * G::kStage + (int)Rows<DB, NT, SPLIT>::kQueries);
+                static_assert(kRing >= I::kWarps * 8 * NT * G::kJoinRow * 4, "the join must fit in the rings");
+                return launch_with_ring<kv4_attention_items_kernel<DB, NT, SPLIT, COUNT>>(
+                    dim3((unsigned)(items * p.splits), (unsigned)a.B), I::kWarps * 32, kRing, di, s, p);
             };
-            // more CTAs than two an SM: four of them fit where 128 registers do
+            // more CTAs than two an SM run in kMany where 128 registers do; from eight an SM on, CTAs of two warps take over,
+            // each warp with twice the tiles and half the starts: 256 sequences of 64 tokens 22 and 15 us, of 300 tokens 33 and
+            // 28 us, but 64 sequences of 200 tokens 10 and 11 us (8 key heads of 128, bf16)
             constexpr bool kFour = DB == 2 || (DB == 4 && NT == 1);
-            cudaError_t e = call_items * p.splits > 2LL * sm_count && kFour ? go(std::integral_constant<bool, kFour>()) : go(std::false_type());
+            const long long ctas = call_items * p.splits;
+            cudaError_t e;
+            if (kFour && ctas >= 8LL * sm_count) e = go(std::integral_constant<int, kFour ? kCrowd : kFew>());
+            else if (kFour && ctas > 2LL * sm_count) e = go(std::integral_constant<int, kFour ? kMany : kFew>());
+            else e = go(std::integral_constant<int, kFew>());
             if (e == cudaSuccess && p.splits > 1) e = join((unsigned)call_items, true);
             return e;
         }

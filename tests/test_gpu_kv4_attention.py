@@ -113,6 +113,19 @@ def test_many_sequences_of_all_lengths(dtype, spare):
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,M,Hq,Hkv,D", [(120, 1, 12, 4, 128), (330, 1, 8, 4, 128), (200, 3, 12, 3, 64), (410, 2, 6, 3, 64),
+                                          (160, 1, 8, 8, 256)])
+def test_many_and_crowded_items(B, M, Hq, Hkv, D, dtype):
+    """Hundreds to thousands of (sequence, key head) items of short sequences, in whole items and as streams."""
+    c = Case([(i * 13) % 90 for i in range(B)], M, Hq, Hkv, D, 16, dtype)
+    out, lse = c.run()
+    c.check(out, lse)
+    c.table = np.concatenate([c.table, np.full((B, 600), 2 ** 30, np.int32)], 1)
+    c.upload()
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("spare", [1, 100, 800])
 def test_the_most_sequences(spare):
     c = Case([(i * 7) % 40 for i in range(1024)], 1, 2, 1, 64, 16, F32, spare=spare)
