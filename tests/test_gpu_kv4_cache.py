@@ -115,6 +115,33 @@ def test_a_million_values_round_as_in_64_bits():
     roundtrip(torch.from_numpy(x).cuda(), torch.from_numpy(x[::-1].copy() * 1e-3).cuda(), list(range(1024)), 64, 16)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,H,D,page", [(8211, 8, 128, 16), (33001, 1, 256, 64), (5003, 21, 96, 4)])
+def test_many_rows(dtype, T, H, D, page):
+    """Enough rows for several tokens a thread, a last group that is not full, some without a slot."""
+    rng = np.random.default_rng(T)
+    pages = -(-T // page) + 1
+    slots = rng.permutation(pages * page)[:T]
+    slots[rng.integers(0, T, 50)] = -1
+    kv = torch.from_numpy(rng.standard_normal((T, 2 * H, D)).astype(np.float32)).to(dtype).cuda()
+    cache = junk_cache(pages, page, H, D)
+    before = host(cache)
+    sl = torch.from_numpy(slots.astype(np.int32)).cuda()
+    q4.kv4_write(cache, kv[:, :H], kv[:, H:], sl)
+    got, there = host(cache), slots >= 0
+    pg, of = slots[there] // page, slots[there] % page
+    outs = [torch.full((T, H, D), 9.0, dtype=dtype, device="cuda") for _ in range(2)]
+    q4.kv4_read(*outs, cache, sl)
+    for x, qs, d, was_qs, was_d, out in ((kv[:, :H], got[0], got[1], before[0], before[1], outs[0]),
+                                         (kv[:, H:], got[2], got[3], before[2], before[3], outs[1])):
+        c, s = ref.quantise(x.double().cpu().numpy()[there])
+        was_qs[pg, :, of], was_d[pg, :, of] = c, s
+        assert np.array_equal(qs, was_qs) and same_halves(d, was_d)
+        want = torch.full((T, H, D), 9.0, dtype=dtype)
+        want[torch.from_numpy(there)] = torch.from_numpy(ref.values(c, s)).float().to(dtype)
+        assert torch.equal(out.cpu(), want)
+
+
 def test_bad_slots_are_recorded_and_written_nowhere():
     H, D, page, pages = 2, 64, 8, 3
     k = torch.randn(4, H, D, device="cuda")

@@ -36,7 +36,8 @@ def check(got, x, gamma, eps, cs, pos, inter, dtype, what):
     (1, 28, 4, 128, 128, False, True), (3, 4, 4, 64, 64, True, True), (5, 7, 1, 96, 96, False, True),
     (2, 3, 1, 32, 16, True, True), (7, 8, 2, 256, 256, False, True), (4, 6, 3, 160, 80, False, False),
     (33, 40, 8, 128, 64, True, False), (2, 5, 5, 192, 176, False, True), (600, 2, 1, 64, 32, False, True),
-    (3, 2, 1, 224, 224, True, True)])
+    (3, 2, 1, 224, 224, True, True),
+    (4099, 28, 6, 128, 128, False, True), (5001, 9, 3, 256, 64, True, True), (12345, 13, 1, 64, 64, False, False)])  # many rows
 def test_matches_the_formula(dtype, T, Hq, Hkv, D, rot, inter, norm):
     g = torch.Generator().manual_seed(T * 1000 + D + rot)
     qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g).to(dtype).cuda()
