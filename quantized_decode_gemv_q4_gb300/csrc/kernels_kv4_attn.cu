@@ -48,19 +48,21 @@ struct Geo {
     static constexpr int kJoinRow = D + 4;                 // floats; the pad spreads the joining stores over the banks
 };
 
-// Warps and stages (tiles of a warp in flight or in use), by registers and shared memory.
+// Warps and stages (tiles of a warp in flight or in use), by registers and shared memory: on an SM 8 warps of up to 255
+// registers, 12 of 168 or 16 of 128.
 template <int DB, int NT, bool SPLIT>
 struct Plan {  // streams
-    static constexpr bool kTwelve = DB == 2 || (DB == 4 && NT == 1);
-    static constexpr int kWarps = kTwelve ? 12 : 8;  // warps of an SM, all in one CTA
-    static constexpr int kStages = DB == 2 ? 5 : DB == 4 && NT == 1 ? 3 : DB == 4 ? 4 : 2;
+    static constexpr bool kSixteen = DB == 4 && NT == 1 && !SPLIT, kTwelve = DB == 2 || (DB == 4 && NT == 1);
+    static constexpr int kWarps = kSixteen ? 16 : kTwelve ? 12 : 8;  // warps of an SM, all in one CTA
+    static constexpr int kStages = kSixteen ? 2 : DB == 2 ? 5 : DB == 4 && NT == 1 ? 3 : DB == 4 ? 4 : 2;
 };
 enum : int { kFew, kMany, kCrowd };  // CTAs of an items launch
 template <int DB, int NT, bool SPLIT, int COUNT>
 struct ItemPlan {  // items: CTAs that hide each other's starts, or few; a crowd has one start a warp less
-    static constexpr int kWarps = COUNT == kCrowd ? 2 : 4;                   // warps of a CTA
+    static constexpr bool kSix = COUNT == kFew && DB <= 4 && NT == 1 && !SPLIT;
+    static constexpr int kWarps = COUNT == kCrowd ? 2 : kSix ? 6 : 4;        // warps of a CTA
     static constexpr int kCtas = COUNT == kFew ? 2 : COUNT == kMany ? 4 : 8;  // CTAs of an SM
-    static constexpr int kStages = COUNT != kFew ? (DB == 2 ? 4 : 2) : DB == 8 ? 2 : 4;
+    static constexpr int kStages = COUNT != kFew ? (DB == 2 ? 4 : 2) : DB == 8 ? 2 : kSix ? 3 : 4;
 };
 
 struct Params {
@@ -113,6 +115,15 @@ __device__ __forceinline__ void lds_floats(uint32_t addr, float (&x)[8]) {
                      : "r"(addr + 4u * i)
                      : "memory");
 }
+__device__ __forceinline__ void lds_floats4(uint32_t addr, float (&x)[4]) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(addr) : "memory");
+}
+// An 8 x 8 matrix of halves, a row's pair of columns in each lane, transposed.
+__device__ __forceinline__ uint32_t turned_over(uint32_t w) {
+    uint32_t x;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(x) : "r"(w));
+    return x;
+}
 __device__ __forceinline__ void sts_word(uint32_t addr, uint32_t w) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
 }
@@ -141,10 +152,20 @@ __device__ __forceinline__ void lds_own(uint32_t addr, uint32_t (&w)[WORDS]) {
     else lds_words<WORDS>(addr, w);
 }
 
-// Token t of a tile lies in row place(t) of its stage: matrix j of ldmatrix reads rows 8 j .. 8 j + 7, and column c of it
-// becomes token 8 (c / 2) + 2 j + c % 2, so that a lane's eight tokens (columns 2 t4 and 2 t4 + 1 of four matrices) are
-// the consecutive ones 8 t4 .. 8 t4 + 7.
-__device__ __forceinline__ int place(int t) { return 8 * (t >> 1 & 3) + 2 * (t >> 3) + (t & 1); }
+// Token t of a tile lies in row place(t) of its stage; lane l of an ldmatrix gives the address of row l % 8 of matrix l / 8,
+// which is row row_of_lane(l).
+//   Tokens along columns: column c of matrix j is token 8 (c / 2) + 2 j + c % 2, so that a lane's eight tokens (columns
+//   2 t4 and 2 t4 + 1 of four matrices) are the consecutive ones 8 t4 .. 8 t4 + 7.
+//   Tokens along rows (KT): row i of matrix j is token 4 i + j, a lane's four tokens are 4 g .. 4 g + 3. (The exclusive or
+//   spreads the neighbours that a copy instruction writes over the banks.)
+template <bool KT>
+__device__ __forceinline__ int place(int t) {
+    return KT ? 8 * (t & 3) + ((t >> 2) ^ (t & 3)) : 8 * (t >> 1 & 3) + 2 * (t >> 3) + (t & 1);
+}
+template <bool KT>
+__device__ __forceinline__ int row_of_lane(int lane) {
+    return KT ? lane ^ (lane >> 3) : lane;
+}
 
 // A row's 16-byte chunk c sits at chunk c ^ swizzle(row), so that eight rows of one chunk cover all banks.
 template <int DB>
@@ -242,25 +263,33 @@ __device__ __forceinline__ float lse_of(float ref, float l) {
 
 
 // One warp's state on an item. SPLIT: fp32 queries and outputs, high and low parts. NT: groups of 8 query rows.
+//
+// Queries that fill the 16 rows of an instruction (two groups of 16-bit ones, the two parts of fp32 ones) are its row
+// operand and the keys its columns, and the scores lie as the values' instruction wants the weights. A single group of
+// 16-bit queries would fill half of it; there (KT) the keys are the rows and the 8 queries the columns, half as many
+// instructions and fewer registers, and movmatrix turns the weights over (64 ragged sequences 74 us with the queries as
+// rows, 70 us so and with 16 warps; one of 131001 tokens 41 and 38 us).
 template <int DB, int NT, bool SPLIT>
 struct Rows {
     using G = Geo<DB>;
+    static constexpr bool KT = !SPLIT && NT == 1;
     static constexpr int D = G::D, MT = SPLIT ? NT : (NT + 1) / 2, ROWS = 8 * NT;
+    static constexpr int LR = KT ? 2 : NT;  // rows whose softmax a lane has a part in: row g of each group; KT: 2 t4, 2 t4 + 1
     int lane, g, t4;
     uint32_t k1024;             // see codes_of
-    uint32_t queries;           // shared address of this lane's row operands: [MT][DB][2] of 16 bytes, 512 apart
-    float factor[NT];           // row g: score * log2(e) = factor * accumulated sum
-    int seen_end[NT], seen_lo[NT];  // row g sees the tokens seen_lo .. seen_end - 1
+    uint32_t queries;           // shared address of this lane's operands: [MT][DB][2] of 16 bytes (KT: 8), kQuad apart
+    float factor[LR];           // of a row: score * log2(e) = factor * accumulated sum
+    int seen_end[LR], seen_lo[LR];  // a row sees the tokens seen_lo .. seen_end - 1
     int all_end, all_lo;        // tokens that every row sees, so that only tiles outside look at each token
     float o[NT][DB][2][4];      // element 2g + j (c0, c1) and 16 + 2g + j (c2, c3; 16-fold) of rows 2 t4, 2 t4 + 1
-    float top[NT], ref[NT], l[NT];  // row g: running maximum, reference, the lane's part of the sum
+    float top[LR], ref[LR], l[LR];  // of a row: running maximum, reference, the lane's part of the sum
     int e_run;                  // the largest exponent of a value scale so far
 
-    static constexpr uint32_t kQueries = MT * DB * 2 * 512;  // bytes of a warp's row operands
+    static constexpr uint32_t kQuad = KT ? 256 : 512, kQueries = MT * DB * 2 * kQuad;  // bytes of a warp's operands
 
     __device__ __forceinline__ void init(uint32_t at) {
         lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-        queries = at + (uint32_t)lane * 16u;
+        queries = at + (uint32_t)lane * (kQuad / 32);
         asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
     }
 
@@ -310,16 +339,17 @@ struct Rows {
                     xh[j] = __half2float(__float2half_rn(y));
                     xl[j] = y - xh[j];
                 }
-                // words 0 and 2: row g, words 1 and 3: row g + 8 (the low parts of fp32 queries; of 16-bit queries the next
-                // group's rows, or nothing)
+                // words 0 and 2: row g, words 1 and 3: row g + 8 (the low parts of fp32 queries; the next group's rows of
+                // 16-bit ones); KT: the column operand's two words
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t at = queries + (uint32_t)(((mt * DB + k) * 2 + i) * 512);
+                    const uint32_t at = queries + (uint32_t)((mt * DB + k) * 2 + i) * kQuad;
                     const uint32_t a0 = pack_half2(xh[i], xh[i + 2]), a2 = pack_half2(xh[4 + i], xh[6 + i]);
                     if constexpr (SPLIT) {
                         sts_quad(at, a0, pack_half2(xl[i], xl[i + 2]), a2, pack_half2(xl[4 + i], xl[6 + i]));
-                    } else if constexpr (NT == 1) {
-                        sts_quad(at, a0, 0u, a2, 0u);
+                    } else if constexpr (KT) {
+                        sts_word(at, a0);
+                        sts_word(at + 4u, a2);
                     } else {
                         sts_word(at + 4u * hi, a0);
                         sts_word(at + 8u + 4u * hi, a2);
@@ -327,12 +357,22 @@ struct Rows {
                 }
             }
         }
+        if constexpr (KT) {  // from row g to rows 2 t4, 2 t4 + 1
+            const float f = factor[0];
+            const int e = seen_end[0], lo = seen_lo[0];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int from = 8 * t4 + 4 * i;
+                factor[i] = __shfl_sync(0xffffffffu, f, from);
+                seen_end[i] = __shfl_sync(0xffffffffu, e, from), seen_lo[i] = __shfl_sync(0xffffffffu, lo, from);
+            }
+        }
         all_end = s.n - a.M + row0 / p.group + 1;
         all_lo = a.window > 0 ? max(s.lo, s.n - a.M + (min(p.R, row0 + ROWS) - 1) / p.group + 1 - a.window) : 0;
 #pragma unroll
         for (int i = 0; i < NT * DB * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) top[n] = -INFINITY, ref[n] = 0.f, l[n] = 0.f;
+        for (int r = 0; r < LR; ++r) top[r] = -INFINITY, ref[r] = 0.f, l[r] = 0.f;
         e_run = -14;
     }
 
@@ -344,7 +384,8 @@ struct Rows {
 
     template <bool MASKED>  // some row does not see every token
     __device__ __forceinline__ void tile(uint32_t st, int tok0) {
-        const uint32_t codes = st + (uint32_t)(lane * G::kRow + swizzle<DB>(lane) * 16);  // chunk k: codes ^ (16 k)
+        const int own_row = row_of_lane<KT>(lane);
+        const uint32_t codes = st + (uint32_t)(own_row * G::kRow + swizzle<DB>(own_row) * 16);  // chunk k: codes ^ (16 k)
         uint32_t kw[DB][4];
 #pragma unroll
         for (int k = 0; k < DB; ++k) ldsm4(codes ^ (uint32_t)(16 * k), kw[k]);
@@ -370,8 +411,10 @@ struct Rows {
             e_run = max(e_run, (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 15);
             __syncwarp();
         }
-        const uint32_t scales = st + (uint32_t)(8 * t4 * 4);  // of block k: + 128 k, of the values' blocks + 128 (DB + k)
-        // scores: sc[n][j] of row g, token 8 t4 + j
+        // of block k: + 128 k, of the values' blocks + 128 (DB + k)
+        const uint32_t scales = st + (uint32_t)(KT ? 16 * g : 32 * t4);
+        // scores, in pairs that an instruction leaves side by side: sc[n][j] and sc[n][j + 1], j even, are of row g of group n
+        // the tokens 8 t4 + j and 8 t4 + j + 1; KT: of rows 2 t4 and 2 t4 + 1 the token 4 g + j / 2
         float sc[NT][8];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -379,36 +422,54 @@ struct Rows {
             for (int j = 0; j < 8; ++j) sc[n][j] = 0.f;
 #pragma unroll
         for (int k = 0; k < DB; ++k) {
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t x[4][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) codes_of(kw[k][j], k1024, x[j]);
+            if constexpr (KT) {
+                uint32_t q[2][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                float c[4][4], kd[8];
-                uint32_t q[2][4];
+                for (int i = 0; i < 2; ++i) lds_words<2>(queries + (uint32_t)(k * 2 + i) * kQuad, q[i]);
+                float c[2][4], kd[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) lds_words<4>(queries + (uint32_t)(((mt * DB + k) * 2 + i) * 512), q[i]);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma(c[j], q[0], x[j][0], x[j][1], zero);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma(c[j], q[1], x[j][2], x[j][3], c[j]);
-                lds_floats(scales + (uint32_t)(128 * k), kd);
-                __syncwarp();  // keeps the blocks' instructions apart: without it registers spill (B = 64 ragged 77 us, not 74)
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t rows[4] = {x[2 * m][2 * i], x[2 * m + 1][2 * i], x[2 * m][2 * i + 1], x[2 * m + 1][2 * i + 1]};
+                        if (i == 0) mma(c[m], rows, q[i][0], q[i][1], zero);
+                        else mma(c[m], rows, q[i][0], q[i][1], c[m]);
+                    }
+                lds_floats4(scales + (uint32_t)(128 * k), kd);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 d = make_float2(kd[2 * j], kd[2 * j + 1]);
-                    // (where 16-bit queries leave rows 8 .. 15 empty this adds zeros; taking the first half alone makes the
-                    // compiler spill: 64 sequences of 1000 tokens 35 us, not 26)
-                    if constexpr (SPLIT || NT == 1) {
-                        const float2 both = fadd2(make_float2(c[j][0], c[j][1]), make_float2(c[j][2], c[j][3]));
-                        const float2 y = ffma2(both, d, make_float2(sc[mt][2 * j], sc[mt][2 * j + 1]));
-                        sc[mt][2 * j] = y.x, sc[mt][2 * j + 1] = y.y;
-                    } else {
+                    const float2 y = ffma2(make_float2(c[j / 2][2 * (j % 2)], c[j / 2][2 * (j % 2) + 1]), make_float2(kd[j], kd[j]),
+                                           make_float2(sc[0][2 * j], sc[0][2 * j + 1]));
+                    sc[0][2 * j] = y.x, sc[0][2 * j + 1] = y.y;
+                }
+            } else {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int n = 2 * mt + u;
-                            if (n < NT) {
+                for (int mt = 0; mt < MT; ++mt) {
+                    float c[4][4], kd[8];
+                    uint32_t q[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) lds_words<4>(queries + (uint32_t)((mt * DB + k) * 2 + i) * kQuad, q[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma(c[j], q[0], x[j][0], x[j][1], zero);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma(c[j], q[1], x[j][2], x[j][3], c[j]);
+                    lds_floats(scales + (uint32_t)(128 * k), kd);
+                    __syncwarp();  // keeps the blocks' instructions apart, and with them the registers in use
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 d = make_float2(kd[2 * j], kd[2 * j + 1]);
+                        if constexpr (SPLIT) {
+                            const float2 both = fadd2(make_float2(c[j][0], c[j][1]), make_float2(c[j][2], c[j][3]));
+                            const float2 y = ffma2(both, d, make_float2(sc[mt][2 * j], sc[mt][2 * j + 1]));
+                            sc[mt][2 * j] = y.x, sc[mt][2 * j + 1] = y.y;
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int n = 2 * mt + u;
                                 const float2 y = ffma2(make_float2(c[j][2 * u], c[j][2 * u + 1]), d,
                                                        make_float2(sc[n][2 * j], sc[n][2 * j + 1]));
                                 sc[n][2 * j] = y.x, sc[n][2 * j + 1] = y.y;
@@ -419,38 +480,47 @@ struct Rows {
             }
         }
 
+        // row r of a lane (r < LR) has the scores sc[KT ? 0 : r][KT ? 2 j + r : j], j < PER
+        constexpr int PER = KT ? 4 : 8;
+        auto score = [&](int r, int j) -> float& { return sc[KT ? 0 : r][KT ? 2 * j + r : j]; };
         bool moved = false;
-        float keep[NT];
-        uint32_t seen[NT];
+        float keep[LR];
+        uint32_t seen[LR];  // bit j
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            seen[n] = 0u;
+        for (int r = 0; r < LR; ++r) {
+            seen[r] = 0u;
             if constexpr (MASKED) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = tok0 + 8 * t4 + j;
-                    if (t >= seen_lo[n] && t < seen_end[n]) seen[n] |= 1u << j;
-                    else sc[n][j] = -INFINITY;
+                for (int j = 0; j < PER; ++j) {
+                    const int t = tok0 + (KT ? 4 * g : 8 * t4) + j;
+                    if (t >= seen_lo[r] && t < seen_end[r]) seen[r] |= 1u << j;
+                    else score(r, j) = -INFINITY;
                 }
             }
-            float m = sc[n][0];
+            float m = score(r, 0);
 #pragma unroll
-            for (int j = 1; j < 8; ++j) m = fmaxf(m, sc[n][j]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const float nt = fmaxf(top[n], m * factor[n]);
+            for (int j = 1; j < PER; ++j) m = fmaxf(m, score(r, j));
+#pragma unroll
+            for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            const float nt = fmaxf(top[r], m * factor[r]);
             const float nr = (nt == -INFINITY ? 0.f : nt) + (float)(e_run - 14);
-            keep[n] = top[n] == -INFINITY ? 1.f : ex2(ref[n] - nr);  // nothing to keep before the first token
-            moved = moved || nr != ref[n];
-            top[n] = nt;
-            ref[n] = nr;
+            keep[r] = top[r] == -INFINITY ? 1.f : ex2(ref[r] - nr);  // nothing to keep before the first token
+            moved = moved || nr != ref[r];
+            top[r] = nt;
+            ref[r] = nr;
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
+            for (int r = 0; r < LR; ++r) l[r] *= keep[r];
+#pragma unroll
             for (int n = 0; n < NT; ++n) {
-                l[n] *= keep[n];
-                const float ka = __shfl_sync(0xffffffffu, keep[n], 8 * t4);
-                const float kb = __shfl_sync(0xffffffffu, keep[n], 8 * t4 + 4);
+                float ka, kb;
+                if constexpr (KT) {
+                    ka = keep[0], kb = keep[1];
+                } else {
+                    ka = __shfl_sync(0xffffffffu, keep[n], 8 * t4);
+                    kb = __shfl_sync(0xffffffffu, keep[n], 8 * t4 + 4);
+                }
 #pragma unroll
                 for (int k = 0; k < DB; ++k) {
 #pragma unroll
@@ -458,19 +528,22 @@ struct Rows {
                 }
             }
         }
+        // weights in the place of the scores; a token that is not seen weighs nothing (also where the query is not finite)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            const int r0 = KT ? 0 : n, r1 = KT ? 1 : n;
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-                float2 y = ffma2(make_float2(sc[n][j], sc[n][j + 1]), make_float2(factor[n], factor[n]), make_float2(-ref[n], -ref[n]));
+                float2 y = ffma2(make_float2(sc[n][j], sc[n][j + 1]), make_float2(factor[r0], factor[r1]), make_float2(-ref[r0], -ref[r1]));
                 y.x = ex2(y.x), y.y = ex2(y.y);
-                if (MASKED && !(seen[n] >> j & 1u)) y.x = 0.f;  // also where the query is not finite
-                if (MASKED && !(seen[n] >> (j + 1) & 1u)) y.y = 0.f;
+                if (MASKED && !(seen[r0] >> (KT ? j / 2 : j) & 1u)) y.x = 0.f;
+                if (MASKED && !(seen[r1] >> (KT ? j / 2 : j + 1) & 1u)) y.y = 0.f;
                 sc[n][j] = y.x, sc[n][j + 1] = y.y;
                 sum = fadd2(sum, y);
             }
-            l[n] += sum.x + sum.y;
+            if constexpr (KT) l[0] += sum.x, l[1] += sum.y;
+            else l[n] += sum.x + sum.y;
         }
 
 #pragma unroll
@@ -479,20 +552,30 @@ struct Rows {
             ldsm4_trans((codes ^ (uint32_t)(16 * k)) + G::kCodes, w);
 #pragma unroll
             for (int u = 0; u < 4; ++u) codes_of(w[u], k1024, x[u]);
+            // weight times value scale, as the column operand: row g, two tokens of matrix j
             float vd[8];
-            lds_floats(scales + (uint32_t)(128 * (DB + k)), vd);
+            if constexpr (KT) {
+                float v[4];
+                lds_floats4(scales + (uint32_t)(128 * (DB + k)), v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) vd[2 * j] = vd[2 * j + 1] = v[j];
+            } else {
+                lds_floats(scales + (uint32_t)(128 * (DB + k)), vd);
+            }
             uint32_t hi[NT][4], lo[SPLIT ? NT : 1][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 d = make_float2(vd[2 * j], vd[2 * j + 1]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
+                    const int r0 = KT ? 0 : n, r1 = KT ? 1 : n;
                     float2 y = __fmul2_rn(make_float2(sc[n][2 * j], sc[n][2 * j + 1]), d);
                     if constexpr (MASKED) {  // a masked token's scale may be anything
-                        if (!(seen[n] >> (2 * j) & 1u)) y.x = 0.f;
-                        if (!(seen[n] >> (2 * j + 1) & 1u)) y.y = 0.f;
+                        if (!(seen[r0] >> (KT ? j : 2 * j) & 1u)) y.x = 0.f;
+                        if (!(seen[r1] >> (KT ? j : 2 * j + 1) & 1u)) y.y = 0.f;
                     }
                     hi[n][j] = pack_half2(y.x, y.y);
+                    if constexpr (KT) hi[n][j] = turned_over(hi[n][j]);
                     if constexpr (SPLIT) {
                         const float2 back = to_float2(hi[n][j]);
                         lo[n][j] = pack_half2(y.x - back.x, y.y - back.y);
@@ -518,10 +601,21 @@ struct Rows {
 
     // Row g's sum over the whole warp, and its reference: -infinity where it saw nothing. bad: NaN, whatever was seen.
     __device__ __forceinline__ void finish(bool bad) {
+        if constexpr (KT) {  // from rows 2 t4, 2 t4 + 1 back to row g
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+            const float l0 = __shfl_sync(0xffffffffu, l[0], g >> 1), l1 = __shfl_sync(0xffffffffu, l[1], g >> 1);
+            const float r0 = __shfl_sync(0xffffffffu, ref[0], g >> 1), r1 = __shfl_sync(0xffffffffu, ref[1], g >> 1);
+            l[0] = g & 1 ? l1 : l0, ref[0] = g & 1 ? r1 : r0;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
-            l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+            if constexpr (!KT) {
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+            }
             if (bad) l[n] = qnan(), ref[n] = 0.f;
             else if (l[n] == 0.f) ref[n] = -INFINITY;
         }
@@ -545,7 +639,7 @@ struct Rows {
 };
 
 // A warp's ring of stages, and its copies into it.
-template <int DB, int STAGES>
+template <int DB, int STAGES, bool KT>
 struct Ring {
     using G = Geo<DB>;
     uint32_t base, in, out;  // shared addresses: of the ring, of the stage to fill next, of the stage to use next
@@ -569,7 +663,7 @@ struct Ring {
             constexpr bool ALL = decltype(all)::value;
 #pragma unroll
             for (int j = 0; j < DB; ++j) {
-                const int tok = j * (32 / DB) + lane / DB, at = place(tok);
+                const int tok = j * (32 / DB) + lane / DB, at = place<KT>(tok);
                 const int r = __shfl_sync(0xffffffffu, row, tok);
                 const long long off = (long long)(ALL ? r : max(r, 0)) * G::kRow;
                 const uint32_t dst = in + (uint32_t)(at * G::kRow + ((lane % DB) ^ swizzle<DB>(at)) * 16);
@@ -634,7 +728,7 @@ kv4_attention_items_kernel(const Params p) {
     const KvAttnArgs& a = p.a;
     const int warp = threadIdx.x >> 5;
     Rows<DB, NT, SPLIT> w;
-    Ring<DB, L::kStages> ring;
+    Ring<DB, L::kStages, Rows<DB, NT, SPLIT>::KT> ring;
     constexpr uint32_t kWarpBytes = L::kStages * G::kStage + Rows<DB, NT, SPLIT>::kQueries;
     const uint32_t mine_at = smem_addr(ring_memory) + (uint32_t)warp * kWarpBytes;
     ring.init(mine_at, a.c);
@@ -806,7 +900,7 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
     // warps of one SM take pieces that are far apart: an SM that gets a stretch of short items gets others too
     const int stream = warp * (int)gridDim.x + (int)blockIdx.x;
     Rows<DB, NT, SPLIT> w;
-    Ring<DB, L::kStages> ring;
+    Ring<DB, L::kStages, Rows<DB, NT, SPLIT>::KT> ring;
     constexpr uint32_t kWarpBytes = L::kStages * G::kStage + Rows<DB, NT, SPLIT>::kQueries;
     const uint32_t mine_at = smem_addr(ring_memory) + (uint32_t)warp * kWarpBytes;
     ring.init(mine_at, a.c);
