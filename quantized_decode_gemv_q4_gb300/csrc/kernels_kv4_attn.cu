@@ -1125,11 +1125,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const 
 // Groups of 8 rows that a warp holds: two where there are more than 8 rows and the outputs fit the registers.
 int row_groups(int M, int group, int D) { return M * group > 8 && D < 256 ? 2 : 1; }
 
-// Items (whole, or split evenly over up to two CTAs an SM, each with two tiles a warp at least) where the page table admits
-// no sequence longer than kItemTokens, for a single sequence, and for few items of up to kSplitTokens; streams otherwise.
-// The streams' scan, their second launch and its join cost 8 us more than a launch of whole items (8 sequences of 100
-// tokens, 8 key heads of 128: 6.3 and 14.9 us; of 1500 tokens, split in 4: 12 and 17.5 us), and do not mind the lengths:
-// a CTA with the longest of ragged items is waited for, 25 us for 8192 tokens split in two.
+// Items (whole, or split evenly over up to two CTAs an SM, 256 tokens each at least) where the page table admits no sequence
+// longer than kItemTokens, for a single sequence, and for few items of up to kSplitTokens; streams otherwise. The streams'
+// scan, their second launch and its join cost 8 us more than a launch of whole items, and do not mind the lengths, where the
+// CTAs with the longest of ragged items are waited for. 8 key heads of 128, bf16, items and streams: 8 sequences of 100
+// tokens 6.2 and 14.2 us, of 1500 tokens 11 and 16 us; 64 of 1000 tokens 25 and 29 us; one of 131001 tokens 37 and 45 us;
+// 64 ragged ones up to 8192 tokens 107 and 69 us.
 constexpr long long kItemTokens = 1024;
 constexpr long long kSplitTokens = 8192;
 
@@ -1208,8 +1209,8 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, const Dev
                     dim3((unsigned)(items * p.splits), (unsigned)a.B), I::kWarps * 32, kRing, di, s, p);
             };
             // more CTAs than two an SM run in kMany where 128 registers do; from eight an SM on, CTAs of two warps take over,
-            // each warp with twice the tiles and half the starts: 256 sequences of 64 tokens 22 and 15 us, of 300 tokens 33 and
-            // 28 us, but 64 sequences of 200 tokens 10 and 11 us (8 key heads of 128, bf16)
+            // each warp with twice the tiles and half the starts: 256 sequences of 64 tokens 21 and 14 us, of 300 tokens 33 and
+            // 27 us, but 64 sequences of 200 tokens 9.8 and 10.7 us (8 key heads of 128, bf16)
             constexpr bool kFour = DB == 2 || (DB == 4 && NT == 1);
             const long long ctas = call_items * p.splits;
             cudaError_t e;

@@ -18,9 +18,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // Where there are many rows (three for each resident thread of the device) a lane takes 4 heads and the resident blocks
-// walk over the tokens, else a lane takes a head. 8191 bf16 tokens of 32 + 8 heads of 128: 42 us with a head a lane, 37 us
+// walk over the tokens, else a lane takes a head. 8191 bf16 tokens of 32 + 8 heads of 128: 49 us with a head a lane, 37 us
 // with 4 heads a lane and a block for every 256 lanes, 32 us so (26 us for the bytes). What is left is the latency of the
-// table row behind the position, one round ahead.
+// table row behind the position, which is read an iteration ahead.
 constexpr int kHeads = 4;
 constexpr int kBlocks = 2;  // resident blocks of an SM
 constexpr long long kManyLanes = 1LL << 20;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs p
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // the position is known a round ahead, so that the table is read along with the heads and not after it
+    // the position is known an iteration ahead, so that the table is read along with the heads and not after it
     auto position = [&](unsigned i) { return pairs > 0 && i < all ? p.positions[i / (unsigned)groups] : 0; };
     int pos = position(idx);
     const unsigned rounds = (all + step - 1) / step;  // the same for every lane of a warp: they meet in the norm's shuffles
