@@ -15,7 +15,8 @@
 //   - the weight times its value scale, kept within 2^15 by the running reference below: one f16 for 16-bit outputs
 //     (half a step 2^-12), a high and a low part for fp32.
 // Scores, running maximum, running sum and outputs are fp32. The reference that the exponentials subtract is the row's
-// running maximum plus the exponent of the largest value scale so far, so weight * scale never leaves f16's range.
+// running maximum plus the exponent of the largest value scale that it has seen, so weight * scale never leaves f16's range,
+// and tokens that a row does not see change none of its bits.
 //
 // Work. A warp takes tiles of 32 tokens, streamed by cp.async into its own ring of shared-memory stages (16-byte chunks
 // XOR-swizzled so that ldmatrix is free of bank conflicts; ldmatrix delivers the keys' words in the layout of a column
@@ -283,7 +284,7 @@ struct Rows {
     int all_end, all_lo;        // tokens that every row sees, so that only tiles outside look at each token
     float o[NT][DB][2][4];      // element 2g + j (c0, c1) and 16 + 2g + j (c2, c3; 16-fold) of rows 2 t4, 2 t4 + 1
     float top[LR], ref[LR], l[LR];  // of a row: running maximum, reference, the lane's part of the sum
-    int e_run;                  // the largest exponent of a value scale so far
+    int e_run[LR];              // of a row: the largest exponent of a value scale that it has seen
 
     static constexpr uint32_t kQuad = KT ? 256 : 512, kQueries = MT * DB * 2 * kQuad;  // bytes of a warp's operands
 
@@ -372,8 +373,7 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < NT * DB * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
 #pragma unroll
-        for (int r = 0; r < LR; ++r) top[r] = -INFINITY, ref[r] = 0.f, l[r] = 0.f;
-        e_run = -14;
+        for (int r = 0; r < LR; ++r) top[r] = -INFINITY, ref[r] = 0.f, l[r] = 0.f, e_run[r] = -14;
     }
 
     // The tile of tokens tok0 .. tok0 + 31 in the stage at shared address st.
@@ -391,8 +391,9 @@ struct Rows {
         for (int k = 0; k < DB; ++k) ldsm4(codes ^ (uint32_t)(16 * k), kw[k]);
         // This lane's token's scales become fp32 [K, V][block][token] in the place of the keys' codes, which are in
         // registers now: a lane then reads those of its eight tokens as they are used (converting them where they are used
-        // would take 64 conversions, eight lanes the same ones). Their largest exponent is noted on the way (zeros stand
-        // where nothing was read).
+        // would take 64 conversions, eight lanes the same ones). Their largest exponent is noted on the way: for all rows, or,
+        // where they differ in what they see, for each token, in the place of its values' scales.
+        const uint32_t exponents = st + (uint32_t)(2 * G::kCodes + G::kScales);  // of token t: + t * DB * 2
         {
             uint32_t own[2][DB / 2], m = 0u;
             const uint32_t at = st + (uint32_t)(2 * G::kCodes + lane * DB * 2);
@@ -406,9 +407,18 @@ struct Rows {
                     const uint32_t to = st + (uint32_t)(((v * DB + 2 * k) * 32 + lane) * 4);
                     sts_word(to, __float_as_uint(d.x));
                     sts_word(to + 128u, __float_as_uint(d.y));
-                    if (v) m = max(m, max(own[v][k] & 0x7C00u, (own[v][k] >> 16) & 0x7C00u));
+                    if (v) {  // the exponents plus one: those of NaN and infinity pass out of the field and count as 0
+                        const uint32_t up = (own[v][k] & 0x7C007C00u) + 0x04000400u;
+                        m = max(m, max(up & 0x7C00u, (up >> 16) & 0x7C00u));
+                    }
                 }
-            e_run = max(e_run, (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 15);
+            if constexpr (MASKED) {
+                sts_word(exponents + (uint32_t)(lane * DB * 2), m);
+            } else {
+                const int e = (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 16;
+#pragma unroll
+                for (int r = 0; r < LR; ++r) e_run[r] = max(e_run[r], e);
+            }
             __syncwarp();
         }
         // of block k: + 128 k, of the values' blocks + 128 (DB + k)
@@ -487,23 +497,36 @@ struct Rows {
         float keep[LR];
         uint32_t seen[LR];  // bit j
 #pragma unroll
-        for (int r = 0; r < LR; ++r) {
-            seen[r] = 0u;
-            if constexpr (MASKED) {
+        for (int r = 0; r < LR; ++r) seen[r] = 0u;
+        if constexpr (MASKED) {
+            uint32_t e[LR] = {};
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const int t = tok0 + (KT ? 4 * g : 8 * t4) + j;
-                    if (t >= seen_lo[r] && t < seen_end[r]) seen[r] |= 1u << j;
+            for (int j = 0; j < PER; ++j) {
+                const int in = (KT ? 4 * g : 8 * t4) + j, t = tok0 + in;
+                uint32_t of_token[1];
+                lds_own<1>(exponents + (uint32_t)(in * DB * 2), of_token);
+#pragma unroll
+                for (int r = 0; r < LR; ++r) {
+                    if (t >= seen_lo[r] && t < seen_end[r]) seen[r] |= 1u << j, e[r] = max(e[r], of_token[0]);
                     else score(r, j) = -INFINITY;
                 }
             }
+#pragma unroll
+            for (int r = 0; r < LR; ++r) {
+#pragma unroll
+                for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) e[r] = max(e[r], __shfl_xor_sync(0xffffffffu, e[r], x));
+                e_run[r] = max(e_run[r], (int)(e[r] >> 10) - 16);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < LR; ++r) {
             float m = score(r, 0);
 #pragma unroll
             for (int j = 1; j < PER; ++j) m = fmaxf(m, score(r, j));
 #pragma unroll
             for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
             const float nt = fmaxf(top[r], m * factor[r]);
-            const float nr = (nt == -INFINITY ? 0.f : nt) + (float)(e_run - 14);
+            const float nr = (nt == -INFINITY ? 0.f : nt) + (float)(e_run[r] - 14);
             keep[r] = top[r] == -INFINITY ? 1.f : ex2(ref[r] - nr);  // nothing to keep before the first token
             moved = moved || nr != ref[r];
             top[r] = nt;

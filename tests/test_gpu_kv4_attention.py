@@ -191,6 +191,41 @@ def test_a_nan_reaches_only_the_queries_that_see_it(spare):
     assert torch.isnan(out[1, 0, 0]).all() and torch.isnan(out[1, 1, 1]).all() and torch.isfinite(out[1, 0, 1:]).all()
 
 
+@pytest.mark.parametrize("scale", [np.nan, 65504.0])
+@pytest.mark.parametrize("spare", [1, 100, 800])
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 128), (F32, 256), (BF16, 64), (BF16, 128), (BF16, 256)])
+@pytest.mark.parametrize("group", [1, 4])
+def test_what_a_query_does_not_see_changes_no_bit(group, dtype, D, spare, scale):
+    """Values of about 1e-3, and tokens behind a query or before its window with any scales, codes and NaN."""
+    c = Case([50, 300], 3, 2 * group, 2, D, 16, dtype, window=20, spare=spare)
+    c.v_d[:] = np.where(np.isfinite(c.v_d), c.v_d * np.float16(2.0 ** -9), c.v_d)
+    c.upload()
+    out, lse = c.run()
+    c.check(out, lse)
+    for back, others in ((1, [0, 1]), (20 + 2, [1, 2])):  # the newest token, seen by query 2; the oldest, seen by query 0
+        saved = [a.copy() for a in (c.k_qs, c.k_d, c.v_qs, c.v_d)]
+        for b, n in enumerate(c.lens):
+            at = c.table[b][(n - back) // 16], slice(None), (n - back) % 16
+            c.k_qs[at], c.v_qs[at], c.k_d[at], c.v_d[at] = 0xF0, 0x1E, scale, scale
+        c.upload()
+        got, got_lse = c.run()
+        assert torch.equal(got[:, others], out[:, others]) and torch.equal(got_lse[:, others], lse[:, others])
+        c.k_qs, c.k_d, c.v_qs, c.v_d = saved
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_nan_block_of_values_leaves_the_other_blocks_as_accurate(dtype):
+    c = Case([70], 1, 4, 2, 128, 16, dtype)
+    c.v_d[:] = np.where(np.isfinite(c.v_d), c.v_d * np.float16(2.0 ** -9), c.v_d)
+    c.v_d[c.table[0][2], 1, 5, 2] = np.nan
+    c.upload()
+    out, lse = c.run()
+    assert torch.isnan(out[:, :, 2:, 64:96]).all()
+    out[:, :, 2:, 64:96] = 0
+    c.v_d[:, 1, :, 2] = 0  # the expected values of that block are zeros
+    c.check(out, lse)
+
+
 @pytest.mark.parametrize("spare", [1, 100, 800])
 def test_bad_pages_and_lengths_are_recorded(spare):
     c = Case([100, 60, 40, 70], 1, 4, 2, 64, 16, F32, spare=spare)
