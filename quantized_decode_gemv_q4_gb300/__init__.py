@@ -336,7 +336,8 @@ class KV4Cache:
 
     ``k_qs``, ``v_qs`` uint8 ``[num_pages, num_kv_heads, page_size, head_dim/2]`` and ``k_d``, ``v_d`` float16
     ``[num_pages, num_kv_heads, page_size, head_dim/32]``, contiguous on one CUDA device. The object keeps the tensors
-    (and the struct that the calls take) and nothing else; :meth:`allocate` makes an empty one, whose rows read as zeros.
+    (and the struct that the calls take, made once: its attributes cannot be set) and nothing else; :meth:`allocate` makes
+    an empty one, whose rows read as zeros.
     """
 
     class _Struct(ctypes.Structure):
@@ -352,13 +353,13 @@ class KV4Cache:
                              "[num_pages, num_kv_heads, page_size, head_dim/32], head_dim a multiple of 32")
         if any(t.device != k_qs.device for t in (k_d, v_qs, v_d)):
             raise ValueError("the cache's tensors must be on one device")
-        self.k_qs, self.k_d, self.v_qs, self.v_d = k_qs, k_d, v_qs, v_d
-        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = pages, heads, page, half * 2
-        self.device = k_qs.device
-        self._struct = KV4Cache._Struct(_ptr(k_qs, torch.uint8, "k_qs"), _ptr(k_d, torch.float16, "k_d"),
-                                        _ptr(v_qs, torch.uint8, "v_qs"), _ptr(v_d, torch.float16, "v_d"), pages, heads, page,
-                                        half * 2)
-        self._ref = ctypes.addressof(self._struct)
+        struct = KV4Cache._Struct(_ptr(k_qs, torch.uint8, "k_qs"), _ptr(k_d, torch.float16, "k_d"),
+                                  _ptr(v_qs, torch.uint8, "v_qs"), _ptr(v_d, torch.float16, "v_d"), pages, heads, page, half * 2)
+        self.__dict__.update(k_qs=k_qs, k_d=k_d, v_qs=v_qs, v_d=v_d, num_pages=pages, num_kv_heads=heads, page_size=page,
+                             head_dim=half * 2, device=k_qs.device, _struct=struct, _ref=ctypes.addressof(struct))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: a KV4Cache's tensors and sizes are fixed; make another one")
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, device="cuda") -> "KV4Cache":

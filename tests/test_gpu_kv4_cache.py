@@ -187,3 +187,13 @@ def test_rows_behind_2_to_the_32_bytes():
     rows = [cache.k_qs[s // page, :, s % page].cpu().numpy() for s in slots]
     assert np.array_equal(np.stack(rows), ref.quantise(k.cpu().numpy())[0])
     assert int((cache.k_qs != 0x88).any(-1).sum()) == 3 * H
+
+
+def test_a_cache_keeps_the_tensors_that_its_struct_points_to():
+    cache = q4.KV4Cache.allocate(2, 16, 2, 64)
+    for name in ("k_qs", "k_d", "v_qs", "v_d"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros_like(getattr(cache, name)))
+    with pytest.raises(AttributeError):
+        cache.num_pages = 3
+    assert cache._struct.k_qs == cache.k_qs.data_ptr() and cache._struct.v_d == cache.v_d.data_ptr()
