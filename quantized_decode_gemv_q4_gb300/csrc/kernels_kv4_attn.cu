@@ -1148,12 +1148,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const 
 // Groups of 8 rows that a warp holds: two where there are more than 8 rows and the outputs fit the registers.
 int row_groups(int M, int group, int D) { return M * group > 8 && D < 256 ? 2 : 1; }
 
-// Items (whole, or split evenly over up to two CTAs an SM, 256 tokens each at least) where the page table admits no sequence
-// longer than kItemTokens, for a single sequence, and for few items of up to kSplitTokens; streams otherwise. The streams'
-// scan, their second launch and its join cost 8 us more than a launch of whole items, and do not mind the lengths, where the
-// CTAs with the longest of ragged items are waited for. 8 key heads of 128, bf16, items and streams: 8 sequences of 100
-// tokens 6.2 and 14.2 us, of 1500 tokens 11 and 16 us; 64 of 1000 tokens 25 and 29 us; one of 131001 tokens 37 and 45 us;
-// 64 ragged ones up to 8192 tokens 107 and 69 us.
+// Items (whole, or split evenly over up to two CTAs an SM, 256 tokens each at least) where the page table and the window let
+// no sequence read more than kItemTokens, for a single sequence, and for few items of up to kSplitTokens; streams otherwise.
+// The streams' scan, their second launch and its join cost 5 to 8 us more than a launch of whole items, and do not mind the
+// lengths, where the CTAs with the longest of ragged items are waited for. 8 key heads of 128, bf16, items and streams: 8
+// sequences of 100 tokens 6.2 and 14.2 us, of 1500 tokens 11 and 16 us; 64 of 1000 tokens 25 and 29 us; 64 with a window of
+// 512 tokens 16 and 22 us; one of 131001 tokens 37 and 45 us; 64 ragged ones up to 2000 tokens 33 and 30 us, up to 8192
+// tokens 107 and 69 us.
 constexpr long long kItemTokens = 1024;
 constexpr long long kSplitTokens = 8192;
 
@@ -1219,7 +1220,9 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, const Dev
             return few ? launch_grid(kv4_attention_join_kernel<DB, NT, 1>, dim3(blocks, 8 * NT), dim3(kJoinThreads), 0, s, true, p)
                        : launch_grid(kv4_attention_join_kernel<DB, NT, 8 * NT>, dim3(blocks), dim3(kJoinThreads), 0, s, true, p);
         };
-        const long long most = (long long)a.max_pages * a.c.page_size, call_items = (long long)items * a.B;
+        // the tokens that an item reads at most
+        const long long held = (long long)a.max_pages * a.c.page_size, call_items = (long long)items * a.B;
+        const long long most = a.window > 0 ? std::min(held, (long long)a.window + a.M - 1) : held;
         if (most <= kItemTokens || a.B == 1 || (most <= kSplitTokens && call_items <= sm_count)) {
             p.warps = 0;
             p.splits = (int)std::max(1LL, std::min(2LL * sm_count / call_items, most / (8 * kTile)));

@@ -258,6 +258,22 @@ def test_windows_past_every_sequence_are_none(spare):
         assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,M,Hq,Hkv,D,longest,window", [
+    (52, 3, 12, 4, 64, 2700, 1400),   # many items of more than a thousand tokens each
+    (45, 1, 8, 4, 128, 1600, 1030),
+    (3, 2, 4, 2, 64, 9300, 8300),     # few, of more tokens than are split between CTAs
+    (3, 2, 4, 2, 64, 9300, 700),
+    (40, 2, 10, 5, 128, 1500, 1023),  # most that is read: 1024 tokens
+    (40, 2, 10, 5, 128, 1500, 1024),
+])
+def test_windows_over_many_and_long_sequences(B, M, Hq, Hkv, D, longest, window, dtype):
+    lens = [longest * ((7 * i) % B + 1) // B for i in range(B)]
+    lens[0], lens[1] = longest, 1
+    c = Case(lens, M, Hq, Hkv, D, 16, dtype, window)
+    c.check(*c.run())
+
+
 def test_many_heads_and_rows():
     """More query heads than a CTA's rows many times over, and a key head for each query head."""
     c = Case([70, 3], 2, 192, 2, 64, 16, BF16)
