@@ -51,6 +51,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs p
     const int ib = turns && !p.interleaved ? p.rot / 2 + lane * V : ia + V;
     const unsigned step = gridDim.x * (kThreads / LPR), all = (unsigned)p.T * (unsigned)groups;
     unsigned idx = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;  // (token, group of heads)
+    // Query and key rows share warps: where only one of them has a norm, the lanes of the other sum along, so that a whole
+    // warp meets in the shuffles.
+    const bool norms = p.q_gamma != nullptr || p.k_gamma != nullptr;
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -95,15 +98,17 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs p
         float a[V], b[V];
         widen(wa[i], a, T());
         widen(wb[i], b, T());
-        if (gamma) {
+        if (norms) {
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) sum = fmaf(a[j], a[j], fmaf(b[j], b[j], sum));
 #pragma unroll
             for (int o = LPR / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float r = rsqrtf(sum / (float)p.D + p.eps);
+            if (gamma) {
+                const float r = rsqrtf(sum / (float)p.D + p.eps);
 #pragma unroll
-            for (int j = 0; j < V; ++j) a[j] = a[j] * r * ga[j], b[j] = b[j] * r * gb[j];
+                for (int j = 0; j < V; ++j) a[j] = a[j] * r * ga[j], b[j] = b[j] * r * gb[j];
+            }
         }
         if (!there || i >= heads) continue;
         float oa[V], ob[V];

@@ -79,3 +79,23 @@ def test_zero_rows_infinities_and_bad_positions():
     q4.qk_norm_rope(out, k_out, x, x, gamma, gamma, cs, pos.clamp(0, 5), eps=1e-6)
     assert torch.all(out[0] == 0) and q4.q4_device_faults() == 0
     assert torch.isfinite(out[2:]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("side", ["q", "k"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter", [
+    (1, 7, 1, 128, 128, False), (3, 5, 3, 64, 32, True), (5, 1, 1, 32, 32, False), (2, 3, 2, 96, 96, True), (4, 2, 1, 256, 256, False),
+    (9, 1, 6, 160, 0, False), (4099, 30, 6, 128, 128, False), (12345, 13, 1, 64, 64, True), (5001, 9, 3, 256, 64, False)])  # many rows
+def test_a_norm_on_one_side_only(dtype, T, Hq, Hkv, D, rot, inter, side):
+    """Query and key heads that share a warp, one of them without a norm."""
+    g = torch.Generator().manual_seed(T + Hq + D)
+    q, k = (torch.randn(T, H, D, generator=g).to(dtype).cuda() for H in (Hq, Hkv))
+    gamma = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    gq, gk = (gamma, None) if side == "q" else (None, gamma)
+    cs = table(rot) if rot else None
+    pos = torch.randint(0, 5000, (T,), generator=g, dtype=torch.int32)
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    q4.qk_norm_rope(qo, ko, q, k, gq, gk, None if cs is None else torch.from_numpy(cs).cuda(), None if cs is None else pos.cuda(),
+                    eps=1e-5, interleaved=inter)
+    for got, x, gam, what in ((qo, q, gq, "q"), (ko, k, gk, "k")):
+        check(got, x.double().cpu().numpy(), None if gam is None else gam.cpu().numpy(), 1e-5, cs, pos.numpy(), inter, dtype, what)
