@@ -12,11 +12,14 @@
 // products (keys) or the softmax weight (values), so what is rounded to f16 is only
 //   - q, scaled to the row's largest magnitude: exact for f16 and bf16 queries, and for fp32 queries split into a high
 //     and a low f16 part (22 bits) that fill the two halves of the instruction's 16 rows;
-//   - the weight times its value scale, kept within 2^15 by the running reference below: one f16 for 16-bit outputs
-//     (half a step 2^-12), a high and a low part for fp32.
+//   - the weight times its value scale, a term: one f16 for 16-bit outputs (half a step: 2^-11 of it), a high and a low part
+//     (2^-22) for fp32.
 // Scores, running maximum, running sum and outputs are fp32. The reference that the exponentials subtract is the row's
-// running maximum plus the exponent of the largest value scale that it has seen, so weight * scale never leaves f16's range,
-// and tokens that a row does not see change none of its bits.
+// running maximum plus the exponent of the largest value scale so far, so that the largest terms lie below 2^15. Scales that
+// differ by up to 2^10 leave the row's largest term in every block at 2^4 or above; what f16 loses below its step of 2^-24 is then,
+// over n tokens, at most n 2^-29 of it, less than the roundings of an fp32 sum of n. A row that has seen scales further apart
+// (or some zeros; and every row in a tile of which the rows of a warp see different tokens) is `apart`: its terms are
+// scaled by the tile's own largest one in each block. Tokens that a row does not see change none of its bits.
 //
 // Work. A warp takes tiles of 32 tokens, streamed by cp.async into its own ring of shared-memory stages (16-byte chunks
 // XOR-swizzled so that ldmatrix is free of bank conflicts; ldmatrix delivers the keys' words in the layout of a column
@@ -28,6 +31,7 @@
 //   - whole items: one CTA per item, its warps' tiles interleaved and joined through shared memory; one launch.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 #include "kv_common.cuh"
 
@@ -38,6 +42,11 @@ namespace {
 constexpr int kTile = 32;       // tokens a warp takes at a time
 constexpr int kMaxB = 1024;     // sequences of a call
 constexpr int kItemCost = 4;    // what starting on an item costs a streaming warp, in tiles
+// A row is `apart` once the value scales that it has seen differ by more than 2^kRange, or some block had zeros and others (a
+// block that is zero throughout, as in padded heads, has nothing to lose). 64 ragged sequences (bf16, heads of 128): 71 us,
+// 77 us with a block of zeros, 113 us with a zero scale among others in every page.
+constexpr int kRange = 10, kNone = -100;
+constexpr uint32_t kNoneSeen = 16u + 64u;  // Rows::e_own before the first token
 
 template <int DB>
 struct Geo {
@@ -263,6 +272,17 @@ __device__ __forceinline__ float lse_of(float ref, float l) {
 }
 
 
+__device__ __forceinline__ uint32_t half_max(uint32_t a, uint32_t b) {
+    uint32_t x;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(x) : "r"(a), "r"(b));
+    return x;
+}
+__device__ __forceinline__ uint32_t half_min(uint32_t a, uint32_t b) {
+    uint32_t x;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(x) : "r"(a), "r"(b));
+    return x;
+}
+
 // One warp's state on an item. SPLIT: fp32 queries and outputs, high and low parts. NT: groups of 8 query rows.
 //
 // Queries that fill the 16 rows of an instruction (two groups of 16-bit ones, the two parts of fp32 ones) are its row
@@ -283,10 +303,21 @@ struct Rows {
     int seen_end[LR], seen_lo[LR];  // a row sees the tokens seen_lo .. seen_end - 1
     int all_end, all_lo;        // tokens that every row sees, so that only tiles outside look at each token
     float o[NT][DB][2][4];      // element 2g + j (c0, c1) and 16 + 2g + j (c2, c3; 16-fold) of rows 2 t4, 2 t4 + 1
-    float top[LR], ref[LR], l[LR];  // of a row: running maximum, reference, the lane's part of the sum
-    int e_run[LR];              // of a row: the largest exponent of a value scale that it has seen
+    float top[LR], l[LR];       // of a row: running maximum, the lane's part of the sum
+    bool same;                  // all rows are of one query: they see the same tokens of every tile
+    // The value scales so far, in tiles of which all rows see the same tokens: the exponents of the largest and of the smallest
+    // that is not zero. A plain tile's smallest (as its f16 bits) lies above `unless`, or usual() looks at it.
+    int e_most, e_least;
+    uint32_t unless;
+    // What only usual() and other than plain tiles need, in a word of each lane in shared memory:
+    // kZeros: bit k: some token's scale of block k was zero, bit 8 + k: some token's was not (left at 0 as long as none was
+    //   zero), as above in tiles of which all rows see the same tokens;
+    // kOwn + r: for a row's other tiles the smallest exponent + 64, and from bit 8 on the same bits;
+    // kLeast: the smallest exponent in any of these, kNone where a row is apart for good.
+    enum : int { kZeros, kLeast, kOwn, kNotes = kOwn + LR };
 
-    static constexpr uint32_t kQuad = KT ? 256 : 512, kQueries = MT * DB * 2 * kQuad;  // bytes of a warp's operands
+    static constexpr uint32_t kQuad = KT ? 256 : 512, kOperands = MT * DB * 2 * kQuad;
+    static constexpr uint32_t kQueries = kOperands + kNotes * 128;  // bytes of a warp's operands and notes
 
     __device__ __forceinline__ void init(uint32_t at) {
         lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -327,7 +358,7 @@ struct Rows {
             const int k2 = big > 0.f && fine ? 13 - e : 0;
             const float f1 = pow2i(k2 / 2), f2 = pow2i(k2 - k2 / 2);
             factor[n] = fine ? (a.scale * 1.4426950408889634f) * pow2i(-(k2 / 2)) * pow2i(-(k2 - k2 / 2)) : qnan();
-            seen_end[n] = there ? s.n - a.M + m + 1 : 0;
+            seen_end[n] = s.n - a.M + min(m, a.M - 1) + 1;
             seen_lo[n] = a.window > 0 ? seen_end[n] - a.window : 0;
             const int mt = SPLIT ? n : n / 2, hi = SPLIT ? 0 : n % 2;
 #pragma unroll
@@ -373,54 +404,152 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < NT * DB * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
 #pragma unroll
-        for (int r = 0; r < LR; ++r) top[r] = -INFINITY, ref[r] = 0.f, l[r] = 0.f, e_run[r] = -14;
+        for (int r = 0; r < LR; ++r) top[r] = -FLT_MAX, l[r] = 0.f, note(kOwn + r, kNoneSeen);
+        note(kZeros, 0u), note(kLeast, 16u);
+        e_most = -14, e_least = 16, unless = 0u;
+        same = row0 / p.group == (min(p.R, row0 + ROWS) - 1) / p.group;
     }
 
     // The tile of tokens tok0 .. tok0 + 31 in the stage at shared address st.
     __device__ __forceinline__ void take(uint32_t st, int tok0) {
-        if (tok0 >= all_lo && tok0 + kTile <= all_end) tile<false>(st, tok0);
-        else tile<true>(st, tok0);
+        const bool whole = tok0 >= all_lo && tok0 + kTile <= all_end;  // every row sees every token
+        if (!whole || !tile<true>(st, tok0, true)) tile<false>(st, tok0, whole || same);
     }
 
-    template <bool MASKED>  // some row does not see every token
-    __device__ __forceinline__ void tile(uint32_t st, int tok0) {
+    __device__ __forceinline__ uint32_t note_at(int i) const {
+        return queries - (uint32_t)lane * (kQuad / 32 - 4) + kOperands + 128u * (uint32_t)i;
+    }
+    __device__ __forceinline__ uint32_t note(int i) const {
+        uint32_t w[1];
+        lds_own<1>(note_at(i), w);
+        return w[0];
+    }
+    __device__ __forceinline__ void note(int i, uint32_t w) const { sts_word(note_at(i), w); }
+
+    // Whether a whole tile is plain although it has zeros among its value scales (of this lane's token: own), or there were
+    // zeros or tiles that not all rows saw alike before it: the zeros must be whole blocks that were always zero. Notes them,
+    // and leaves in lo the smallest exponent (as bits) of the other scales.
+    __device__ __forceinline__ bool usual(const uint32_t (&own)[DB / 2], uint32_t hi, uint32_t& lo) {
+        uint32_t zeros = note(kZeros);
+        if (lo == 0u || (zeros & 255u) != 0u) {
+            uint32_t blocks = 0u, least = 0x7C00u;
+            bool fits = true;
+#pragma unroll
+            for (int k = 0; k < DB; ++k) {
+                const uint32_t x = own[k / 2] >> (16 * (k % 2)) & 0x7FFFu;
+                blocks |= x == 0u ? 1u << k : 256u << k;
+                fits = fits && (x == 0u || x >= 0x0400u);
+                least = x == 0u ? least : min(least, x & 0x7C00u);
+            }
+#pragma unroll
+            for (int r = 0; r < LR; ++r) fits = fits && note(kOwn + r) == kNoneSeen;
+            zeros = __reduce_or_sync(0xffffffffu, blocks) | (zeros == 0u && e_least < 16 ? 0xFF00u : zeros);
+            if (!__all_sync(0xffffffffu, fits) || (zeros & zeros >> 8 & 255u) != 0u) return false;
+            lo = __reduce_min_sync(0xffffffffu, least);
+        }
+        const int e_before = min(e_least, (int)note(kLeast));
+        if (max(e_most, (int)(hi >> 10) - 15) - min(e_before, (int)(lo >> 10) - 15) > kRange) return false;
+        note(kZeros, zeros);
+        unless = 0xFFFFu;
+        return true;
+    }
+
+    // PLAIN: a tile that every row sees whole, of finite normal value scales, without a row that is apart; false, with nothing
+    // changed, where it is not. Else any tile; alike: all rows see the same of its tokens.
+    template <bool PLAIN>
+    __device__ __forceinline__ bool tile(uint32_t st, int tok0, bool alike) {
+        constexpr bool MASKED = !PLAIN;
         const int own_row = row_of_lane<KT>(lane);
         const uint32_t codes = st + (uint32_t)(own_row * G::kRow + swizzle<DB>(own_row) * 16);  // chunk k: codes ^ (16 k)
+        uint32_t own[2][DB / 2];  // the scales of this lane's token
+        const uint32_t own_at = st + (uint32_t)(2 * G::kCodes + lane * DB * 2);
+        lds_own<DB / 2>(own_at, own[0]);
+        lds_own<DB / 2>(own_at + G::kScales, own[1]);
         uint32_t kw[DB][4];
 #pragma unroll
         for (int k = 0; k < DB; ++k) ldsm4(codes ^ (uint32_t)(16 * k), kw[k]);
+        const float offset_was = (float)(e_most - 14);
+        bool apart[LR], some_apart = false;
+        if constexpr (PLAIN) {
+            uint32_t most = own[1][0] & 0x7C007C00u, least = most;
+#pragma unroll
+            for (int k = 1; k < DB / 2; ++k) {
+                const uint32_t e = own[1][k] & 0x7C007C00u;
+                most = half_max(most, e), least = half_min(least, e);
+            }
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
+            uint32_t lo = __reduce_min_sync(0xffffffffu, min(least & 0xFFFFu, least >> 16));
+            if (hi >= 0x7C00u || (lo <= unless && !usual(own[1], hi, lo))) return false;
+            const int e_hi = max(e_most, (int)(hi >> 10) - 15), e_lo = min(e_least, (int)(lo >> 10) - 15);
+            if (e_hi - e_lo > kRange) return false;
+            e_most = e_hi, e_least = e_lo;
+        }
+        if constexpr (MASKED) {
+            int hi = -100, lo = 16;  // of this lane's token
+            uint32_t blocks = 0u;
+#pragma unroll
+            for (int k = 0; k < DB; ++k) {
+                const float2 d = to_float2(own[1][k / 2]);
+                const float x = fabsf(k % 2 ? d.y : d.x);
+                blocks |= x == 0.f ? 1u << k : 256u << k;
+                const int e = (int)(__float_as_uint(x) >> 23) - 127;
+                if (x > 0.f && x < INFINITY) hi = max(hi, e), lo = min(lo, e);
+            }
+            uint32_t zeros = note(kZeros), e_own[LR];
+#pragma unroll
+            for (int r = 0; r < LR; ++r) e_own[r] = note(kOwn + r);
+            if (zeros == 0u && e_least < 16) zeros = 0xFF00u;  // so far no zeros
+            if (alike) {
+                const bool seen = tok0 + lane >= seen_lo[0] && tok0 + lane < seen_end[0];
+                e_most = max(e_most, __reduce_max_sync(0xffffffffu, seen ? hi : -100));
+                e_least = min(e_least, __reduce_min_sync(0xffffffffu, seen ? lo : 16));
+                zeros |= __reduce_or_sync(0xffffffffu, seen ? blocks : 0u);
+            } else {  // a token's word in the place of its values' scales
+                sts_word(own_at + G::kScales, (uint32_t)(lo + 64) | blocks << 8);
+                __syncwarp();
+                const auto joined = [](uint32_t a, uint32_t b) { return min(a & 255u, b & 255u) | ((a | b) & ~255u); };
+#pragma unroll
+                for (int j = 0; j < (KT ? 4 : 8); ++j) {
+                    const int in = (KT ? 4 * g : 8 * t4) + j;
+                    uint32_t word[1];
+                    lds_own<1>(st + (uint32_t)(2 * G::kCodes + G::kScales + in * DB * 2), word);
+#pragma unroll
+                    for (int r = 0; r < LR; ++r)
+                        if (tok0 + in >= seen_lo[r] && tok0 + in < seen_end[r]) e_own[r] = joined(e_own[r], word[0]);
+                }
+#pragma unroll
+                for (int r = 0; r < LR; ++r)
+#pragma unroll
+                    for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) e_own[r] = joined(e_own[r], __shfl_xor_sync(0xffffffffu, e_own[r], x));
+            }
+            note(kZeros, zeros);
+            int least = 16;
+#pragma unroll
+            for (int r = 0; r < LR; ++r) {
+                note(kOwn + r, e_own[r]);
+                const uint32_t z = zeros | e_own[r] >> 8;
+                const int e = min(e_least, (int)(e_own[r] & 255u) - 64);
+                apart[r] = !alike || (z & z >> 8 & 255u) != 0u || e_most - e > kRange;
+                some_apart = some_apart || apart[r];
+                least = min(least, (z & z >> 8 & 255u) != 0u || (e_own[r] >> 8 & 255u) != 0u ? kNone : e);
+            }
+            least = __reduce_min_sync(0xffffffffu, least);
+            note(kLeast, (uint32_t)least);
+            if (!alike || (zeros & 255u) != 0u || e_most - least > kRange) unless = 0xFFFFu;
+        }
         // This lane's token's scales become fp32 [K, V][block][token] in the place of the keys' codes, which are in
         // registers now: a lane then reads those of its eight tokens as they are used (converting them where they are used
-        // would take 64 conversions, eight lanes the same ones). Their largest exponent is noted on the way: for all rows, or,
-        // where they differ in what they see, for each token, in the place of its values' scales.
-        const uint32_t exponents = st + (uint32_t)(2 * G::kCodes + G::kScales);  // of token t: + t * DB * 2
-        {
-            uint32_t own[2][DB / 2], m = 0u;
-            const uint32_t at = st + (uint32_t)(2 * G::kCodes + lane * DB * 2);
-            lds_own<DB / 2>(at, own[0]);
-            lds_own<DB / 2>(at + G::kScales, own[1]);
+        // would take 64 conversions, eight lanes the same ones).
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-                for (int k = 0; k < DB / 2; ++k) {
-                    const float2 d = to_float2(own[v][k]);
-                    const uint32_t to = st + (uint32_t)(((v * DB + 2 * k) * 32 + lane) * 4);
-                    sts_word(to, __float_as_uint(d.x));
-                    sts_word(to + 128u, __float_as_uint(d.y));
-                    if (v) {  // the exponents plus one: those of NaN and infinity pass out of the field and count as 0
-                        const uint32_t up = (own[v][k] & 0x7C007C00u) + 0x04000400u;
-                        m = max(m, max(up & 0x7C00u, (up >> 16) & 0x7C00u));
-                    }
-                }
-            if constexpr (MASKED) {
-                sts_word(exponents + (uint32_t)(lane * DB * 2), m);
-            } else {
-                const int e = (int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 16;
-#pragma unroll
-                for (int r = 0; r < LR; ++r) e_run[r] = max(e_run[r], e);
+            for (int k = 0; k < DB / 2; ++k) {
+                const float2 d = to_float2(own[v][k]);
+                const uint32_t to = st + (uint32_t)(((v * DB + 2 * k) * 32 + lane) * 4);
+                sts_word(to, __float_as_uint(d.x));
+                sts_word(to + 128u, __float_as_uint(d.y));
             }
-            __syncwarp();
-        }
+        __syncwarp();
         // of block k: + 128 k, of the values' blocks + 128 (DB + k)
         const uint32_t scales = st + (uint32_t)(KT ? 16 * g : 32 * t4);
         // scores, in pairs that an instruction leaves side by side: sc[n][j] and sc[n][j + 1], j even, are of row g of group n
@@ -493,31 +622,23 @@ struct Rows {
         // row r of a lane (r < LR) has the scores sc[KT ? 0 : r][KT ? 2 j + r : j], j < PER
         constexpr int PER = KT ? 4 : 8;
         auto score = [&](int r, int j) -> float& { return sc[KT ? 0 : r][KT ? 2 * j + r : j]; };
-        bool moved = false;
-        float keep[LR];
         uint32_t seen[LR];  // bit j
 #pragma unroll
         for (int r = 0; r < LR; ++r) seen[r] = 0u;
         if constexpr (MASKED) {
-            uint32_t e[LR] = {};
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int in = (KT ? 4 * g : 8 * t4) + j, t = tok0 + in;
-                uint32_t of_token[1];
-                lds_own<1>(exponents + (uint32_t)(in * DB * 2), of_token);
 #pragma unroll
                 for (int r = 0; r < LR; ++r) {
-                    if (t >= seen_lo[r] && t < seen_end[r]) seen[r] |= 1u << j, e[r] = max(e[r], of_token[0]);
+                    if (t >= seen_lo[r] && t < seen_end[r]) seen[r] |= 1u << j;
                     else score(r, j) = -INFINITY;
                 }
             }
-#pragma unroll
-            for (int r = 0; r < LR; ++r) {
-#pragma unroll
-                for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) e[r] = max(e[r], __shfl_xor_sync(0xffffffffu, e[r], x));
-                e_run[r] = max(e_run[r], (int)(e[r] >> 10) - 16);
-            }
         }
+        const float offset = (float)(e_most - 14);
+        float keep[LR], ref[LR];
+        bool moved = false;
 #pragma unroll
         for (int r = 0; r < LR; ++r) {
             float m = score(r, 0);
@@ -525,16 +646,15 @@ struct Rows {
             for (int j = 1; j < PER; ++j) m = fmaxf(m, score(r, j));
 #pragma unroll
             for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            const float nt = fmaxf(top[r], m * factor[r]);
-            const float nr = (nt == -INFINITY ? 0.f : nt) + (float)(e_run[r] - 14);
-            keep[r] = top[r] == -INFINITY ? 1.f : ex2(ref[r] - nr);  // nothing to keep before the first token
-            moved = moved || nr != ref[r];
-            top[r] = nt;
-            ref[r] = nr;
+            const float was = top[r] + offset_was;
+            top[r] = fmaxf(top[r], m * factor[r]);
+            ref[r] = top[r] + offset;
+            keep[r] = was - ref[r];
+            moved = moved || was != ref[r];
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int r = 0; r < LR; ++r) l[r] *= keep[r];
+            for (int r = 0; r < LR; ++r) keep[r] = ex2(keep[r]), l[r] *= keep[r];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float ka, kb;
@@ -551,7 +671,15 @@ struct Rows {
                 }
             }
         }
-        // weights in the place of the scores; a token that is not seen weighs nothing (also where the query is not finite)
+        weights<MASKED>(sc, seen, ref);
+        if (MASKED && __any_sync(0xffffffffu, some_apart)) values<MASKED, MASKED>(codes, scales, sc, seen, apart);
+        else values<MASKED, false>(codes, scales, sc, seen, apart);
+        return true;
+    }
+
+    // Weights in the place of the scores; a token that is not seen weighs nothing (also where the query is not finite).
+    template <bool MASKED>
+    __device__ __forceinline__ void weights(float (&sc)[NT][8], const uint32_t (&seen)[LR], const float (&ref)[LR]) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r0 = KT ? 0 : n, r1 = KT ? 1 : n;
@@ -568,7 +696,13 @@ struct Rows {
             if constexpr (KT) l[0] += sum.x, l[1] += sum.y;
             else l[n] += sum.x + sum.y;
         }
+    }
 
+    // The weights sc of a tile times its values, added to the outputs. APART: for a row that is apart the tile's largest term
+    // in each block is brought to 2^14, and the products are summed from zero and brought back; other rows keep their bits.
+    template <bool MASKED, bool APART>
+    __device__ __forceinline__ void values(uint32_t codes, uint32_t scales, const float (&sc)[NT][8], const uint32_t (&seen)[LR],
+                                           const bool (&apart)[LR]) {
 #pragma unroll
         for (int k = 0; k < DB; ++k) {
             uint32_t w[4], x[4][4];
@@ -585,18 +719,43 @@ struct Rows {
             } else {
                 lds_floats(scales + (uint32_t)(128 * (DB + k)), vd);
             }
+            auto term = [&](int n, int j) {
+                const int r0 = KT ? 0 : n, r1 = KT ? 1 : n;
+                float2 y = __fmul2_rn(make_float2(sc[n][2 * j], sc[n][2 * j + 1]), make_float2(vd[2 * j], vd[2 * j + 1]));
+                if constexpr (MASKED) {  // a masked token's scale may be anything
+                    if (!(seen[r0] >> (KT ? j : 2 * j) & 1u)) y.x = 0.f;
+                    if (!(seen[r1] >> (KT ? j : 2 * j + 1) & 1u)) y.y = 0.f;
+                }
+                return y;
+            };
+            float up[LR], down[LR];  // APART: the row's powers of two; down 0: it is not apart
+            if constexpr (APART) {
+#pragma unroll
+                for (int r = 0; r < LR; ++r) up[r] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = term(n, j);
+                        const int r0 = KT ? 0 : n, r1 = KT ? 1 : n;
+                        up[r0] = fmaxf(up[r0], fabsf(y.x)), up[r1] = fmaxf(up[r1], fabsf(y.y));
+                    }
+#pragma unroll
+                for (int r = 0; r < LR; ++r) {
+#pragma unroll
+                    for (int x = KT ? 4 : 1; x <= (KT ? 16 : 2); x <<= 1) up[r] = fmaxf(up[r], __shfl_xor_sync(0xffffffffu, up[r], x));
+                    const int e = max((int)(__float_as_uint(up[r]) >> 23), 30) - 127;  // below 2^-97 nothing is left to keep
+                    up[r] = apart[r] ? pow2i(14 - e) : 1.f;
+                    down[r] = apart[r] ? pow2i(e - 14) : 0.f;
+                }
+            }
             uint32_t hi[NT][4], lo[SPLIT ? NT : 1][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 d = make_float2(vd[2 * j], vd[2 * j + 1]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const int r0 = KT ? 0 : n, r1 = KT ? 1 : n;
-                    float2 y = __fmul2_rn(make_float2(sc[n][2 * j], sc[n][2 * j + 1]), d);
-                    if constexpr (MASKED) {  // a masked token's scale may be anything
-                        if (!(seen[r0] >> (KT ? j : 2 * j) & 1u)) y.x = 0.f;
-                        if (!(seen[r1] >> (KT ? j : 2 * j + 1) & 1u)) y.y = 0.f;
-                    }
+                    float2 y = term(n, j);
+                    if constexpr (APART) y = __fmul2_rn(y, make_float2(up[KT ? 0 : n], up[KT ? 1 : n]));
                     hi[n][j] = pack_half2(y.x, y.y);
                     if constexpr (KT) hi[n][j] = turned_over(hi[n][j]);
                     if constexpr (SPLIT) {
@@ -605,33 +764,56 @@ struct Rows {
                     }
                 }
             }
+            const uint32_t rows[2][2][4] = {{{x[0][0], x[0][1], x[1][0], x[1][1]}, {x[0][2], x[0][3], x[1][2], x[1][3]}},
+                                            {{x[2][0], x[2][1], x[3][0], x[3][1]}, {x[2][2], x[2][3], x[3][2], x[3][3]}}};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t a0[4] = {x[2 * u][0], x[2 * u][1], x[2 * u + 1][0], x[2 * u + 1][1]};
-                const uint32_t a1[4] = {x[2 * u][2], x[2 * u][3], x[2 * u + 1][2], x[2 * u + 1][3]};
+            for (int n = 0; n < NT; ++n) {
+                auto add = [&](float (&to)[2][4]) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma(o[n][k][0], a0, hi[n][2 * u], hi[n][2 * u + 1], o[n][k][0]);
-                    mma(o[n][k][1], a1, hi[n][2 * u], hi[n][2 * u + 1], o[n][k][1]);
-                    if constexpr (SPLIT) {
-                        mma(o[n][k][0], a0, lo[n][2 * u], lo[n][2 * u + 1], o[n][k][0]);
-                        mma(o[n][k][1], a1, lo[n][2 * u], lo[n][2 * u + 1], o[n][k][1]);
+                    for (int u = 0; u < 2; ++u) {
+                        mma(to[0], rows[u][0], hi[n][2 * u], hi[n][2 * u + 1], to[0]);
+                        mma(to[1], rows[u][1], hi[n][2 * u], hi[n][2 * u + 1], to[1]);
+                        if constexpr (SPLIT) {
+                            mma(to[0], rows[u][0], lo[n][2 * u], lo[n][2 * u + 1], to[0]);
+                            mma(to[1], rows[u][1], lo[n][2 * u], lo[n][2 * u + 1], to[1]);
+                        }
                     }
+                };
+                if constexpr (APART) {
+                    float from[2];  // of rows 2 t4, 2 t4 + 1, which the outputs are of
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) from[i] = KT ? down[KT ? i : 0] : __shfl_sync(0xffffffffu, down[KT ? 0 : n], 8 * t4 + 4 * i);
+                    float sum[2][4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sum[j][c] = from[c % 2] == 0.f ? o[n][k][j][c] : 0.f;
+                    add(sum);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            o[n][k][j][c] = from[c % 2] == 0.f ? sum[j][c] : fmaf(sum[j][c], from[c % 2], o[n][k][j][c]);
+                } else {
+                    add(o[n][k]);
                 }
             }
         }
     }
 
     // Row g's sum over the whole warp, and its reference: -infinity where it saw nothing. bad: NaN, whatever was seen.
-    __device__ __forceinline__ void finish(bool bad) {
+    __device__ __forceinline__ void finish(bool bad, float (&ref)[NT]) {
+        float of[LR];
+#pragma unroll
+        for (int r = 0; r < LR; ++r) of[r] = top[r] + (float)(e_most - 14);
         if constexpr (KT) {  // from rows 2 t4, 2 t4 + 1 back to row g
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int x = 4; x <= 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
             const float l0 = __shfl_sync(0xffffffffu, l[0], g >> 1), l1 = __shfl_sync(0xffffffffu, l[1], g >> 1);
-            const float r0 = __shfl_sync(0xffffffffu, ref[0], g >> 1), r1 = __shfl_sync(0xffffffffu, ref[1], g >> 1);
-            l[0] = g & 1 ? l1 : l0, ref[0] = g & 1 ? r1 : r0;
+            const float r0 = __shfl_sync(0xffffffffu, of[0], g >> 1), r1 = __shfl_sync(0xffffffffu, of[1], g >> 1);
+            l[0] = g & 1 ? l1 : l0, of[0] = g & 1 ? r1 : r0;
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -639,8 +821,8 @@ struct Rows {
                 l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
                 l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
             }
+            ref[n] = l[n] == 0.f ? -INFINITY : of[n];
             if (bad) l[n] = qnan(), ref[n] = 0.f;
-            else if (l[n] == 0.f) ref[n] = -INFINITY;
         }
     }
 
@@ -801,13 +983,14 @@ kv4_attention_items_kernel(const Params p) {
     }
     cp_async_wait<0>();
     bad = __any_sync(0xffffffffu, bad) != 0;
-    w.finish(bad);
+    float ref[NT];
+    w.finish(bad, ref);
     if (bad && w.lane == 0) atomicOr(a.fault, s.bad ? (unsigned)kFaultBadLength : (unsigned)kFaultBadPage);
     __syncthreads();  // every warp's stages are free: the join uses their memory
     float* jo = reinterpret_cast<float*>(ring_memory);
     if (w.t4 == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) join_l[warp][8 * n + w.g] = w.l[n], join_ref[warp][8 * n + w.g] = w.ref[n];
+        for (int n = 0; n < NT; ++n) join_l[warp][8 * n + w.g] = w.l[n], join_ref[warp][8 * n + w.g] = ref[n];
     }
     w.each_pair([&](int n, int i, int e, float2 v) {
         *reinterpret_cast<float2*>(jo + (warp * ROWS + 8 * n + 2 * w.t4 + i) * G::kJoinRow + e) = v;
@@ -1003,14 +1186,15 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
         }
         const int b = use.b, h = use.item / p.chunks, row0 = (use.item - h * p.chunks) * ROWS;
         bad = __any_sync(0xffffffffu, bad) != 0;
-        w.finish(bad);
+        float ref[NT];
+        w.finish(bad, ref);
         if (bad && w.lane == 0) atomicOr(a.fault, use.s.bad ? (unsigned)kFaultBadLength : (unsigned)kFaultBadPage);
         if (use.count == use.s.tiles) {  // the whole item: its outputs
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float inv = w.l[n] == 0.f ? 0.f : 1.f / w.l[n];
                 const int r = row0 + 8 * n + w.g;
-                if (a.lse && w.t4 == 0 && r < p.R) a.lse[lse_at(p, b, h, r)] = lse_of(w.ref[n], w.l[n]);
+                if (a.lse && w.t4 == 0 && r < p.R) a.lse[lse_at(p, b, h, r)] = lse_of(ref[n], w.l[n]);
                 w.l[n] = inv;
             }
             long long to[NT][2];
@@ -1039,7 +1223,7 @@ __global__ void __launch_bounds__(Plan<DB, NT, SPLIT>::kWarps * 32, 1) kv4_atten
             if (w.t4 == 0) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    part[ROWS * D + 8 * n + w.g] = w.ref[n], part[ROWS * D + ROWS + 8 * n + w.g] = w.l[n];
+                    part[ROWS * D + 8 * n + w.g] = ref[n], part[ROWS * D + ROWS + 8 * n + w.g] = w.l[n];
             }
             w.each_pair([&](int n, int i, int e, float2 v) {
                 const int r = 8 * n + 2 * w.t4 + i;
