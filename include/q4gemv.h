@@ -261,8 +261,9 @@ int kv4_read(void *k_out, void *v_out, const kv4_cache *cache, const int32_t *sl
  *   int32[B][max_pages], seq_lens int32[B] (device). 1 <= M <= 16; 1 <= B <= 1024; head_dim 64, 128 or 256;
  *   Hq a multiple of num_kv_heads; 0 < scale <= 1e30; max_pages * page_size <= 2^30.
  *   A sequence whose length is outside [0, max_pages * page_size], or that reads a page id outside [0, num_pages), gets
- *   NaN rows, and Q4_FAULT_BAD_LENGTH or Q4_FAULT_BAD_PAGE is recorded. A query row that holds a NaN or an infinity
- *   gives NaN.
+ *   NaN rows, and Q4_FAULT_BAD_LENGTH or Q4_FAULT_BAD_PAGE is recorded. A query row that holds a NaN or an infinity,
+ *   or has a score (scale * q . k, times log2 e) above fp32's range, gives NaN; scores below its range count as minus
+ *   infinity.
  *   workspace: device memory, 16-byte aligned, of at least the bytes that kv4_attention_workspace states for these
  *   sizes on the current device (whatever B and the lengths); its contents do not matter before or after. Calls that
  *   may run at the same time need a workspace each.

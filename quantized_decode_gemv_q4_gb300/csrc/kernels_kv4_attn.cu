@@ -801,7 +801,8 @@ struct Rows {
         }
     }
 
-    // Row g's sum over the whole warp, and its reference: -infinity where it saw nothing. bad: NaN, whatever was seen.
+    // Row g's sum over the whole warp, and its reference: -infinity where it saw nothing. NaN where a score was above fp32's
+    // range (every weight under an infinite reference is 0), and whatever was seen if bad.
     __device__ __forceinline__ void finish(bool bad, float (&ref)[NT]) {
         float of[LR];
 #pragma unroll
@@ -822,7 +823,7 @@ struct Rows {
                 l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
             }
             ref[n] = l[n] == 0.f ? -INFINITY : of[n];
-            if (bad) l[n] = qnan(), ref[n] = 0.f;
+            if (bad || of[n] == INFINITY) l[n] = qnan(), ref[n] = 0.f;
         }
     }
 

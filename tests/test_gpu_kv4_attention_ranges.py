@@ -201,3 +201,24 @@ def test_a_crowd_of_items_of_two_row_groups(dtype):
     out, lse = c.run()
     c.check(out, lse)
     check(c, out)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("spare", [1, 800])
+@pytest.mark.parametrize("group", [1, 12])
+def test_scores_above_the_range_of_fp32_give_nan(group, spare, dtype):
+    """In out and in lse, however the work is divided; other queries are as they were."""
+    c = Case([90, 200], 2, 2 * group, 2, 64, 16, dtype, spare=spare, scale=0.125)
+    positive(c)
+    put_key(c, 1, 70, 1.0)
+    c.upload()
+    out, lse = c.run()
+    check(c, out)
+    c.q[1, 1, 1] *= 3e37
+    put = c.table[1][70 // 16], slice(None), 70 % 16
+    c.k_d[put] = 60000.0  # a score of 1e44 and more for that query
+    c.upload()
+    got, got_lse = c.run()
+    assert torch.isnan(got[1, 1, 1]).all() and torch.isnan(got_lse[1, 1, 1])
+    assert torch.equal(got[0], out[0]) and torch.equal(got_lse[0], lse[0])
+    assert torch.isfinite(got[1, 0]).all() and torch.isfinite(got[1, 1, 0]).all()
