@@ -351,6 +351,8 @@ class KV4Cache:
         if v_qs.shape != k_qs.shape or half % 16 or any(tuple(t.shape) != (pages, heads, page, half // 16) for t in (k_d, v_d)):
             raise ValueError("the codes must be [num_pages, num_kv_heads, page_size, head_dim/2] and the scales "
                              "[num_pages, num_kv_heads, page_size, head_dim/32], head_dim a multiple of 32")
+        if pages * heads * page > 0x7FFFFFFF:
+            raise ValueError("a cache holds at most 2^31 - 1 rows")
         if any(t.device != k_qs.device for t in (k_d, v_qs, v_d)):
             raise ValueError("the cache's tensors must be on one device")
         struct = KV4Cache._Struct(_ptr(k_qs, torch.uint8, "k_qs"), _ptr(k_d, torch.float16, "k_d"),
@@ -555,8 +557,8 @@ def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float |
     size = workspace.numel()
     _call(load().kv4_attention, dev, op, None if lse is None else _flat(lse, torch.float32, dev, "lse", B * M * Hq), qp,
           cache._ref, _flat(block_table, torch.int32, dev, "block_table", B * table_shape[1]),
-          _flat(seq_lens, torch.int32, dev, "seq_lens", B), B, M, Hq, table_shape[1], qs, os_,
-          D ** -0.5 if scale is None else scale, window, code, _flat(workspace, torch.uint8, dev, "workspace", size), size,
+          _flat(seq_lens, torch.int32, dev, "seq_lens", B), B, M, Hq, min(table_shape[1], 0x7FFFFFFF), qs, os_,
+          D ** -0.5 if scale is None else scale, max(-1, min(window, 0x7FFFFFFF)), code, _flat(workspace, torch.uint8, dev, "workspace", size), size,
           _stream_on(dev, stream))
 
 

@@ -222,3 +222,15 @@ def test_scores_above_the_range_of_fp32_give_nan(group, spare, dtype):
     assert torch.isnan(got[1, 1, 1]).all() and torch.isnan(got_lse[1, 1, 1])
     assert torch.equal(got[0], out[0]) and torch.equal(got_lse[0], lse[0])
     assert torch.isfinite(got[1, 0]).all() and torch.isfinite(got[1, 1, 0]).all()
+
+
+def test_windows_past_the_c_abi_s_integers():
+    c = Case([40, 300], 2, 4, 2, 64, 16, F32)
+    out, _ = c.run()
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 70):
+        c.window = window
+        assert torch.equal(c.run()[0], out)
+    for window in (-1, -2 ** 32 + 5, -2 ** 40):
+        c.window = window
+        with pytest.raises(q4.Q4Error, match="window"):
+            c.run()

@@ -138,3 +138,11 @@ def test_token_rows():
             rows(bad)
     with pytest.raises(TypeError):
         q4._rows(base, 320, torch.float16, -1, "t")
+
+
+def test_a_cache_of_too_many_rows_is_refused_by_the_binding():
+    """Sizes past 32 bits, which the struct would take modulo 2^32."""
+    for pages in (1 << 26, (1 << 32) + 4):
+        qs, d = (torch.empty(pages, 2, 16, n, dtype=t, device="meta") for n, t in ((32, torch.uint8), (2, torch.float16)))
+        with pytest.raises(ValueError, match="rows"):
+            q4.KV4Cache(qs, d, qs, d)
