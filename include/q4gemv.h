@@ -193,10 +193,11 @@ int moe_router_q4(int32_t *expert_ids, float *expert_weights, float *logits, con
  * ---- Between two projections of a decode step: q/k norm and rotation, the 4-bit cache, attention over it ----
  * (No counterpart in the source pages, whose kernels end at the projections.)
  *
- * Activations here are fp32, fp16 or bf16 (`dtype`, the same for every activation of a call); sums, statistics and
- * products are fp32 or wider in effect, and values are rounded to the type once, when they are stored. A tensor of T
- * tokens is rows of heads * D contiguous elements, `stride` elements from one token's row to the next (so q, k and v
- * may be columns of one projection output); every row must be 16-byte aligned.
+ * Activations here are fp32, fp16 or bf16 (`dtype`, the same for every activation of a call); sums and statistics are
+ * fp32, and values are rounded to the type once, when they are stored. (One product is narrower: kv4_attention rounds a
+ * softmax weight times its value's scale to one fp16 for 16-bit types, 2^-11 of it, and to two, 2^-22, for fp32.) A
+ * tensor of T tokens is rows of heads * D contiguous elements, `stride` elements from one token's row to the next (so q,
+ * k and v may be columns of one projection output); every row must be 16-byte aligned.
  */
 enum { Q4_F32 = 0, Q4_F16 = 1, Q4_BF16 = 2 };
 
@@ -208,6 +209,7 @@ enum { Q4_F32 = 0, Q4_F16 = 1, Q4_BF16 = 2 };
  *   q, q_out [T][Hq][D], k, k_out [T][Hkv][D]; an output may be its input (same pointer and stride) or must not overlap
  *   any input; q_gamma, k_gamma float[D] or NULL; cos_sin float[max_pos][rot_dim]: row p holds cos for the rot_dim / 2
  *   pairs, then sin; positions int32[T] (device). gamma and cos_sin 16-byte aligned.
+ *   The sum of squares is fp32: elements beyond about 1e18, or all below 1e-19 with an eps below 1e-38, leave its range.
  *   D a multiple of 32 up to 256; T * (Hq + Hkv) < 2^31; rot_dim a multiple of 16, 0..D (0: no rotation, cos_sin and positions unused).
  *   A token whose position is outside [0, max_pos) gets NaN heads and Q4_FAULT_BAD_POSITION is recorded.
  */
@@ -267,6 +269,7 @@ int kv4_read(void *k_out, void *v_out, const kv4_cache *cache, const int32_t *sl
  *   workspace: device memory, 16-byte aligned, of at least the bytes that kv4_attention_workspace states for these
  *   sizes on the current device (whatever B and the lengths); its contents do not matter before or after. Calls that
  *   may run at the same time need a workspace each.
+ *   A query element is held to 2^-34 of its row's largest (an fp32 one to 2^-22 of itself where that is more).
  *   The work is divided by the lengths of all sequences of the call, so a sequence's result may differ in the last bits
  *   when it is computed in another batch; the same call gives the same bits.
  */

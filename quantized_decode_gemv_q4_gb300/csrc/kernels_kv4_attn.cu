@@ -2,7 +2,7 @@
 //
 // Query m of a sequence of length n sits at position p = n - M + m and sees the tokens max(0, p + 1 - window) .. p
 // (window 0: all): out = sum_t softmax_t(scale q . k_t) v_t. The queries that share a key head (group * M rows) read
-// each of its cached rows once.
+// and decode each of its cached rows once for every 16 of them (8 at head size 256).
 //
 // Arithmetic. Both products run on m16n8k16 matrix instructions over the codes themselves: a 4-bit code at bits 0-3 of a
 // half ORed with the pattern of 1024 is 1024 + code, at bits 4-7 it is 1024 + 16 code, and one packed subtraction leaves
@@ -10,16 +10,18 @@
 // bare codes as f16 subnormals need no subtraction, but the matrix unit aligns its products by the operands' unnormalised
 // exponents and keeps 7 bits less: scores 2^-17 off instead of 2^-24.) A block's scale multiplies the fp32 sum of its 32
 // products (keys) or the softmax weight (values), so what is rounded to f16 is only
-//   - q, scaled to the row's largest magnitude: exact for f16 and bf16 queries, and for fp32 queries split into a high
-//     and a low f16 part (22 bits) that fill the two halves of the instruction's 16 rows;
+//   - q, scaled to the row's largest magnitude: f16 and bf16 queries as they are, fp32 queries split into a high and a low
+//     f16 part (22 bits) that fill the two halves of the instruction's 16 rows. Elements far below the largest meet f16's last
+//     step and are off by up to 2^-34 of the largest, which a score's own roundings exceed unless a token's key scales differ
+//     by more than 2^14;
 //   - the weight times its value scale, a term: one f16 for 16-bit outputs (half a step: 2^-11 of it), a high and a low part
 //     (2^-22) for fp32.
 // Scores, running maximum, running sum and outputs are fp32. The reference that the exponentials subtract is the row's
 // running maximum plus the exponent of the largest value scale so far, so that the largest terms lie below 2^15. Scales that
-// differ by up to 2^10 leave the row's largest term in every block at 2^4 or above; what f16 loses below its step of 2^-24 is then,
-// over n tokens, at most n 2^-29 of it, less than the roundings of an fp32 sum of n. A row that has seen scales further apart
-// (or some zeros; and every row in a tile of which the rows of a warp see different tokens) is `apart`: its terms are
-// scaled by the tile's own largest one in each block. Tokens that a row does not see change none of its bits.
+// differ by up to 2^10 leave the row's largest term in every block at 2^4 or above; what f16 loses below its step of 2^-24
+// is then, over n tokens, at most n 2^-29 of it, less than the roundings of an fp32 sum of n. A row that has seen scales
+// further apart (or some zeros; and every row in a tile of which the rows of a warp see different tokens) is `apart`: its
+// terms are scaled by the tile's own largest one in each block. Tokens that a row does not see change none of its bits.
 //
 // Work. A warp takes tiles of 32 tokens, streamed by cp.async into its own ring of shared-memory stages (16-byte chunks
 // XOR-swizzled so that ldmatrix is free of bank conflicts; ldmatrix delivers the keys' words in the layout of a column
@@ -289,7 +291,7 @@ __device__ __forceinline__ uint32_t half_min(uint32_t a, uint32_t b) {
 // operand and the keys its columns, and the scores lie as the values' instruction wants the weights. A single group of
 // 16-bit queries would fill half of it; there (KT) the keys are the rows and the 8 queries the columns, half as many
 // instructions and fewer registers, and movmatrix turns the weights over (64 ragged sequences 74 us with the queries as
-// rows, 70 us so and with 16 warps; one of 131001 tokens 41 and 38 us).
+// rows, 70 us so and with 16 warps; one of 131001 tokens 41 and 38 us; both sides before rows could be apart).
 template <int DB, int NT, bool SPLIT>
 struct Rows {
     using G = Geo<DB>;
@@ -1333,13 +1335,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_attention_join_kernel(const 
 // Groups of 8 rows that a warp holds: two where there are more than 8 rows and the outputs fit the registers.
 int row_groups(int M, int group, int D) { return M * group > 8 && D < 256 ? 2 : 1; }
 
-// Items (whole, or split evenly over up to two CTAs an SM, 256 tokens each at least) where the page table and the window let
-// no sequence read more than kItemTokens, for a single sequence, and for few items of up to kSplitTokens; streams otherwise.
+// Items (whole, or split evenly over up to two CTAs an SM, one for every 256 tokens that the page table or the window admits)
+// where the page table and the window let no sequence read more than kItemTokens, for a single sequence, and for few items of
+// up to kSplitTokens; streams otherwise. The host knows what is admitted, not the lengths: a table much wider than its
+// sequence costs CTAs without a tile, and the join (one sequence of 100 tokens, fp32, 4 key heads of 128: 5.7 us behind a table
+// for 128 tokens, 6.9, 7.6 and 8.5 us behind one for 2,048, 16,384 and 131,072; of 16,384 tokens 9.8 and, for 131,072, 10.9).
 // The streams' scan, their second launch and its join cost 5 to 8 us more than a launch of whole items, and do not mind the
 // lengths, where the CTAs with the longest of ragged items are waited for. 8 key heads of 128, bf16, items and streams: 8
-// sequences of 100 tokens 6.2 and 14.2 us, of 1500 tokens 11 and 16 us; 64 of 1000 tokens 25 and 29 us; 64 with a window of
-// 512 tokens 16 and 22 us; one of 131001 tokens 37 and 45 us; 64 ragged ones up to 2000 tokens 33 and 30 us, up to 8192
-// tokens 107 and 69 us.
+// sequences of 100 tokens 6.3 and 14.2 us, of 1500 tokens 11 and 16 us; 64 of 1000 tokens 25 and 29 us; 64 with a window of
+// 512 tokens 16 and 22 us; one of 131001 tokens 38 and 46 us; 64 ragged ones up to 2000 tokens 33 and 30 us, up to 8192
+// tokens 107 and 71 us.
 constexpr long long kItemTokens = 1024;
 constexpr long long kSplitTokens = 8192;
 
@@ -1420,8 +1425,8 @@ cudaError_t launch_kv4_attention(const KvAttnArgs& a, void* workspace, const Dev
                     dim3((unsigned)(items * p.splits), (unsigned)a.B), I::kWarps * 32, kRing, di, s, p);
             };
             // more CTAs than two an SM run in kMany where 128 registers do; from eight an SM on, CTAs of two warps take over,
-            // each warp with twice the tiles and half the starts: 256 sequences of 64 tokens 21 and 14 us, of 300 tokens 33 and
-            // 27 us, but 64 sequences of 200 tokens 9.8 and 10.7 us (8 key heads of 128, bf16)
+            // each warp with twice the tiles and half the starts: 256 sequences of 64 tokens 21 and 15 us, of 300 tokens 33 and
+            // 28 us, but 64 sequences of 200 tokens 10.1 and 10.7 us (8 key heads of 128, bf16)
             constexpr bool kFour = DB == 2 || (DB == 4 && NT == 1);
             const long long ctas = call_items * p.splits;
             cudaError_t e;
