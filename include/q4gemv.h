@@ -71,7 +71,7 @@ enum {
 
 /* Fault bits reported by q4_device_faults. */
 enum {
-    Q4_FAULT_BAD_EXPERT = 4,   /* moe_q4_gemv or moe_q4_pure_read saw an expert id outside [0, E) */
+    Q4_FAULT_BAD_EXPERT = 4,   /* moe_q4_gemv, moe_q4_pure_read or moe_q4_down_gemv saw an expert id outside [0, E) */
     Q4_FAULT_WAIT_TIMEOUT = 8, /* a wait for a weight stage ran out of its cycle limit (rows written as NaN) */
     Q4_FAULT_COPY_LOST = 16,   /* even the final wait for a warp's issued copies ran out (not seen in practice) */
     Q4_FAULT_BAD_SLOT = 32,    /* kv4_write or kv4_read saw a slot >= num_pages * page_size */
@@ -277,6 +277,80 @@ int kv4_attention_workspace(size_t *bytes, int M, int Hq, int Hkv, int D, int dt
 int kv4_attention(void *out, float *lse, const void *q, const kv4_cache *cache, const int32_t *block_table,
                   const int32_t *seq_lens, int B, int M, int Hq, int max_pages, long long q_stride, long long out_stride,
                   float scale, int window, int dtype, void *workspace, size_t workspace_bytes, q4_stream_t stream);
+
+/*
+ * ---- Around and inside a mixture-of-experts block ----
+ * (No counterpart in the source pages.) Activations as in the section above: Q4_F32, Q4_F16 or Q4_BF16, rows of a token
+ * `stride` elements apart and 16-byte aligned, fp32 sums, one rounding when a value is stored.
+ *
+ * residual_norm: the norm behind a block, its gate and scales, the residual sum and the norm before the next block.
+ *   b = x (post_gamma NULL) or x_i * post_gamma_i / sqrt(sum_j x_j^2 / K + eps);
+ *   h = residual_scale * residual + branch_scale * gate * b;  y = h_i * pre_gamma_i / sqrt(sum_j h_j^2 / K + eps).
+ *   h_out [T][K]; y_out [T][K], NULL exactly when pre_gamma is NULL; x [T][K]; residual [T][K] or NULL (no such term);
+ *   gate NULL (1), or with gate_width K [T][K], with gate_width 1 [T] (a number per token; any alignment of its type), rows
+ *   gate_stride elements apart (0: the same for every token); post_gamma, pre_gamma float[K] or NULL (16-byte aligned).
+ *   y follows from the fp32 h, not from the stored one. h_out or y_out may be x or residual (same pointer and stride), and
+ *   must otherwise not overlap an input or each other.
+ *   T >= 1; K a multiple of 8 up to 32768; the scales finite. The sums of squares are fp32: elements beyond about 1e17, or
+ *   all below 1e-19 with an eps below 1e-38, leave its range.
+ */
+int residual_norm(void *h_out, void *y_out, const void *x, const void *residual, const float *post_gamma, const void *gate,
+                  const float *pre_gamma, float eps, float residual_scale, float branch_scale, int T, int K, int gate_width,
+                  long long h_out_stride, long long y_out_stride, long long x_stride, long long residual_stride,
+                  long long gate_stride, int dtype, q4_stream_t stream);
+
+/*
+ * moe_q4_down_gemv: the down projections of the selected experts and their weighted sum, behind moe_q4_swiglu_gemv.
+ *   out[t][n] = residual[t][n] + sum_{s < topk} expert_weights[t][s] * sum_k W[e*N + n][k] * h[t][s][k],
+ *   e = expert_ids[t*topk + s]. Each selected expert's rows are read once for up to 16 (of long rows: 8) of its slots.
+ *   out [T][N]; residual [T][N] or NULL, which out may be (same pointer and stride); qs uint8[E*N][K/32][16], d
+ *   uint16[E*N][K/32]; h float[T][topk][K] (16-byte aligned); expert_ids int32[T][topk], expert_weights float[T][topk]
+ *   (device). 1 <= topk <= E; T*topk <= 512; N a multiple of 8; K % 32 == 0, K <= 65536; E*N < 2^31.
+ *   A token with an id outside [0, E) gets a NaN row; Q4_FAULT_BAD_EXPERT is recorded and, when dev_status is not NULL,
+ *   stored there. An expert may be given twice to a token.
+ *   workspace: as for kv4_attention, of at least the bytes that moe_q4_down_workspace states for these sizes.
+ *   A slot whose h holds a NaN or an infinity makes its token's row NaN. An element of h is held to 2^-33 of its slot's
+ *   largest (or to 2^-22 of itself where that is more).
+ */
+int moe_q4_down_workspace(size_t *bytes, int T, int topk, int N, int K);
+int moe_q4_down_gemv(void *out, const uint8_t *qs, const uint16_t *d, const float *h, const int32_t *expert_ids,
+                     const float *expert_weights, const void *residual, int T, int topk, int E, int N, int K,
+                     long long out_stride, long long residual_stride, int dtype, int32_t *dev_status, void *workspace,
+                     size_t workspace_bytes, q4_stream_t stream);
+
+/*
+ * A mixture-of-experts layer's weights in planar Q4: router uint8[E][K/32][16] and uint16[E][K/32]; gate and up E*N rows of
+ * K weights, down E*K rows of N weights (codes 16-byte aligned). Device memory of the caller; the struct itself is host
+ * memory and is copied by the call.
+ */
+typedef struct {
+    const uint8_t *router_qs;
+    const uint16_t *router_d;
+    const uint8_t *gate_qs;
+    const uint16_t *gate_d;
+    const uint8_t *up_qs;
+    const uint16_t *up_d;
+    const uint8_t *down_qs;
+    const uint16_t *down_d;
+    int E, N, K;
+} moe_q4_weights;
+
+/*
+ * moe_q4_layer: the whole layer for T tokens.
+ *   xn = x (gamma NULL) or its RMSNorm x_i * gamma_i / sqrt(sum_j x_j^2 / K + eps), in fp32; the router, its ties and
+ *   weights as moe_router_q4 on xn; h = silu(Wg xn) * (Wu xn) of each pick, in fp32; out = residual + sum of weight * Wd h.
+ *   out, x [T][K]; residual [T][K] or NULL. out may be x or residual, residual may be x (same pointers and strides).
+ *   expert_ids int32[T][topk], expert_weights float[T][topk]: the picks, each written when not NULL.
+ *   1 <= topk <= E <= 4096; T*topk <= 512; N % 32 == 0, N <= 65536; K % 32 == 0, K <= 32768; E*N, E*K < 2^31.
+ *   A token whose x, logits or h hold a NaN or an infinity gets a NaN row (its ids are valid all the same); no other token
+ *   is touched. workspace: as above, of the bytes that moe_q4_layer_workspace states; x and h are held as h is in
+ *   moe_q4_down_gemv.
+ */
+int moe_q4_layer_workspace(size_t *bytes, int T, int topk, int E, int N, int K);
+int moe_q4_layer(void *out, const void *x, const moe_q4_weights *weights, const float *gamma, float eps, const void *residual,
+                 int32_t *expert_ids, float *expert_weights, int T, int topk, int normalize, long long out_stride,
+                 long long x_stride, long long residual_stride, int dtype, void *workspace, size_t workspace_bytes,
+                 q4_stream_t stream);
 
 /*
  * Pure-read ceiling instruments: the same bytes, the same addressing and the same launch shape as the

@@ -8,8 +8,8 @@ library's message. There is no CPU path: without the compiled library every call
 Layouts (row-major, little-endian):
   * Q4 planar: ``qs`` uint8 ``[N, K/32, 16]`` (or ``[N, K/2]``), ``d`` float16 ``[N, K/32]``.
   * Q4_K: ``w`` uint8 ``[N, K/256, 144]`` (or ``[N, K/256*144]``).
-  * inputs and outputs of the GEMVs float32; of the norm/rotation, cache and attention calls float32, float16 or
-    bfloat16 (one type per call).
+  * inputs and outputs of the GEMVs float32; of the norm/rotation, cache, attention, block norm, expert down and layer
+    calls float32, float16 or bfloat16 (one type per call).
   * 4-bit cache: :class:`KV4Cache`, planar Q4 rows in pages ``[num_pages, num_kv_heads, page_size, ...]``.
 """
 
@@ -28,6 +28,7 @@ __all__ = [
     "q4k_pure_read",
     "moe_q4_pure_read", "q4_dequant", "q4k_dequant",
     "KV4Cache", "qk_norm_rope", "kv4_write", "kv4_read", "kv4_attention", "kv4_attention_workspace",
+    "residual_norm", "moe_q4_down_gemv", "moe_q4_down_workspace", "MoEWeights", "moe_q4_layer", "moe_q4_layer_workspace",
     "q4_device_faults", "q4_set_launch_overlap", "q4_get_launch_overlap", "q4_set_wait_limit", "q4_get_wait_limit",
     "FAULT_BAD_EXPERT", "FAULT_WAIT_TIMEOUT", "FAULT_COPY_LOST", "DEFAULT_WAIT_LIMIT",
     "FAULT_BAD_SLOT", "FAULT_BAD_PAGE", "FAULT_BAD_LENGTH", "FAULT_BAD_POSITION",
@@ -76,6 +77,12 @@ _SIGNATURES = {
     "kv4_read": [_P, _P, _P, _P, _I, _L, _L, _I, _P],
     "kv4_attention_workspace": [ctypes.POINTER(ctypes.c_size_t), _I, _I, _I, _I, _I],
     "kv4_attention": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _L, _L, ctypes.c_float, _I, _I, _P, ctypes.c_size_t, _P],
+    "residual_norm": [_P, _P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, ctypes.c_float, _I, _I, _I, _L, _L, _L, _L, _L,
+                      _I, _P],
+    "moe_q4_down_workspace": [ctypes.POINTER(ctypes.c_size_t), _I, _I, _I, _I],
+    "moe_q4_down_gemv": [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _L, _L, _I, _P, _P, ctypes.c_size_t, _P],
+    "moe_q4_layer_workspace": [ctypes.POINTER(ctypes.c_size_t), _I, _I, _I, _I, _I],
+    "moe_q4_layer": [_P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _I, _I, _I, _L, _L, _L, _I, _P, ctypes.c_size_t, _P],
     "q4_device_faults": [ctypes.POINTER(ctypes.c_uint)],
     "q4_fma_ceiling": [_P, _I, ctypes.c_longlong, ctypes.c_float, ctypes.c_float, ctypes.POINTER(ctypes.c_longlong),
                        _P],
@@ -559,6 +566,166 @@ def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float |
           cache._ref, _flat(block_table, torch.int32, dev, "block_table", B * table_shape[1]),
           _flat(seq_lens, torch.int32, dev, "seq_lens", B), B, M, Hq, min(table_shape[1], 0x7FFFFFFF), qs, os_,
           D ** -0.5 if scale is None else scale, max(-1, min(window, 0x7FFFFFFF)), code, _flat(workspace, torch.uint8, dev, "workspace", size), size,
+          _stream_on(dev, stream))
+
+
+# ---- around and inside a mixture-of-experts block ----
+
+def _mat(t: torch.Tensor, T: int, K: int, dtype: torch.dtype, dev: int, name: str):
+    """(address, elements from one token to the next) of token rows [T, K] on device `dev`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on device {dev}, got {t.device}")
+    if t.shape != (T, K):
+        raise ValueError(f"{name}: expected [{T}, {K}], got {list(t.shape)}")
+    step, one = t.stride()
+    if one != 1 and K > 1:
+        raise ValueError(f"{name}: a token's row must be contiguous")
+    return t.data_ptr(), step if T > 1 else K
+
+
+def _on_stream(dev: int, stream, make):
+    """make() on the stream that uses what it allocates, so that the allocator hands it on only to work behind the call."""
+    s = torch.cuda.current_stream(dev) if stream is None else (
+        stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev))
+    with torch.cuda.stream(s):
+        return make()
+
+
+def residual_norm(h_out, y_out, x, residual=None, post_gamma=None, gate=None, pre_gamma=None, eps: float = 1e-6,
+                  residual_scale: float = 1.0, branch_scale: float = 1.0, stream=None) -> None:
+    """h_out = residual_scale * residual + branch_scale * gate * b with b = x, or its RMSNorm when post_gamma (float32 [K]) is
+    given, and y_out = RMSNorm(h) with pre_gamma (float32 [K]; y_out and pre_gamma are given together or both None). x,
+    residual, h_out, y_out [T, K]; gate [K], [T, 1] or [T, K], or None. h_out or y_out may be x or residual."""
+    code, dev = _act(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    (T, K), dt = x.shape, x.dtype
+    xp, xs = _mat(x, T, K, dt, dev, "x")
+    hp, hs = _mat(h_out, T, K, dt, dev, "h_out")
+    yp, ys = (None, 0) if y_out is None else _mat(y_out, T, K, dt, dev, "y_out")
+    rp, rs = (None, 0) if residual is None else _mat(residual, T, K, dt, dev, "residual")
+    gp, gs, width = None, 0, K
+    if gate is not None:
+        if gate.shape == (K,):
+            gp = _flat(gate, dt, dev, "gate", K)
+        elif gate.dim() == 2 and gate.shape[1] == 1 and K > 1:
+            width = 1
+            gp, gs = _mat(gate, T, 1, dt, dev, "gate")
+            gs = gs if T > 1 else 1
+        else:
+            gp, gs = _mat(gate, T, K, dt, dev, "gate")
+    _call(load().residual_norm, dev, hp, yp, xp, rp,
+          None if post_gamma is None else _flat(post_gamma, torch.float32, dev, "post_gamma", K), gp,
+          None if pre_gamma is None else _flat(pre_gamma, torch.float32, dev, "pre_gamma", K), eps, residual_scale, branch_scale,
+          T, K, width, hs, ys, xs, rs, gs, code, _stream_on(dev, stream))
+
+
+def moe_q4_down_workspace(out, h) -> torch.Tensor:
+    """Workspace for moe_q4_down_gemv calls with out [T, N] and h [T, topk, K]. Calls that may run at the same time (other
+    streams, other graphs) need one each."""
+    _, dev = _act(out, "out")
+    if h.dim() != 3 or out.dim() != 2:
+        raise ValueError("out must be [T, N] and h [T, topk, K]")
+    T, topk, K = h.shape
+    need = ctypes.c_size_t(0)
+    _call(load().moe_q4_down_workspace, dev, ctypes.byref(need), T, topk, out.shape[1], K)
+    return torch.empty(max(16, need.value), dtype=torch.uint8, device=out.device)
+
+
+def moe_q4_down_gemv(out, qs, d, h, expert_ids, expert_weights, residual=None, dev_status=None, workspace=None,
+                     stream=None) -> None:
+    """out[t] = residual[t] + sum_s expert_weights[t, s] * W[expert_ids[t, s]] h[t, s]: the experts' down projections (planar
+    Q4, qs [E, N, K/32, 16], d [E, N, K/32]) behind moe_q4_swiglu_gemv, and their weighted sum. h float32 [T, topk, K],
+    expert_ids int32 and expert_weights float32 [T, topk]; out and residual [T, N] (residual may be None, or out).
+    workspace: from moe_q4_down_workspace, kept between calls; None: allocated for this call."""
+    code, dev = _act(out, "out")
+    dt = out.dtype
+    if h.dim() != 3 or d.dim() != 3 or out.dim() != 2:
+        raise ValueError("out must be [T, N], d [E, N, K/32] and h [T, topk, K]")
+    T, topk, K = h.shape
+    E, N, _ = d.shape
+    op, os_ = _mat(out, T, N, dt, dev, "out")
+    rp, rs = (None, 0) if residual is None else _mat(residual, T, N, dt, dev, "residual")
+    if workspace is None:
+        workspace = _on_stream(dev, stream, lambda: moe_q4_down_workspace(out, h))
+    size = workspace.numel()
+    _call(load().moe_q4_down_gemv, dev, op, _flat(qs, torch.uint8, dev, "qs", E * N * K // 2),
+          _flat(d, torch.float16, dev, "d", E * N * (K // 32)), _flat(h, torch.float32, dev, "h", T * topk * K),
+          _flat(expert_ids, torch.int32, dev, "expert_ids", T * topk),
+          _flat(expert_weights, torch.float32, dev, "expert_weights", T * topk), rp, T, topk, E, N, K, os_, rs, code,
+          None if dev_status is None else _flat(dev_status, torch.int32, dev, "dev_status", 1),
+          _flat(workspace, torch.uint8, dev, "workspace", size), size, _stream_on(dev, stream))
+
+
+class MoEWeights:
+    """A mixture-of-experts layer's weights in planar Q4 (``moe_q4_weights`` of the header).
+
+    ``router_qs`` uint8 ``[E, K/32, 16]`` and ``router_d`` float16 ``[E, K/32]``; ``gate`` and ``up`` ``[E, N, K/32, 16]`` and
+    ``[E, N, K/32]``; ``down`` ``[E, K, N/32, 16]`` and ``[E, K, N/32]``; contiguous on one CUDA device. The object keeps the
+    tensors (and the struct that the calls take, made once: its attributes cannot be set) and nothing else.
+    """
+
+    class _Struct(ctypes.Structure):
+        _fields_ = [(f"{m}_{part}", _P) for m in ("router", "gate", "up", "down") for part in ("qs", "d")] + [
+            ("E", _I), ("N", _I), ("K", _I)]
+
+    def __init__(self, router_qs, router_d, gate_qs, gate_d, up_qs, up_d, down_qs, down_d):
+        tensors = dict(router_qs=router_qs, router_d=router_d, gate_qs=gate_qs, gate_d=gate_d, up_qs=up_qs, up_d=up_d,
+                       down_qs=down_qs, down_d=down_d)
+        if router_d.dim() != 2 or gate_d.dim() != 3:
+            raise ValueError("router_d must be [E, K/32] and gate_d [E, N, K/32]")
+        (E, blocks), N = router_d.shape, gate_d.shape[1]
+        K = blocks * 32
+        if N % 32:
+            raise ValueError(f"N must be a multiple of 32 (got {N})")
+        shapes = dict(router=(E, blocks), gate=(E, N, blocks), up=(E, N, blocks), down=(E, K, N // 32))
+        for m, shape in shapes.items():
+            if tuple(tensors[m + "_d"].shape) != shape or tuple(tensors[m + "_qs"].shape) != (*shape, 16):
+                raise ValueError(f"{m}: expected codes {[*shape, 16]} and scales {list(shape)}, got "
+                                 f"{list(tensors[m + '_qs'].shape)} and {list(tensors[m + '_d'].shape)}")
+        if any(t.device != router_qs.device for t in tensors.values()):
+            raise ValueError("the weights must be on one device")
+        struct = MoEWeights._Struct(*(_ptr(t, torch.uint8 if name.endswith("qs") else torch.float16, name)
+                                      for name, t in tensors.items()), E, N, K)
+        self.__dict__.update(tensors, E=E, N=N, K=K, device=router_qs.device, _struct=struct, _ref=ctypes.addressof(struct))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: MoEWeights' tensors and sizes are fixed; make another one")
+
+
+def moe_q4_layer_workspace(moe: MoEWeights, x, topk: int) -> torch.Tensor:
+    """Workspace for moe_q4_layer calls with x's [T, K]. Calls that may run at the same time (other streams, other graphs)
+    need one each."""
+    _, dev = _act(x, "x")
+    need = ctypes.c_size_t(0)
+    _call(load().moe_q4_layer_workspace, dev, ctypes.byref(need), x.shape[0], topk, moe.E, moe.N, moe.K)
+    return torch.empty(max(16, need.value), dtype=torch.uint8, device=x.device)
+
+
+def moe_q4_layer(out, x, moe: MoEWeights, topk: int, gamma=None, eps: float = 1e-6, residual=None, normalize: bool = True,
+                 expert_ids=None, expert_weights=None, workspace=None, stream=None) -> None:
+    """A whole mixture-of-experts layer: out = residual + sum over the topk picks of weight * Wd (silu(Wg xn) * (Wu xn)), with
+    xn = x [T, K] or its RMSNorm when gamma (float32 [K]) is given, picks and weights as moe_router_q4. residual [T, K] or
+    None; out may be x or residual. expert_ids int32 and expert_weights float32 [T, topk] receive the picks when given.
+    workspace: from moe_q4_layer_workspace, kept between calls; None: allocated for this call."""
+    code, dev = _act(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    T, K, dt = x.shape[0], moe.K, x.dtype
+    if dev != moe.device.index:
+        raise ValueError(f"x: expected a tensor on {moe.device}, got {x.device}")
+    xp, xs = _mat(x, T, K, dt, dev, "x")
+    op, os_ = _mat(out, T, K, dt, dev, "out")
+    rp, rs = (None, 0) if residual is None else _mat(residual, T, K, dt, dev, "residual")
+    if workspace is None:
+        workspace = _on_stream(dev, stream, lambda: moe_q4_layer_workspace(moe, x, topk))
+    size = workspace.numel()
+    _call(load().moe_q4_layer, dev, op, xp, moe._ref, None if gamma is None else _flat(gamma, torch.float32, dev, "gamma", K), eps,
+          rp, None if expert_ids is None else _flat(expert_ids, torch.int32, dev, "expert_ids", T * topk),
+          None if expert_weights is None else _flat(expert_weights, torch.float32, dev, "expert_weights", T * topk), T, topk,
+          1 if normalize else 0, os_, xs, rs, code, _flat(workspace, torch.uint8, dev, "workspace", size), size,
           _stream_on(dev, stream))
 
 

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "../../include/q4gemv.h"
+#include "block.h"
 #include "kv.h"
 #include "launch.h"
 
@@ -533,6 +534,145 @@ int kv4_attention(void* out, float* lse, const void* q, const kv4_cache* cache, 
             return fail(Q4_EINVAL, "%s: the workspace holds %zu bytes, %zu are needed", what, workspace_bytes, need);
     }
     return finish(what, launch_kv4_attention(a, workspace, di, (cudaStream_t)stream));
+}
+
+int residual_norm(void* h_out, void* y_out, const void* x, const void* residual, const float* post_gamma, const void* gate,
+                  const float* pre_gamma, float eps, float residual_scale, float branch_scale, int T, int K, int gate_width,
+                  long long h_out_stride, long long y_out_stride, long long x_stride, long long residual_stride,
+                  long long gate_stride, int dtype, q4_stream_t stream) {
+    const char* what = "residual_norm";
+    if (T <= 0) return fail(Q4_EINVAL, "%s: T must be >= 1 (got %d)", what, T);
+    if (K <= 0 || K % 8 != 0 || K > 32768)
+        return fail(Q4_EINVAL, "%s: K must be a multiple of 8 up to 32768 (got %d)", what, K);
+    Q4_TRY(check_dtype(what, dtype));
+    Q4_TRY(check_rows(what, "x", x, x_stride, K, dtype));
+    Q4_TRY(check_rows(what, "h_out", h_out, h_out_stride, K, dtype));
+    if ((y_out != nullptr) != (pre_gamma != nullptr))
+        return fail(Q4_EINVAL, "%s: y_out and pre_gamma come together", what);
+    if (y_out) Q4_TRY(check_rows(what, "y_out", y_out, y_out_stride, K, dtype));
+    if (y_out == h_out) return fail(Q4_EINVAL, "%s: y_out and h_out are the same", what);
+    if (residual) Q4_TRY(check_rows(what, "residual", residual, residual_stride, K, dtype));
+    if (post_gamma) Q4_TRY(check_vec(what, "post_gamma", post_gamma));
+    if (pre_gamma) Q4_TRY(check_vec(what, "pre_gamma", pre_gamma));
+    if (gate) {
+        if (gate_width != 1 && gate_width != K)
+            return fail(Q4_EINVAL, "%s: gate_width must be K or 1 (got %d)", what, gate_width);
+        if (gate_stride < 0 || (gate_stride > 0 && gate_stride < gate_width))
+            return fail(Q4_EINVAL, "%s: token stride of gate is %lld, below its row of %d elements", what, gate_stride, gate_width);
+        if (gate_width == K ? !aligned(gate, 16) || (gate_stride * (long long)dtype_bytes(dtype)) % 16 != 0
+                            : !aligned(gate, dtype_bytes(dtype)))
+            return fail(Q4_EALIGN, "%s: every row of gate must be 16-byte aligned", what);
+    }
+    Q4_TRY(check_eps(what, eps));
+    if (!std::isfinite(residual_scale) || !std::isfinite(branch_scale))
+        return fail(Q4_EINVAL, "%s: the scales must be finite", what);
+    DeviceInfo di;
+    Q4_TRY(check_device(what, &di));
+    const ResidualNormArgs a = {h_out, y_out, x, residual, gate, post_gamma, pre_gamma, eps, residual_scale, branch_scale, T, K,
+                                gate_width, h_out_stride, y_out_stride, x_stride, residual_stride, gate_stride, di.sm_count};
+    return finish(what, launch_residual_norm(a, dtype, (cudaStream_t)stream));
+}
+
+// Sizes of a mixture of experts: `rows` and `cols` of a matrix, slots T * topk.
+static int check_slots(const char* what, int T, int topk, int E) {
+    if (E <= 0) return fail(Q4_EINVAL, "%s: E must be >= 1 (got %d)", what, E);
+    if (T <= 0 || topk <= 0) return fail(Q4_EINVAL, "%s: T and topk must be >= 1", what);
+    if (topk > E) return fail(Q4_EINVAL, "%s: topk=%d exceeds E=%d", what, topk, E);
+    if ((long long)T * topk > 512) return fail(Q4_EINVAL, "%s: T*topk=%lld exceeds 512", what, (long long)T * topk);
+    return Q4_OK;
+}
+
+static int check_down_sizes(const char* what, int T, int topk, int E, int N, int K) {
+    Q4_TRY(check_slots(what, T, topk, E));
+    if (N <= 0 || N % 8 != 0) return fail(Q4_EINVAL, "%s: N must be a positive multiple of 8 (got %d)", what, N);
+    if (K <= 0 || K % 32 != 0 || K > 65536)
+        return fail(Q4_EINVAL, "%s: K must be a multiple of 32 up to 65536 (got %d)", what, K);
+    if ((long long)E * N > 0x7fffffffLL) return fail(Q4_EINVAL, "%s: E*N exceeds 2^31-1 rows", what);
+    return Q4_OK;
+}
+
+static int check_workspace(const char* what, const void* workspace, size_t bytes, size_t need) {
+    if (!workspace) return fail(Q4_EINVAL, "%s: null workspace", what);
+    if (!aligned(workspace, 16)) return fail(Q4_EALIGN, "%s: workspace must be 16-byte aligned", what);
+    if (bytes < need) return fail(Q4_EINVAL, "%s: the workspace holds %zu bytes, %zu are needed", what, bytes, need);
+    return Q4_OK;
+}
+
+int moe_q4_down_workspace(size_t* bytes, int T, int topk, int N, int K) {
+    const char* what = "moe_q4_down_workspace";
+    if (!bytes) return fail(Q4_EINVAL, "%s: null output pointer", what);
+    Q4_TRY(check_down_sizes(what, T, topk, topk, N, K));
+    *bytes = moe_down_workspace_bytes(T, topk, N, K);
+    return finish(what, cudaSuccess);
+}
+
+int moe_q4_down_gemv(void* out, const uint8_t* qs, const uint16_t* d, const float* h, const int32_t* expert_ids,
+                     const float* expert_weights, const void* residual, int T, int topk, int E, int N, int K,
+                     long long out_stride, long long residual_stride, int dtype, int32_t* dev_status, void* workspace,
+                     size_t workspace_bytes, q4_stream_t stream) {
+    const char* what = "moe_q4_down_gemv";
+    Q4_TRY(check_dtype(what, dtype));
+    Q4_TRY(check_down_sizes(what, T, topk, E, N, K));
+    Q4_TRY(check_rows(what, "out", out, out_stride, N, dtype));
+    if (residual) Q4_TRY(check_rows(what, "residual", residual, residual_stride, N, dtype));
+    Q4_TRY(check_q4_weights(what, qs, d, N, K));
+    Q4_TRY(check_vec(what, "h", h));
+    Q4_TRY(check_index(what, "expert_ids", expert_ids));
+    if (!expert_weights) return fail(Q4_EINVAL, "%s: null expert_weights", what);
+    if (!aligned(expert_weights, 4)) return fail(Q4_EALIGN, "%s: expert_weights must be 4-byte aligned", what);
+    if (dev_status && !aligned(dev_status, 4)) return fail(Q4_EALIGN, "%s: dev_status must be 4-byte aligned", what);
+    Q4_TRY(check_workspace(what, workspace, workspace_bytes, moe_down_workspace_bytes(T, topk, N, K)));
+    DeviceInfo di;
+    MoeDownArgs a = {out, qs, d, h, expert_ids, expert_weights, residual, T, topk, E, N, K, out_stride, residual_stride,
+                     dev_status, nullptr};
+    Q4_TRY(check_device_faults(what, &di, &a.fault));
+    return finish(what, launch_moe_down(a, dtype, workspace, di, (cudaStream_t)stream));
+}
+
+static int check_layer_sizes(const char* what, int T, int topk, int E, int N, int K) {
+    Q4_TRY(check_slots(what, T, topk, E));
+    if (E > 4096) return fail(Q4_EINVAL, "%s: E must be in 1..4096 (got %d)", what, E);
+    if (N <= 0 || N % 32 != 0 || N > 65536)
+        return fail(Q4_EINVAL, "%s: N must be a multiple of 32 up to 65536 (got %d)", what, N);
+    if (K <= 0 || K % 32 != 0 || K > 32768)
+        return fail(Q4_EINVAL, "%s: K must be a multiple of 32 up to 32768 (got %d)", what, K);
+    return Q4_OK;
+}
+
+int moe_q4_layer_workspace(size_t* bytes, int T, int topk, int E, int N, int K) {
+    const char* what = "moe_q4_layer_workspace";
+    if (!bytes) return fail(Q4_EINVAL, "%s: null output pointer", what);
+    Q4_TRY(check_layer_sizes(what, T, topk, E, N, K));
+    *bytes = moe_layer_workspace_bytes(T, topk, N, K);
+    return finish(what, cudaSuccess);
+}
+
+int moe_q4_layer(void* out, const void* x, const moe_q4_weights* weights, const float* gamma, float eps, const void* residual,
+                 int32_t* expert_ids, float* expert_weights, int T, int topk, int normalize, long long out_stride,
+                 long long x_stride, long long residual_stride, int dtype, void* workspace, size_t workspace_bytes,
+                 q4_stream_t stream) {
+    const char* what = "moe_q4_layer";
+    if (!weights) return fail(Q4_EINVAL, "%s: null weights", what);
+    const moe_q4_weights& w = *weights;
+    Q4_TRY(check_dtype(what, dtype));
+    Q4_TRY(check_layer_sizes(what, T, topk, w.E, w.N, w.K));
+    Q4_TRY(check_q4_weights(what, w.router_qs, w.router_d, w.E, w.K));
+    Q4_TRY(check_q4_weights(what, w.gate_qs, w.gate_d, w.N, w.K));
+    Q4_TRY(check_q4_weights(what, w.up_qs, w.up_d, w.N, w.K));
+    Q4_TRY(check_q4_weights(what, w.down_qs, w.down_d, w.K, w.N));
+    Q4_TRY(check_rows(what, "out", out, out_stride, w.K, dtype));
+    Q4_TRY(check_rows(what, "x", x, x_stride, w.K, dtype));
+    if (residual) Q4_TRY(check_rows(what, "residual", residual, residual_stride, w.K, dtype));
+    if (gamma) Q4_TRY(check_vec(what, "gamma", gamma));
+    Q4_TRY(check_eps(what, eps));
+    if (!aligned(expert_ids, 4) || !aligned(expert_weights, 4))
+        return fail(Q4_EALIGN, "%s: expert_ids and expert_weights must be 4-byte aligned", what);
+    Q4_TRY(check_workspace(what, workspace, workspace_bytes, moe_layer_workspace_bytes(T, topk, w.N, w.K)));
+    DeviceInfo di;
+    MoeLayerArgs a = {w, out, x, residual, gamma, eps, T, topk, normalize != 0, out_stride, x_stride, residual_stride,
+                      expert_ids, expert_weights, nullptr};
+    Q4_TRY(check_device_faults(what, &di, &a.fault));
+    return finish(what, launch_moe_layer(a, dtype, workspace, di, (cudaStream_t)stream));
 }
 
 const char* q4_last_error(void) { return g_last_error.c_str(); }

@@ -1,0 +1,53 @@
+// Internal host-side interface of the block norm and of the mixture-of-experts layer.
+// Arguments reaching these functions have already been validated by the ABI layer.
+#pragma once
+
+#include "kv.h"
+#include "launch.h"
+
+namespace q4 {
+
+struct ResidualNormArgs {
+    void *h_out, *y_out;  // y_out nullptr: no norm behind the sum
+    const void *x, *residual, *gate;  // residual, gate: nullable
+    const float *post_gamma, *pre_gamma;
+    float eps, residual_scale, branch_scale;
+    int T, K, gate_width;  // gate_width: K (element by element) or 1 (a number per token)
+    long long h_stride, y_stride, x_stride, residual_stride, gate_stride;
+    int sm_count;
+};
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, int dtype, cudaStream_t s);
+
+// Down projections of T * topk slots and their weighted sum per token: rows = outputs, cols = inputs of an expert's matrix.
+struct MoeDownArgs {
+    void* out;
+    const uint8_t* qs;
+    const uint16_t* d;
+    const float* h;       // [T][topk][cols]
+    const int32_t* ids;   // [T][topk]
+    const float* weights; // [T][topk]
+    const void* residual; // nullable
+    int T, topk, E, rows, cols;
+    long long out_stride, residual_stride;
+    int32_t* status;  // nullable
+    unsigned* fault;
+};
+size_t moe_down_workspace_bytes(int T, int topk, int rows, int cols);
+cudaError_t launch_moe_down(const MoeDownArgs& a, int dtype, void* workspace, const DeviceInfo& di, cudaStream_t s);
+
+struct MoeLayerArgs {
+    moe_q4_weights w;
+    void* out;
+    const void *x, *residual;  // residual: nullable
+    const float* gamma;        // nullable: no norm
+    float eps;
+    int T, topk, normalize;
+    long long out_stride, x_stride, residual_stride;
+    int32_t* ids;    // nullable (kept in the workspace)
+    float* weights;  // nullable
+    unsigned* fault;
+};
+size_t moe_layer_workspace_bytes(int T, int topk, int N, int K);
+cudaError_t launch_moe_layer(const MoeLayerArgs& a, int dtype, void* workspace, const DeviceInfo& di, cudaStream_t s);
+
+}  // namespace q4
