@@ -302,10 +302,11 @@ int residual_norm(void *h_out, void *y_out, const void *x, const void *residual,
 /*
  * moe_q4_down_gemv: the down projections of the selected experts and their weighted sum, behind moe_q4_swiglu_gemv.
  *   out[t][n] = residual[t][n] + sum_{s < topk} expert_weights[t][s] * sum_k W[e*N + n][k] * h[t][s][k],
- *   e = expert_ids[t*topk + s]. Each selected expert's rows are read once for up to 16 (of long rows: 8) of its slots.
+ *   e = expert_ids[t*topk + s]. Each selected expert's rows are read once for up to 8 of its slots.
  *   out [T][N]; residual [T][N] or NULL, which out may be (same pointer and stride); qs uint8[E*N][K/32][16], d
  *   uint16[E*N][K/32]; h float[T][topk][K] (16-byte aligned); expert_ids int32[T][topk], expert_weights float[T][topk]
- *   (device). 1 <= topk <= E; T*topk <= 512; N a multiple of 8; K % 32 == 0, K <= 65536; E*N < 2^31.
+ *   (device). 1 <= topk <= E; T*topk <= 512; N a multiple of 8 up to 2^20; K % 32 == 0, K <= 65536;
+ *   E*N < 2^31.
  *   A token with an id outside [0, E) gets a NaN row; Q4_FAULT_BAD_EXPERT is recorded and, when dev_status is not NULL,
  *   stored there. An expert may be given twice to a token.
  *   workspace: as for kv4_attention, of at least the bytes that moe_q4_down_workspace states for these sizes.

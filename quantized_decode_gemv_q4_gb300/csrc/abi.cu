@@ -584,7 +584,8 @@ static int check_slots(const char* what, int T, int topk, int E) {
 
 static int check_down_sizes(const char* what, int T, int topk, int E, int N, int K) {
     Q4_TRY(check_slots(what, T, topk, E));
-    if (N <= 0 || N % 8 != 0) return fail(Q4_EINVAL, "%s: N must be a positive multiple of 8 (got %d)", what, N);
+    if (N <= 0 || N % 8 != 0 || N > (1 << 20))
+        return fail(Q4_EINVAL, "%s: N must be a multiple of 8 up to 2^20 (got %d)", what, N);
     if (K <= 0 || K % 32 != 0 || K > 65536)
         return fail(Q4_EINVAL, "%s: K must be a multiple of 32 up to 65536 (got %d)", what, K);
     if ((long long)E * N > 0x7fffffffLL) return fail(Q4_EINVAL, "%s: E*N exceeds 2^31-1 rows", what);

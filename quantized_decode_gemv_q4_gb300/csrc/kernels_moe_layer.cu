@@ -105,11 +105,13 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const PrepParams p) {
 // scale in fp32. The columns are the segment's vectors in two f16 parts (x = hi + lo to 2^-22), scaled by a power of two that
 // puts a vector's largest element near 2^14: with up to 4 slots both parts share an instruction's 8 columns, with more each
 // part has its own and both add into the same sums. The parts lie in shared memory in the order in which lanes take them.
-constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kStages = 3;                       // of a warp's ring; 2 where the vectors leave no room
 constexpr int kChunk = 4;                        // blocks of a chunk
-constexpr uint32_t kScalesAt = 2048, kStageBytes = 2304;  // a stage: 32 rows x 64 bytes of codes, 32 x 4 scales
+constexpr uint32_t kStageBytes = 2048;           // a stage: 32 rows x 64 bytes of codes
+constexpr uint32_t kGroupBytes = 512;            // 32 rows x 8 scales: those of two chunks, in a ring of their own
+constexpr uint32_t kSlotBytes = kStageBytes + kGroupBytes;
 constexpr int kMaxSlots = 512;
+constexpr int kStageLoads = 2;
 constexpr int kMaxCap = 8;
 constexpr int kPartBlocks = 88;                  // most blocks of a part: 8 slots' fit beside the ring
 
@@ -121,15 +123,17 @@ struct ExpertParams {
     float* out;                // [parts][slots][rows]
     unsigned* out_max;         // as in_max, of the outputs (gate and up)
     const int32_t* ids;
-    int E, rows, blocks, parts, slots, per_in, cap, stages, scale_bytes;  // slot s reads input row s / per_in
+    int E, rows, blocks, slots, per_in;  // slot s reads input row s / per_in
+    int units, parts, part_blocks, cap, stages, scale_bytes, table_bits;
     uint32_t ring_at, deposits_at, frags_at;
 };
 
 struct Tables {
-    int ids[kMaxSlots], seg_e[kMaxSlots];
-    uint16_t list[kMaxSlots], list_base[kMaxSlots], seg_at[kMaxSlots];
+    int seg_e[kMaxSlots];
+    uint16_t list[kMaxSlots], seg_at[kMaxSlots];
     uint8_t seg_n[kMaxSlots];
-    int warp_segs[kWarps], warp_slots[kWarps];
+    int8_t exponent[kMaxSlots];  // of a slot's vector: see vector_exponent; kNotFinite
+    int warp_sums[16];
     float back[2][kMaxCap];
 };
 
@@ -182,7 +186,10 @@ __device__ __forceinline__ void codes_of(uint32_t w, uint32_t k1024, uint32_t (&
 }
 
 // The power of two that takes a vector whose largest size has the bits `m` to at most 2^15, as its exponent.
-__device__ __forceinline__ int vector_exponent(unsigned m) { return m == 0u ? 0 : min(141 - (int)(m >> 23), 126); }
+constexpr int kNotFinite = 127;
+__device__ __forceinline__ int vector_exponent(unsigned m) {
+    return m == 0u ? 0 : m >= 0x7f800000u ? kNotFinite : min(141 - (int)(m >> 23), 126);
+}
 
 // A warp's chunks of one segment and part: the items [at, end) of (unit, chunk), counted from the CTA's first unit there.
 struct Cursor {
@@ -191,240 +198,445 @@ struct Cursor {
     int chunks, block0, blocks;  // of the part
 };
 
-template <bool GateUp>
-__global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const ExpertParams p) {
+// PER: slots of a thread. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
+// that finishes a unit): a call runs each instruction few times, and fetching them costs as much as running them.
+template <bool GateUp, int W, int PER>
+__global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const ExpertParams p) {
+    constexpr int kThreads = W * 32;
     extern __shared__ __align__(128) uint8_t smem[];
     Tables& tab = *reinterpret_cast<Tables*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t base = smem_addr(smem), ring = base + p.ring_at + (uint32_t)(warp * p.stages) * kStageBytes, frags = base + p.frags_at;
+    const uint32_t base = smem_addr(smem), ring = base + p.ring_at + (uint32_t)(warp * p.stages) * kSlotBytes, frags = base + p.frags_at;
     float* deposits = reinterpret_cast<float*>(smem + p.deposits_at);
 
-    grid_dependency_wait();
-    grid_launch_dependents();
-
-    // Segments: the slots of an expert in their order, `cap` at a time, experts in the order of their first slots.
-    for (int s = tid; s < p.slots; s += kThreads) tab.ids[s] = p.ids[s];
+    // Segments: the slots of an expert in their order, `cap` at a time, experts in the order of their first slots. A hash
+    // table of experts, each with the bits of its slots, lies where the ring and the vectors lie later.
+    const int words = (p.slots + 31) / 32, entries = 1 << p.table_bits;
+    uint16_t* const list_base = reinterpret_cast<uint16_t*>(smem + p.ring_at);
+    int* const keys = reinterpret_cast<int*>(list_base + kMaxSlots);
+    uint32_t* const masks = reinterpret_cast<uint32_t*>(keys + entries);
+    for (int i = tid; i < entries * (1 + words); i += kThreads) keys[i] = i < entries ? -1 : 0;
     __syncthreads();
+    // The ids and the weights were written before the kernel before this one began (down: its producer waits for them
+    // itself before it lets this kernel start), so everything up to the first vectors runs while it ends.
+    if (GateUp) grid_dependency_wait();
+    grid_launch_dependents();
     int segs = 0;
     {
-        const int s = tid;
-        const bool in = s < p.slots;
-        const int e = in ? tab.ids[s] : -1;
-        const bool valid = e >= 0 && e < p.E;
-        int first = s, rank = 0, total = 0;
-        if (valid) {
-            for (int o = p.slots - 1; o >= 0; --o) {
-                const bool same = tab.ids[o] == e;
-                total += same;
-                rank += same && o < s;
-                if (same) first = o;
+        int e[PER], entry[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int s = tid * PER + i;
+            e[i] = s < p.slots ? __ldcg(p.ids + s) : -1;
+            if (GateUp && s < p.slots) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + s / p.per_in));
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int s = tid * PER + i;
+            entry[i] = -1;
+            if (e[i] >= 0 && e[i] < p.E) {
+                int at = (int)(((unsigned)e[i] * 2654435769u) >> (32 - p.table_bits));
+                for (;; at = (at + 1) & (entries - 1)) {  // at most half of the entries are ever used
+                    const int was = atomicCAS(keys + at, -1, e[i]);
+                    if (was == -1 || was == e[i]) break;
+                }
+                atomicOr(masks + at * words + (s >> 5), 1u << (s & 31));
+                entry[i] = at;
             }
         }
-        const bool leads = valid && rank == 0;
-        const int mine = leads ? (total + p.cap - 1) / p.cap : 0, slots = leads ? total : 0;
-        int a = mine, b = slots;  // inclusive sums over the warp
+        __syncthreads();
+        int first[PER], rank[PER], total[PER], mine = 0, slots = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int s = tid * PER + i;
+            first[i] = s, rank[i] = 0, total[i] = 0;
+            if (entry[i] >= 0) {
+                for (int w = words - 1; w >= 0; --w) {
+                    const uint32_t m = masks[entry[i] * words + w];
+                    total[i] += __popc(m);
+                    rank[i] += w < s >> 5 ? __popc(m) : w == s >> 5 ? __popc(m & ((1u << (s & 31)) - 1u)) : 0;
+                    if (m) first[i] = w * 32 + __ffs(m) - 1;
+                }
+                if (rank[i] == 0) mine += (total[i] + p.cap - 1) / p.cap, slots += total[i];
+            }
+        }
+        int both = mine << 16 | slots;  // sums up to 512 each
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-            if (lane >= o) a += x, b += y;
+            const int x = __shfl_up_sync(0xffffffffu, both, o);
+            if (lane >= o) both += x;
         }
-        if (lane == 31) tab.warp_segs[warp] = a, tab.warp_slots[warp] = b;
+        if (lane == 31) tab.warp_sums[warp] = both;
         __syncthreads();
-        int seg = a - mine, at = b - slots;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) seg += tab.warp_segs[w], at += tab.warp_slots[w];
-            segs += tab.warp_segs[w];
+        int before = both - (mine << 16 | slots);
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += tab.warp_sums[w];
+            segs += tab.warp_sums[w] >> 16;
         }
-        if (leads) {
-            tab.list_base[s] = (uint16_t)at;
-            for (int i = 0; i < mine; ++i) {
-                tab.seg_e[seg + i] = e;
-                tab.seg_at[seg + i] = (uint16_t)(at + i * p.cap);
-                tab.seg_n[seg + i] = (uint8_t)min(p.cap, total - i * p.cap);
+        int seg = before >> 16, at = before & 0xffff;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (total[i] == 0 || rank[i] != 0) continue;
+            list_base[tid * PER + i] = (uint16_t)at;
+#pragma unroll 1
+            for (int o = 0; o < total[i]; o += p.cap, ++seg) {
+                tab.seg_e[seg] = e[i];
+                tab.seg_at[seg] = (uint16_t)(at + o);
+                tab.seg_n[seg] = (uint8_t)min(p.cap, total[i] - o);
             }
+            at += total[i];
         }
         __syncthreads();
-        if (valid) tab.list[tab.list_base[first] + rank] = (uint16_t)s;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (total[i] != 0) tab.list[list_base[first[i]] + rank[i]] = (uint16_t)(tid * PER + i);
         __syncthreads();
     }
 
-    const int units = GateUp ? p.rows / 16 : (p.rows + 31) / 32;
-    const long long all = (long long)segs * p.parts * units;
-    const long long u_lo = all * blockIdx.x / gridDim.x, u_hi = all * (blockIdx.x + 1) / gridDim.x;
-    if (u_lo >= u_hi) return;
-    const int v_lo = (int)(u_lo / units), v_hi = (int)((u_hi - 1) / units);
-
+    // The CTA's piece of the line of units.
+    const unsigned all = (unsigned)(segs * p.parts * p.units), quotient = all / gridDim.x, rest = all - quotient * gridDim.x;
+    const int u_lo = (int)(quotient * blockIdx.x + rest * blockIdx.x / gridDim.x);
+    const int u_hi = (int)(quotient * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / gridDim.x);
+    if (u_lo >= u_hi) {
+        if (!GateUp) grid_dependency_wait();
+        return;
+    }
+    const int v_lo = u_lo / p.units, v_hi = (u_hi - 1) / p.units;
+    auto first_unit = [&](int v) { return v == v_lo ? u_lo - v * p.units : 0; };
+    auto items_of = [&](int v, int chunks) { return ((v == v_hi ? u_hi - v * p.units : p.units) - first_unit(v)) * chunks; };
     auto enter = [&](Cursor& c, int v) {
-        const int ua = v == v_lo ? (int)(u_lo - (long long)v * units) : 0;
-        const int ub = v == v_hi ? (int)(u_hi - (long long)v * units) : units;
         const int part = v % p.parts;
-        const int per = ((p.blocks + p.parts - 1) / p.parts + kChunk - 1) / kChunk * kChunk;  // blocks of a part
         c.v = v;
-        c.block0 = part * per;
-        c.blocks = min(per, p.blocks - c.block0);
+        c.block0 = part * p.part_blocks;
+        c.blocks = min(p.part_blocks, p.blocks - c.block0);
         c.chunks = (c.blocks + kChunk - 1) / kChunk;
-        const int items = (ub - ua) * c.chunks;
-        c.at = (int)((unsigned)items * (unsigned)warp / kWarps);
-        c.end = (int)((unsigned)items * (unsigned)(warp + 1) / kWarps);
+        const unsigned items = (unsigned)items_of(v, c.chunks);
+        c.at = (int)(items * (unsigned)warp / W);
+        c.end = (int)(items * (unsigned)(warp + 1) / W);
         const int unit = c.at / c.chunks;
         c.chunk = c.at - unit * c.chunks;
-        c.unit = ua + unit;
+        c.unit = first_unit(v) + unit;
     };
 
     // ---- the ring: stages are filled in the order in which they are used, across segments
     Cursor f = {};
+    f.v = v_lo - 1;
+    const uint32_t ring_bytes = (uint32_t)p.stages * kStageBytes, group_bytes = (uint32_t)p.stages * kGroupBytes;
     uint32_t fill_at = 0, use_at = 0;  // stages of the ring, as offsets
-    const uint32_t ring_bytes = (uint32_t)p.stages * kStageBytes;
-    const char *src0 = nullptr, *src1 = nullptr, *src_d = nullptr;  // of this lane, at the cursor's chunk 0
-    bool row_a = true, row_b = true, row_c = true, row_d = true, row_s = true;
-    auto aim = [&]() {  // a new unit
-        const int e = tab.seg_e[f.v / p.parts];
-        const int row = GateUp ? f.unit * 16 : f.unit * 32;
-        const long long first = (long long)e * p.rows + row;
-        const int r = lane >> 2, c = lane & 3;
-        const long long second = GateUp ? first : first + 16;
-        src0 = reinterpret_cast<const char*>(p.qs0) + ((first + r) * p.blocks + f.block0 + c) * 16;
-        src1 = reinterpret_cast<const char*>(p.qs1) + ((second + r) * p.blocks + f.block0 + c) * 16;
-        src_d = reinterpret_cast<const char*>(lane < 16 ? p.d0 : p.d1) +
-                (((lane < 16 ? first : second) + (lane & 15)) * p.blocks + f.block0) * 2;
-        if (!GateUp) {
-            const int left = p.rows - row;
-            row_a = r < left, row_b = r + 8 < left, row_c = r + 16 < left, row_d = r + 24 < left;
-            row_s = (lane < 16 ? 0 : 16) + (lane & 15) < left;
+    uint32_t group_fill = 0, group_use = 0;  // groups of scales: a group is new at every even chunk and at a piece's first
+    bool fresh = true;
+    const int r4 = lane >> 2, c4 = lane & 3;
+    const uint32_t to_codes = ring + r4 * 64 + ((c4 ^ ((r4 >> 1) & 3)) << 4), to_scales = ring + ring_bytes + lane * 16;
+    const long long row_bytes = (long long)p.blocks * 16;
+    const char *src0 = nullptr, *src1 = nullptr, *src_d = nullptr;  // of this lane, at the cursor
+    int rows_left = 32;                                        // of the unit, all of them for gate and up
+    auto fill_edge = [&](int left, bool group, int group_left) {  // past the last column or row: zeros
+        const char* none = reinterpret_cast<const char*>(p.qs0);
+        const uint32_t to = to_codes + fill_at;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const bool there = c4 < left && r4 + 8 * i < rows_left;
+            const char* src = (i < 2 ? src0 : src1) + (i & 1) * 8 * row_bytes;
+            copy_async<16>(to + 512 * i, there ? src : none, there ? 16u : 0u);
+        }
+        if (!group) return;
+        const uint32_t to_d = to_scales + group_fill;
+        const int valid = lane < rows_left ? min(group_left, 8) : 0;
+        if (p.scale_bytes == 2) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint16_t h = i < valid ? __ldg(reinterpret_cast<const uint16_t*>(src_d) + i) : (uint16_t)0;
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to_d + 2 * i), "h"(h) : "memory");
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) copy_async<4>(to_d + 4 * i, 2 * i < valid ? src_d + 4 * i : none, 2 * i < valid ? 4u : 0u);
         }
     };
-    enter(f, v_lo);
-    auto settle = [&]() {  // to the next item, if there is one
-        while (f.at >= f.end && f.v < v_hi) enter(f, f.v + 1);
-        if (f.at < f.end) aim();
-    };
-    settle();
     auto fill = [&]() {
+        if (f.at >= f.end) {
+            while (f.at >= f.end && f.v < v_hi) enter(f, f.v + 1);
+            if (f.at < f.end) {
+                const long long first = (long long)tab.seg_e[f.v / p.parts] * p.rows + (GateUp ? f.unit * 16 : f.unit * 32);
+                const long long second = GateUp ? first : first + 16;
+                const int block = f.block0 + f.chunk * kChunk, group = block & ~(2 * kChunk - 1);
+                src0 = reinterpret_cast<const char*>(p.qs0) + (first + r4) * row_bytes + (block + c4) * 16;
+                src1 = reinterpret_cast<const char*>(p.qs1) + (second + r4) * row_bytes + (block + c4) * 16;
+                src_d = reinterpret_cast<const char*>(lane < 16 ? p.d0 : p.d1) +
+                        (((lane < 16 ? first : second) + (lane & 15)) * p.blocks + group) * 2;
+                if (!GateUp) rows_left = p.rows - f.unit * 32;
+                fresh = true;
+            }
+        }
         if (f.at < f.end) {
-            const uint32_t dst = ring + fill_at;
-            const int r = lane >> 2, c = lane & 3, left = f.blocks - f.chunk * kChunk;
-            const uint32_t to = dst + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-            const long long o = (long long)f.chunk * (kChunk * 16), eight = (long long)p.blocks * 128;
-            const bool in = c < left;
-            auto copy = [&](uint32_t at, const char* src, bool there) {
-                copy_async<16>(at, there && in ? src : reinterpret_cast<const char*>(p.qs0), there && in ? 16u : 0u);
-            };
-            copy(to, src0 + o, row_a);
-            copy(to + 512, src0 + o + eight, row_b);
-            copy(to + 1024, src1 + o, row_c);
-            copy(to + 1536, src1 + o + eight, row_d);
-            const uint32_t to_d = dst + kScalesAt + lane * 8;
-            const char* sd = src_d + f.chunk * (kChunk * 2);
-            if (p.scale_bytes == 8) {
-                copy_async<8>(to_d, row_s ? sd : reinterpret_cast<const char*>(p.qs0), row_s ? 8u : 0u);
-            } else if (p.scale_bytes == 4) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool there = row_s && 2 * i < left;
-                    copy_async<4>(to_d + 4 * i, there ? sd + 4 * i : reinterpret_cast<const char*>(p.qs0), there ? 4u : 0u);
+            const bool group = fresh || (f.chunk & 1) == 0;
+            if (p.scale_bytes >= 8 && (GateUp || rows_left >= 32)) {  // 8, 16: rows of whole chunks
+                const uint32_t to = to_codes + fill_at, to_d = to_scales + group_fill;
+                copy_async<16>(to, src0, 16u);
+                copy_async<16>(to + 512, src0 + 8 * row_bytes, 16u);
+                copy_async<16>(to + 1024, src1, 16u);
+                copy_async<16>(to + 1536, src1 + 8 * row_bytes, 16u);
+                if (group) {
+                    if (p.scale_bytes == 16) {
+                        copy_async<16>(to_d, src_d, 16u);
+                    } else {
+                        copy_async<8>(to_d, src_d, 8u);
+                        const bool more = (f.chunk | 1) < f.chunks;
+                        copy_async<8>(to_d + 8, more ? src_d + 8 : src_d, more ? 8u : 0u);
+                    }
                 }
             } else {
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    h[i] = row_s && i < left ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(sd) + i) : 0u;
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to_d), "r"(h[0] | h[1] << 16), "r"(h[2] | h[3] << 16)
-                             : "memory");
+                fill_edge(f.blocks - f.chunk * kChunk, group, f.blocks - (f.chunk & ~1) * kChunk);
             }
+            if (group) group_fill = group_fill + kGroupBytes == group_bytes ? 0u : group_fill + kGroupBytes;
+            fresh = false;
+            src0 += kChunk * 16, src1 += kChunk * 16;
+            if (f.chunk & 1) src_d += 2 * kChunk * 2;
             ++f.at;
-            if (++f.chunk == f.chunks) {
+            if (++f.chunk == f.chunks) {  // on to the next unit of the part
+                const int rows = GateUp ? 16 : 32;
+                src_d += ((long long)rows * p.blocks - f.chunks / 2 * (2 * kChunk)) * 2;
+                src0 += rows * row_bytes - f.chunks * (kChunk * 16), src1 += rows * row_bytes - f.chunks * (kChunk * 16);
                 f.chunk = 0;
                 ++f.unit;
-                if (f.at < f.end) aim();
+                if (!GateUp) rows_left -= 32;
             }
-            if (f.at >= f.end) settle();
         }
         fill_at = fill_at + kStageBytes == ring_bytes ? 0u : fill_at + kStageBytes;
         cp_async_commit();
     };
-    for (int i = 0; i < p.stages - 1; ++i) fill();
 
     uint32_t k1024;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
     const int g = lane >> 2, t4 = lane & 3;
     // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8: rows 0-7 and 8-15 of a block, then of the next one
-    const int lm_row = (lane & 7) + (lane & 8), lm_half = lane >> 4;
+    const int lm_row = (lane & 7) + (lane & 8);
+    const uint32_t from_codes = ring + lm_row * 64 + (((lane >> 4) ^ ((lm_row >> 1) & 3)) << 4), from_scales = ring + ring_bytes + g * 16;
 
-    Cursor c;
-    for (int v = v_lo; v <= v_hi; ++v) {
-        enter(c, v);
-        const int seg = v / p.parts, n = tab.seg_n[seg], at = tab.seg_at[seg];
-        const int np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8;  // columns kept of each part
-        const uint32_t per_block = (uint32_t)np * 128u;
-        float* back = tab.back[v & 1];
-
-        // ---- the segment's vectors, in two parts
-        for (int j = 0; j < n; ++j) {
-            const int row = tab.list[at + j] / p.per_in;
-            const unsigned m = p.in_max[row];
-            const int k = vector_exponent(m);
-            const float scale = pow2i(k);
-            if (tid == j) back[j] = m >= 0x7f800000u ? qnan() : pow2i(-k);
-            const float* x = p.in + (long long)row * (p.blocks * 32) + (long long)c.block0 * 32;
-            for (int i = tid; i < c.chunks * kChunk * 4; i += kThreads) {
-                const int b = i >> 2, t = i & 3;
-                float4 lo4 = make_float4(0.f, 0.f, 0.f, 0.f), hi4 = lo4;
-                if (b < c.blocks) {
-                    lo4 = *reinterpret_cast<const float4*>(x + b * 32 + t * 4);
-                    hi4 = *reinterpret_cast<const float4*>(x + b * 32 + 16 + t * 4);
-                }
-                const float pair[4][2] = {{lo4.x, lo4.z}, {hi4.x, hi4.z}, {lo4.y, lo4.w}, {hi4.y, hi4.w}};
-                uint32_t hi[4], lo[4];
+    Cursor c = {};
+    c.v = v_lo - 1;
+    bool begun = false, waited = GateUp;  // a part is under way; the vectors are there
+    bool head = false;                    // the unit was begun by a warp before this one, which joins it
+    bool entered = false;                 // the next item is the part's first
+    int ahead = 0, n = 0, at = 0, np = 1, staged = -1;
+    uint32_t per_block = 0, column = 0, vec = 0, scales = 0;
+    const float* back = tab.back[0];
+    float acc[2][4] = {};
+    auto deposit = [&]() {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float a = pair[q][0] * scale, b2 = pair[q][1] * scale;
-                    const __half2 h = __floats2half2_rn(a, b2);
-                    const float2 back2 = __half22float2(h);
-                    hi[q] = bits_of(h);
-                    lo[q] = bits_of(__floats2half2_rn(a - back2.x, b2 - back2.y));
+        for (int i = 0; i < 8; ++i) {
+            deposits[(warp * 8 + i) * 32 + lane] = acc[i >> 2][i & 3];
+            acc[i >> 2][i & 3] = 0.f;
+        }
+    };
+    // One chunk. Everything that it needs from shared memory is asked for before any of it is used (the second part of wide
+    // columns excepted, for which there are no registers).
+    auto multiply = [&](auto wide) {
+        constexpr bool Wide = decltype(wide)::value;  // 8 columns for each part
+        const uint32_t codes = from_codes + use_at, sc = scales + ((c.chunk & 1) << 3);
+        uint32_t w[2][2][4], scale[2][2][2];  // codes of (pair of blocks, tile); scales of (tile, rows g or g + 8)
+#pragma unroll
+        for (int pair = 0; pair < 2; ++pair)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) ldsm4((pair ? codes ^ 32u : codes) + m * 1024, w[pair][m]);
+        uint4 x[kChunk];
+#pragma unroll
+        for (int b = 0; b < kChunk; ++b) x[b] = lds128(vec + b * (Wide ? 1024u : per_block));
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(scale[m][h][0]), "=r"(scale[m][h][1])
+                             : "r"(sc + m * 256 + h * 128));
+#pragma unroll
+        for (int b = 0; b < kChunk; ++b) {
+            uint4 l = x[b];
+            if (Wide) l = lds128(vec + b * 1024u + 512u);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t ra[4], rb[4];
+                codes_of(w[b >> 1][m][2 * (b & 1)], k1024, ra);
+                codes_of(w[b >> 1][m][2 * (b & 1) + 1], k1024, rb);
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                float s[4];
+                mma(s, ra[0], rb[0], ra[1], rb[1], x[b].x, x[b].y, zero);
+                mma(s, ra[2], rb[2], ra[3], rb[3], x[b].z, x[b].w, s);
+                if (Wide) {
+                    mma(s, ra[0], rb[0], ra[1], rb[1], l.x, l.y, s);
+                    mma(s, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s);
                 }
-                const uint32_t to = frags + b * per_block + j * 64 + t * 16;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
-                             : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + np * 64), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
-                             "r"(lo[3])
-                             : "memory");
+                const __half2 pa = half2_of(scale[m][0][b >> 1]), pb = half2_of(scale[m][1][b >> 1]);
+                const float da = (b & 1) ? __high2float(pa) : __low2float(pa), db = (b & 1) ? __high2float(pb) : __low2float(pb);
+                acc[m][0] = fmaf(da, s[0], acc[m][0]);
+                acc[m][1] = fmaf(da, s[1], acc[m][1]);
+                acc[m][2] = fmaf(db, s[2], acc[m][2]);
+                acc[m][3] = fmaf(db, s[3], acc[m][3]);
             }
         }
-        __syncthreads();
+    };
+    for (;;) {
+        int done = -1;  // a unit whose sums are complete in acc
+        if (ahead < p.stages - 1 || c.at < c.end) {
+            __syncwarp();
+            fill();
+            if (ahead < p.stages - 1) {
+                ++ahead;
+                continue;
+            }
+            if (p.stages == kStages) cp_async_wait<kStages - 1>();
+            else cp_async_wait<1>();
+            __syncwarp();
+            if (entered || (c.chunk & 1) == 0) {
+                scales = from_scales + group_use;
+                group_use = group_use + kGroupBytes == group_bytes ? 0u : group_use + kGroupBytes;
+                entered = false;
+            }
+            if (np == 8) multiply(std::true_type());
+            else multiply(std::false_type());
+            use_at = use_at + kStageBytes == ring_bytes ? 0u : use_at + kStageBytes;
+            vec += kChunk * per_block;
+            ++c.at;
+            if (++c.chunk == c.chunks) {
+                if (head) deposit();
+                else done = c.unit;
+                head = false;
+                c.chunk = 0;
+                vec = column;
+                ++c.unit;
+            }
+        } else if (begun) {
+            // ---- the part's end: a unit cut between warps is joined by the one that began it
+            begun = false;
+            bool open = c.chunk != 0;
+            if (open && head) {
+                deposit();
+                open = false;
+            }
+            __syncthreads();
+            if (open) {
+                const int unit_end = c.at - c.chunk + c.chunks;  // as items
+                const unsigned items = (unsigned)items_of(c.v, c.chunks);
+#pragma unroll 1
+                for (int w = warp + 1, end = c.end; w < W && end < unit_end; ++w) {
+                    const int to = (int)(items * (unsigned)(w + 1) / W);
+                    if (to == end) continue;
+                    end = to;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += deposits[(w * 8 + i) * 32 + lane];
+                }
+                done = c.unit;
+            }
+        } else {
+            // ---- the next part: the segment's vectors, in two parts
+            if (c.v == v_hi) break;
+            enter(c, c.v + 1);
+            if (!waited) {
+                grid_dependency_wait();
+                for (int s = tid; s < p.slots; s += kThreads) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + s / p.per_in));
+                waited = true;
+                __syncthreads();
+            }
+            begun = true;
+            if (c.at >= c.end) c.chunk = 0;
+            head = c.chunk != 0;
+            entered = true;
+            const int seg = c.v / p.parts;
+            n = tab.seg_n[seg], at = tab.seg_at[seg];
+            np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8;  // columns kept of each part
+            per_block = (uint32_t)np * 128u;
+            // A lane's column of a block: slot g of the first part, and of the second behind it; with up to 4 slots the second
+            // part has columns 4 to 7, and with fewer the columns behind them repeat them.
+            column = frags + (np == 8 ? g : (g >> 2) * np + (g & (np - 1))) * 64 + t4 * 16;
+            vec = column + (uint32_t)c.chunk * (kChunk * per_block);
+            float* const to_back = tab.back[c.v & 1];
+            back = to_back;
+            if (tid < n) {
+                const int k = tab.exponent[tab.list[at + tid]];
+                to_back[tid] = k == kNotFinite ? qnan() : pow2i(-k);
+            }
+            const int only = GateUp && n == 1 ? tab.list[at] / p.per_in : -1;
+            if (only < 0 || only != staged) {
+                // Four lanes take a block of a vector; a thread's loads of two blocks are in flight together.
+                const int per_vector = c.chunks * kChunk * 4;
+                int j = 0, i = tid;
+#pragma unroll 1
+                for (bool more = true; more;) {
+                    float4 x[kStageLoads][2];
+                    uint32_t to[kStageLoads];
+                    float scale[kStageLoads];
+                    int loads = 0;
+#pragma unroll
+                    for (int u = 0; u < kStageLoads; ++u) {
+                        while (i >= per_vector) i -= per_vector, ++j;
+                        x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (j < n) {
+                            const int slot = tab.list[at + j], b = i >> 2, t = i & 3;
+                            scale[u] = pow2i(tab.exponent[slot]);
+                            to[u] = frags + b * per_block + j * 64 + t * 16;
+                            if (b < c.blocks) {
+                                const float* from = p.in + (long long)(slot / p.per_in) * (p.blocks * 32) + (c.block0 + b) * 32 + t * 4;
+                                x[u][0] = __ldcg(reinterpret_cast<const float4*>(from));
+                                x[u][1] = __ldcg(reinterpret_cast<const float4*>(from + 16));
+                            }
+                            ++loads;
+                        }
+                        i += kThreads;
+                    }
+                    more = loads == kStageLoads;
+#pragma unroll
+                    for (int u = 0; u < kStageLoads; ++u) {
+                        if (u >= loads) break;
+                        const float pair[4][2] = {{x[u][0].x, x[u][0].z}, {x[u][1].x, x[u][1].z}, {x[u][0].y, x[u][0].w}, {x[u][1].y, x[u][1].w}};
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float a = pair[q][0] * scale[u], b = pair[q][1] * scale[u];
+                            const __half2 h = __floats2half2_rn(a, b);
+                            const float2 f2 = __half22float2(h);
+                            hi[q] = bits_of(h);
+                            lo[q] = bits_of(__floats2half2_rn(a - f2.x, b - f2.y));
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u]), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
+                                     "r"(hi[3])
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u] + np * 64), "r"(lo[0]), "r"(lo[1]),
+                                     "r"(lo[2]), "r"(lo[3])
+                                     : "memory");
+                    }
+                }
+                staged = only;
+            }
+            __syncthreads();
+        }
 
-        // ---- products
-        float acc[2][4];
-        auto clear = [&]() {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-        };
-        // A unit's sums leave: joined over the parts of the vectors, scaled back, and for gate and up as silu(g) * u.
-        auto finish = [&](int unit) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (np <= 4) acc[m][i] += __shfl_xor_sync(0xffffffffu, acc[m][i], 2);
-            const int part = v % p.parts;
+        if (done >= 0) {
+            // ---- a unit's sums leave: joined over the parts of the vectors, scaled back, for gate and up as silu(g) * u
+            const bool wide = np == 8;
             unsigned big[2] = {0u, 0u};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = 2 * t4 + (i & 1), r = g + (i >> 1) * 8;
-                if (j >= n || (np <= 4 && t4 >= 2)) continue;
+                float u[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float other = __shfl_xor_sync(0xffffffffu, acc[m][i], 2);
+                    u[m] = wide ? acc[m][i] : acc[m][i] + other;
+                    acc[m][i] = 0.f;
+                }
+                if (j >= n || (!wide && t4 >= 2)) continue;
                 const float b = back[j];
                 const long long slot = tab.list[at + j];
                 if (GateUp) {
-                    const float h = silu(acc[0][i] * b) * (acc[1][i] * b);
-                    p.out[slot * p.rows + unit * 16 + r] = h;
+                    const float h = silu(u[0] * b) * (u[1] * b);
+                    p.out[slot * p.rows + done * 16 + r] = h;
                     big[i & 1] = max(big[i & 1], __float_as_uint(h) & 0x7fffffffu);
                 } else {
-                    float* out = p.out + ((long long)part * p.slots + slot) * p.rows + unit * 32;
+                    float* out = p.out + ((long long)(c.v % p.parts) * p.slots + slot) * p.rows + done * 32;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
-                        if (unit * 32 + m * 16 + r < p.rows) out[m * 16 + r] = acc[m][i] * b;
+                        if (done * 32 + m * 16 + r < p.rows) out[m * 16 + r] = u[m] * b;
                 }
             }
             if (GateUp) {
@@ -433,125 +645,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const ExpertPar
 #pragma unroll
                     for (int o = 4; o <= 16; o <<= 1) big[q] = max(big[q], __shfl_xor_sync(0xffffffffu, big[q], o));
                     const int j = 2 * t4 + q;
-                    if (g == 0 && j < n && !(np <= 4 && t4 >= 2)) atomicMax(p.out_max + tab.list[at + j], big[q]);
+                    if (g == 0 && j < n && (wide || t4 < 2)) atomicMax(p.out_max + tab.list[at + j], big[q]);
                 }
             }
-            clear();
-        };
-        auto products = [&](auto wide, uint32_t stage, uint32_t fr) {
-            constexpr bool Wide = decltype(wide)::value;
-            const uint32_t part_bytes = (uint32_t)np * 64u;
-            const uint32_t mine = fr + (Wide ? (uint32_t)g * 64u : (uint32_t)(g >> 2) * part_bytes + (uint32_t)(g & 3) * 64u) + t4 * 16;
-            const bool column = Wide || (g & 3) < np;
-            float2 d[2][2][2];  // scales of rows g and g + 8, blocks 0, 1 and 2, 3
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t a, b;
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                 : "=r"(a), "=r"(b)
-                                 : "r"(stage + kScalesAt + (m * 16 + h * 8 + g) * 8));
-                    d[m][h][0] = __half22float2(half2_of(a));
-                    d[m][h][1] = __half22float2(half2_of(b));
-                }
-#pragma unroll
-            for (int pair = 0; pair < 2; ++pair) {
-                uint32_t w[2][4];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    ldsm4(stage + m * 1024 + lm_row * 64 + (((2 * pair + lm_half) ^ ((lm_row >> 1) & 3)) << 4), w[m]);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t from = mine + (2 * pair + b) * per_block;
-                    uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-                    if (column) h = lds128(from);
-                    if (Wide) l = lds128(from + part_bytes);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t ra[4], rb[4];
-                        codes_of(w[m][2 * b], k1024, ra);
-                        codes_of(w[m][2 * b + 1], k1024, rb);
-                        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                        float s[4];
-                        mma(s, ra[0], rb[0], ra[1], rb[1], h.x, h.y, zero);
-                        mma(s, ra[2], rb[2], ra[3], rb[3], h.z, h.w, s);
-                        if (Wide) {
-                            mma(s, ra[0], rb[0], ra[1], rb[1], l.x, l.y, s);
-                            mma(s, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s);
-                        }
-                        const float da = b ? d[m][0][pair].y : d[m][0][pair].x, db = b ? d[m][1][pair].y : d[m][1][pair].x;
-                        acc[m][0] = fmaf(da, s[0], acc[m][0]);
-                        acc[m][1] = fmaf(da, s[1], acc[m][1]);
-                        acc[m][2] = fmaf(db, s[2], acc[m][2]);
-                        acc[m][3] = fmaf(db, s[3], acc[m][3]);
-                    }
-                }
-            }
-        };
-        auto deposit = [&]() {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) deposits[(warp * 8 + i) * 32 + lane] = acc[i >> 2][i & 3];
-            clear();
-        };
-        clear();
-        const int first_item = c.at;
-        bool head = c.chunk != 0;  // the unit was begun by a warp before this one, which joins it
-        while (c.at < c.end) {
-            if (p.stages == kStages) cp_async_wait<kStages - 2>();
-            else cp_async_wait<0>();
-            __syncwarp();
-            fill();
-            const uint32_t stage = ring + use_at;
-            const uint32_t fr = frags + (uint32_t)(c.chunk * kChunk) * per_block;
-            if (np == 8) products(std::integral_constant<bool, true>(), stage, fr);
-            else products(std::integral_constant<bool, false>(), stage, fr);
-            use_at = use_at + kStageBytes == ring_bytes ? 0u : use_at + kStageBytes;
-            ++c.at;
-            if (++c.chunk == c.chunks) {
-                if (head) deposit();
-                else finish(c.unit);
-                head = false;
-                c.chunk = 0;
-                ++c.unit;
-            }
-        }
-        if (first_item < c.end && head) deposit();
-        const bool tail = first_item < c.end && !head && c.chunk != 0;  // begun here, not done
-        __syncthreads();
-        if (tail) {
-            const int unit_end = c.at - c.chunk + c.chunks;  // as items
-            for (int w = warp + 1, end = c.end; w < kWarps && end < unit_end; ++w) {
-                const unsigned items = (unsigned)((v == v_hi ? (int)(u_hi - (long long)v * units) : units) -
-                                                  (v == v_lo ? (int)(u_lo - (long long)v * units) : 0)) * (unsigned)c.chunks;
-                const int to = (int)(items * (unsigned)(w + 1) / kWarps);
-                if (to == end) continue;
-                end = to;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += deposits[(w * 8 + i) * 32 + lane];
-            }
-            finish(c.unit);
         }
     }
 }
 
 // The launch shape of one matrix (or gate and up): parts, slots of a segment, shared memory.
 struct ExpertPlan {
-    int parts, cap, stages;
+    int parts, part_blocks, cap, stages;
     uint32_t ring_at, deposits_at, frags_at, smem;
 };
 int moe_parts(int blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
-ExpertPlan plan_experts(int blocks, bool cut, int max_smem) {
+ExpertPlan plan_experts(int blocks, bool cut, int warps, int max_smem) {
     ExpertPlan l;
     l.parts = cut ? moe_parts(blocks) : 1;
-    const int per = ((blocks + l.parts - 1) / l.parts + kChunk - 1) / kChunk * kChunk;
+    const int per = l.part_blocks = ((blocks + l.parts - 1) / l.parts + 7) / 8 * 8;  // whole groups of scales
     l.cap = 0;
     for (int stages = kStages; stages >= 2; --stages)
         for (int cap = kMaxCap; cap >= 1; cap /= 2) {
             l.cap = cap, l.stages = stages;
             l.ring_at = (sizeof(Tables) + 127) / 128 * 128;
-            l.deposits_at = l.ring_at + (uint32_t)(kWarps * stages) * kStageBytes;
-            l.frags_at = l.deposits_at + kWarps * 8 * 32 * 4;
+            l.deposits_at = l.ring_at + (uint32_t)(warps * stages) * kSlotBytes;
+            l.frags_at = l.deposits_at + (uint32_t)warps * 8 * 32 * 4;
             l.smem = l.frags_at + (uint32_t)per * cap * 128u;
             if (l.smem <= (uint32_t)max_smem) return l;
         }
@@ -559,21 +676,36 @@ ExpertPlan plan_experts(int blocks, bool cut, int max_smem) {
     return l;
 }
 
-template <bool GateUp>
-cudaError_t launch_experts(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
-    const ExpertPlan l = plan_experts(p.blocks, !GateUp, di.max_smem_optin);
-    if (l.cap == 0) return cudaErrorNotSupported;
-    p.parts = l.parts, p.cap = l.cap, p.stages = l.stages;
-    p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
-    const uintptr_t d = reinterpret_cast<uintptr_t>(p.d0) | reinterpret_cast<uintptr_t>(p.d1);
-    p.scale_bytes = p.blocks % 4 == 0 && d % 8 == 0 ? 8 : p.blocks % 2 == 0 && d % 4 == 0 ? 4 : 2;
-    auto kern = moe_expert_kernel<GateUp>;
+template <bool GateUp, int W, int PER>
+cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ctas, const DeviceInfo& di, bool overlap,
+                              cudaStream_t s) {
+    auto kern = moe_expert_kernel<GateUp, W, PER>;
     static std::once_flag once[64];
     cudaError_t e = cudaSuccess;
     std::call_once(once[di.device & 63],
                    [&] { e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin); });
     if (e != cudaSuccess) return e;
-    return launch_grid(kern, dim3((unsigned)di.sm_count), dim3(kThreads), l.smem, s, overlap, p);
+    return launch_grid(kern, dim3((unsigned)(di.sm_count * ctas)), dim3(W * 32), l.smem, s, overlap, p);
+}
+
+template <bool GateUp>
+cudaError_t launch_experts(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
+    const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
+    ExpertPlan l = plan_experts(p.blocks, !GateUp, 8, half);
+    const bool two = l.cap >= 4 && l.stages == kStages && p.slots <= 2 * p.E && p.slots <= 256;
+    if (!two) l = plan_experts(p.blocks, !GateUp, 16, di.max_smem_optin);
+    const bool eight = l.cap == 0;  // the longest vectors leave room for 8 warps
+    if (eight) l = plan_experts(p.blocks, !GateUp, 8, di.max_smem_optin);
+    if (l.cap == 0) return cudaErrorNotSupported;
+    p.units = GateUp ? p.rows / 16 : (p.rows + 31) / 32;
+    p.parts = l.parts, p.part_blocks = l.part_blocks, p.cap = l.cap, p.stages = l.stages;
+    p.table_bits = 1;
+    while ((1 << p.table_bits) < 2 * p.slots) ++p.table_bits;
+    p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
+    const uintptr_t d = reinterpret_cast<uintptr_t>(p.d0) | reinterpret_cast<uintptr_t>(p.d1);
+    p.scale_bytes = p.blocks % 8 == 0 && d % 16 == 0 ? 16 : p.blocks % 4 == 0 && d % 8 == 0 ? 8 : p.blocks % 2 == 0 && d % 4 == 0 ? 4 : 2;
+    if (two) return launch_experts_as<GateUp, 8, 1>(p, l, 2, di, overlap, s);
+    return eight ? launch_experts_as<GateUp, 8, 2>(p, l, 1, di, overlap, s) : launch_experts_as<GateUp, 16, 1>(p, l, 1, di, overlap, s);
 }
 
 // The largest size in each row of [rows][cols], as its bits.
