@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const PrepParams p) {
 // ---- the experts' products -------------------------------------------------------------------------------------------
 //
 // One kernel for gate and up (with SwiGLU) and for down. Slots that go to the same expert form a segment of up to `cap`
-// (8, or fewer where the vectors are long); long inputs of the down projection are cut into parts whose sums the join adds. A
+// (8, of one part 16, or fewer where the vectors are long); long inputs of the down projection are cut into parts whose sums the join adds. A
 // segment's rows are units of 32: 16 of gate and the same 16 of up, or 32 of down. All units lie on one line that is cut
 // into equal pieces, one for each CTA (one CTA an SM), and a piece's chunks of 4 blocks (128 columns) are cut into equal
 // pieces for its warps. So every weight is read once a segment, and a warp adds a unit's chunks in registers; a unit cut
@@ -102,9 +102,11 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const PrepParams p) {
 //
 // Products run on m16n8k16 matrix instructions with the weights as rows: ldmatrix brings a block's word to each lane, eight
 // codes become eight exact f16 values code - 8 with nine instructions, and a block's fp32 sums are multiplied by the block's
-// scale in fp32. The columns are the segment's vectors in two f16 parts (x = hi + lo to 2^-22), scaled by a power of two that
-// puts a vector's largest element near 2^14: with up to 4 slots both parts share an instruction's 8 columns, with more each
-// part has its own and both add into the same sums. The parts lie in shared memory in the order in which lanes take them.
+// scale in fp32. The columns are the segment's vectors in f16, scaled by a power of two that puts a vector's largest element
+// near 2^14. fp32 and f16 layers hold a vector in two parts (x = hi + lo to 2^-22): with up to 4 slots both parts share an
+// instruction's 8 columns, with more each part has its own and both add into the same sums. bf16 layers hold one part: 11
+// bits, an error of 2^-11 at most where the layer's own output is rounded by 2^-8, and twice the slots in an instruction. The
+// parts lie in shared memory in the order in which lanes take them.
 constexpr int kStages = 3;                       // of a warp's ring; 2 where the vectors leave no room
 constexpr int kChunk = 4;                        // blocks of a chunk
 constexpr uint32_t kStageBytes = 2048;           // a stage: 32 rows x 64 bytes of codes
@@ -112,7 +114,7 @@ constexpr uint32_t kGroupBytes = 512;            // 32 rows x 8 scales: those of
 constexpr uint32_t kSlotBytes = kStageBytes + kGroupBytes;
 constexpr int kMaxSlots = 512;
 constexpr int kStageLoads = 2;
-constexpr int kMaxCap = 8;
+constexpr int kMaxCap = 16;
 constexpr int kPartBlocks = 88;                  // most blocks of a part: 8 slots' fit beside the ring
 
 struct ExpertParams {
@@ -200,9 +202,11 @@ struct Cursor {
 
 // PER: slots of a thread. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
 // that finishes a unit): a call runs each instruction few times, and fetching them costs as much as running them.
-template <bool GateUp, int W, int PER>
+template <bool GateUp, int Parts, int W, int PER>
 __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const ExpertParams p) {
     constexpr int kThreads = W * 32;
+    constexpr int kNarrow = Parts == 2 ? 4 : 8;    // slots in one instruction's columns
+    constexpr int kTiles = Parts == 2 ? 1 : 2;     // sums of 8 slots that a warp keeps
     extern __shared__ __align__(128) uint8_t smem[];
     Tables& tab = *reinterpret_cast<Tables*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -422,18 +426,20 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     int ahead = 0, n = 0, at = 0, np = 1, staged = -1;
     uint32_t per_block = 0, column = 0, vec = 0, scales = 0;
     const float* back = tab.back[0];
-    float acc[2][4] = {};
+    const int sums = Parts == 1 && p.cap > kNarrow ? 16 : 8;  // that a warp may deposit
+    float acc[kTiles][2][4] = {};
     auto deposit = [&]() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            deposits[(warp * 8 + i) * 32 + lane] = acc[i >> 2][i & 3];
-            acc[i >> 2][i & 3] = 0.f;
+        for (int i = 0; i < 8 * kTiles; ++i) {
+            if (i >= 8 && np <= kNarrow) break;
+            deposits[(warp * sums + i) * 32 + lane] = acc[i >> 3][i >> 2 & 1][i & 3];
+            acc[i >> 3][i >> 2 & 1][i & 3] = 0.f;
         }
     };
-    // One chunk. Everything that it needs from shared memory is asked for before any of it is used (the second part of wide
-    // columns excepted, for which there are no registers).
+    // One chunk. Everything that it needs from shared memory is asked for before any of it is used (the second columns of
+    // wide segments excepted, for which there are no registers).
     auto multiply = [&](auto wide) {
-        constexpr bool Wide = decltype(wide)::value;  // 8 columns for each part
+        constexpr bool Wide = decltype(wide)::value;  // 16 columns: two parts of 8 slots, or 16 slots
         const uint32_t codes = from_codes + use_at, sc = scales + ((c.chunk & 1) << 3);
         uint32_t w[2][2][4], scale[2][2][2];  // codes of (pair of blocks, tile); scales of (tile, rows g or g + 8)
 #pragma unroll
@@ -460,19 +466,25 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                 codes_of(w[b >> 1][m][2 * (b & 1)], k1024, ra);
                 codes_of(w[b >> 1][m][2 * (b & 1) + 1], k1024, rb);
                 const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                float s[4];
+                float s[4], s2[4];
                 mma(s, ra[0], rb[0], ra[1], rb[1], x[b].x, x[b].y, zero);
                 mma(s, ra[2], rb[2], ra[3], rb[3], x[b].z, x[b].w, s);
                 if (Wide) {
-                    mma(s, ra[0], rb[0], ra[1], rb[1], l.x, l.y, s);
-                    mma(s, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s);
+                    if (Parts == 1) {
+                        mma(s2, ra[0], rb[0], ra[1], rb[1], l.x, l.y, zero);
+                        mma(s2, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s2);
+                    } else {
+                        mma(s, ra[0], rb[0], ra[1], rb[1], l.x, l.y, s);
+                        mma(s, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s);
+                    }
                 }
                 const __half2 pa = half2_of(scale[m][0][b >> 1]), pb = half2_of(scale[m][1][b >> 1]);
                 const float da = (b & 1) ? __high2float(pa) : __low2float(pa), db = (b & 1) ? __high2float(pb) : __low2float(pb);
-                acc[m][0] = fmaf(da, s[0], acc[m][0]);
-                acc[m][1] = fmaf(da, s[1], acc[m][1]);
-                acc[m][2] = fmaf(db, s[2], acc[m][2]);
-                acc[m][3] = fmaf(db, s[3], acc[m][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[0][m][i] = fmaf(i < 2 ? da : db, s[i], acc[0][m][i]);
+                    if (Wide && Parts == 1) acc[kTiles - 1][m][i] = fmaf(i < 2 ? da : db, s2[i], acc[kTiles - 1][m][i]);
+                }
             }
         }
     };
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                 group_use = group_use + kGroupBytes == group_bytes ? 0u : group_use + kGroupBytes;
                 entered = false;
             }
-            if (np == 8) multiply(std::true_type());
+            if (np > kNarrow) multiply(std::true_type());
             else multiply(std::false_type());
             use_at = use_at + kStageBytes == ring_bytes ? 0u : use_at + kStageBytes;
             vec += kChunk * per_block;
@@ -524,7 +536,10 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                     if (to == end) continue;
                     end = to;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += deposits[(w * 8 + i) * 32 + lane];
+                    for (int i = 0; i < 8 * kTiles; ++i) {
+                        if (i >= 8 && np <= kNarrow) break;
+                        acc[i >> 3][i >> 2 & 1][i & 3] += deposits[(w * sums + i) * 32 + lane];
+                    }
                 }
                 done = c.unit;
             }
@@ -544,11 +559,11 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
             entered = true;
             const int seg = c.v / p.parts;
             n = tab.seg_n[seg], at = tab.seg_at[seg];
-            np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8;  // columns kept of each part
-            per_block = (uint32_t)np * 128u;
+            np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16;  // columns kept of each part
+            per_block = (uint32_t)np * (Parts * 64u);
             // A lane's column of a block: slot g of the first part, and of the second behind it; with up to 4 slots the second
             // part has columns 4 to 7, and with fewer the columns behind them repeat them.
-            column = frags + (np == 8 ? g : (g >> 2) * np + (g & (np - 1))) * 64 + t4 * 16;
+            column = frags + (Parts == 1 || np == 8 ? g & (np - 1) : (g >> 2) * np + (g & (np - 1))) * 64 + t4 * 16;
             vec = column + (uint32_t)c.chunk * (kChunk * per_block);
             float* const to_back = tab.back[c.v & 1];
             back = to_back;
@@ -601,7 +616,8 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u]), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
                                      "r"(hi[3])
                                      : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u] + np * 64), "r"(lo[0]), "r"(lo[1]),
+                        if (Parts == 2)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u] + np * 64), "r"(lo[0]), "r"(lo[1]),
                                      "r"(lo[2]), "r"(lo[3])
                                      : "memory");
                     }
@@ -613,39 +629,44 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
 
         if (done >= 0) {
             // ---- a unit's sums leave: joined over the parts of the vectors, scaled back, for gate and up as silu(g) * u
-            const bool wide = np == 8;
-            unsigned big[2] = {0u, 0u};
+            const bool joined = Parts == 2 && np <= kNarrow;  // columns 4 to 7 are the second part of columns 0 to 3
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 2 * t4 + (i & 1), r = g + (i >> 1) * 8;
-                float u[2];
+            for (int tile = 0; tile < kTiles; ++tile) {
+                if (tile == 1 && np <= kNarrow) break;
+                unsigned big[2] = {0u, 0u};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float other = __shfl_xor_sync(0xffffffffu, acc[m][i], 2);
-                    u[m] = wide ? acc[m][i] : acc[m][i] + other;
-                    acc[m][i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const int j = tile * 8 + 2 * t4 + (i & 1), r = g + (i >> 1) * 8;
+                    float u[2];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        float& sum = acc[tile][m][i];
+                        u[m] = Parts == 2 ? __shfl_xor_sync(0xffffffffu, sum, 2) : 0.f;
+                        u[m] = joined ? sum + u[m] : sum;
+                        sum = 0.f;
+                    }
+                    if (j >= n || (joined && t4 >= 2)) continue;
+                    const float b = back[j];
+                    const long long slot = tab.list[at + j];
+                    if (GateUp) {
+                        const float h = silu(u[0] * b) * (u[1] * b);
+                        p.out[slot * p.rows + done * 16 + r] = h;
+                        big[i & 1] = max(big[i & 1], __float_as_uint(h) & 0x7fffffffu);
+                    } else {
+                        float* out = p.out + ((long long)(c.v % p.parts) * p.slots + slot) * p.rows + done * 32;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            if (done * 32 + m * 16 + r < p.rows) out[m * 16 + r] = u[m] * b;
+                    }
                 }
-                if (j >= n || (!wide && t4 >= 2)) continue;
-                const float b = back[j];
-                const long long slot = tab.list[at + j];
                 if (GateUp) {
-                    const float h = silu(u[0] * b) * (u[1] * b);
-                    p.out[slot * p.rows + done * 16 + r] = h;
-                    big[i & 1] = max(big[i & 1], __float_as_uint(h) & 0x7fffffffu);
-                } else {
-                    float* out = p.out + ((long long)(c.v % p.parts) * p.slots + slot) * p.rows + done * 32;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-                        if (done * 32 + m * 16 + r < p.rows) out[m * 16 + r] = u[m] * b;
-                }
-            }
-            if (GateUp) {
+                    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) big[q] = max(big[q], __shfl_xor_sync(0xffffffffu, big[q], o));
-                    const int j = 2 * t4 + q;
-                    if (g == 0 && j < n && (wide || t4 < 2)) atomicMax(p.out_max + tab.list[at + j], big[q]);
+                        for (int o = 4; o <= 16; o <<= 1) big[q] = max(big[q], __shfl_xor_sync(0xffffffffu, big[q], o));
+                        const int j = tile * 8 + 2 * t4 + q;
+                        if (g == 0 && j < n && !(joined && t4 >= 2)) atomicMax(p.out_max + tab.list[at + j], big[q]);
+                    }
                 }
             }
         }
@@ -658,28 +679,28 @@ struct ExpertPlan {
     uint32_t ring_at, deposits_at, frags_at, smem;
 };
 int moe_parts(int blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
-ExpertPlan plan_experts(int blocks, bool cut, int warps, int max_smem) {
+ExpertPlan plan_experts(int blocks, bool cut, int vector_parts, int warps, int max_smem) {
     ExpertPlan l;
     l.parts = cut ? moe_parts(blocks) : 1;
     const int per = l.part_blocks = ((blocks + l.parts - 1) / l.parts + 7) / 8 * 8;  // whole groups of scales
     l.cap = 0;
     for (int stages = kStages; stages >= 2; --stages)
-        for (int cap = kMaxCap; cap >= 1; cap /= 2) {
+        for (int cap = vector_parts == 1 ? 16 : 8; cap >= 1; cap /= 2) {
             l.cap = cap, l.stages = stages;
             l.ring_at = (sizeof(Tables) + 127) / 128 * 128;
             l.deposits_at = l.ring_at + (uint32_t)(warps * stages) * kSlotBytes;
-            l.frags_at = l.deposits_at + (uint32_t)warps * 8 * 32 * 4;
-            l.smem = l.frags_at + (uint32_t)per * cap * 128u;
+            l.frags_at = l.deposits_at + (uint32_t)warps * (cap > 8 ? 16 : 8) * 32 * 4;
+            l.smem = l.frags_at + (uint32_t)(per * cap * vector_parts) * 64u;
             if (l.smem <= (uint32_t)max_smem) return l;
         }
     l.cap = 0;
     return l;
 }
 
-template <bool GateUp, int W, int PER>
+template <bool GateUp, int Parts, int W, int PER>
 cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ctas, const DeviceInfo& di, bool overlap,
                               cudaStream_t s) {
-    auto kern = moe_expert_kernel<GateUp, W, PER>;
+    auto kern = moe_expert_kernel<GateUp, Parts, W, PER>;
     static std::once_flag once[64];
     cudaError_t e = cudaSuccess;
     std::call_once(once[di.device & 63],
@@ -688,14 +709,14 @@ cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ct
     return launch_grid(kern, dim3((unsigned)(di.sm_count * ctas)), dim3(W * 32), l.smem, s, overlap, p);
 }
 
-template <bool GateUp>
-cudaError_t launch_experts(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
+template <bool GateUp, int Parts>
+cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
     const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
-    ExpertPlan l = plan_experts(p.blocks, !GateUp, 8, half);
-    const bool two = l.cap >= 4 && l.stages == kStages && p.slots <= 2 * p.E && p.slots <= 256;
-    if (!two) l = plan_experts(p.blocks, !GateUp, 16, di.max_smem_optin);
+    ExpertPlan l = plan_experts(p.blocks, !GateUp, Parts, 8, half);
+    const bool two = l.cap >= 8 / Parts && l.stages == kStages && 2 * p.slots <= l.cap * p.E && p.slots <= 256;
+    if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 16, di.max_smem_optin);
     const bool eight = l.cap == 0;  // the longest vectors leave room for 8 warps
-    if (eight) l = plan_experts(p.blocks, !GateUp, 8, di.max_smem_optin);
+    if (eight) l = plan_experts(p.blocks, !GateUp, Parts, 8, di.max_smem_optin);
     if (l.cap == 0) return cudaErrorNotSupported;
     p.units = GateUp ? p.rows / 16 : (p.rows + 31) / 32;
     p.parts = l.parts, p.part_blocks = l.part_blocks, p.cap = l.cap, p.stages = l.stages;
@@ -704,8 +725,14 @@ cudaError_t launch_experts(ExpertParams p, const DeviceInfo& di, bool overlap, c
     p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
     const uintptr_t d = reinterpret_cast<uintptr_t>(p.d0) | reinterpret_cast<uintptr_t>(p.d1);
     p.scale_bytes = p.blocks % 8 == 0 && d % 16 == 0 ? 16 : p.blocks % 4 == 0 && d % 8 == 0 ? 8 : p.blocks % 2 == 0 && d % 4 == 0 ? 4 : 2;
-    if (two) return launch_experts_as<GateUp, 8, 1>(p, l, 2, di, overlap, s);
-    return eight ? launch_experts_as<GateUp, 8, 2>(p, l, 1, di, overlap, s) : launch_experts_as<GateUp, 16, 1>(p, l, 1, di, overlap, s);
+    if (two) return launch_experts_as<GateUp, Parts, 8, 1>(p, l, 2, di, overlap, s);
+    return eight ? launch_experts_as<GateUp, Parts, 8, 2>(p, l, 1, di, overlap, s)
+                 : launch_experts_as<GateUp, Parts, 16, 1>(p, l, 1, di, overlap, s);
+}
+
+template <bool GateUp>
+cudaError_t launch_experts(const ExpertParams& p, int dtype, const DeviceInfo& di, bool overlap, cudaStream_t s) {
+    return dtype == Q4_BF16 ? launch_experts_of<GateUp, 1>(p, di, overlap, s) : launch_experts_of<GateUp, 2>(p, di, overlap, s);
 }
 
 // The largest size in each row of [rows][cols], as its bits.
@@ -806,12 +833,12 @@ struct DownSpace {
 };
 
 cudaError_t launch_down(const DownSpace& w, const float* h, const uint8_t* qs, const uint16_t* d, const int32_t* ids, int slots,
-                        int E, int rows, int cols, const DeviceInfo& di, cudaStream_t s) {
+                        int E, int rows, int cols, int dtype, const DeviceInfo& di, cudaStream_t s) {
     ExpertParams p = {};
     p.qs0 = p.qs1 = qs, p.d0 = p.d1 = d;
     p.in = h, p.in_max = w.h_max, p.out = w.z, p.ids = ids;
     p.E = E, p.rows = rows, p.blocks = cols / 32, p.slots = slots, p.per_in = 1;
-    return launch_experts<false>(p, di, true, s);
+    return launch_experts<false>(p, dtype, di, true, s);
 }
 
 }  // namespace
@@ -834,7 +861,7 @@ cudaError_t launch_moe_down(const MoeDownArgs& a, int dtype, void* workspace, co
     cfg.attrs = attr, cfg.numAttrs = launch_overlap() ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, moe_max_kernel, a.h, w.h_max, a.cols);
     if (e != cudaSuccess) return e;
-    if ((e = launch_down(w, a.h, a.qs, a.d, a.ids, slots, a.E, a.rows, a.cols, di, s)) != cudaSuccess) return e;
+    if ((e = launch_down(w, a.h, a.qs, a.d, a.ids, slots, a.E, a.rows, a.cols, dtype, di, s)) != cudaSuccess) return e;
     const JoinParams join = {a.out, a.residual, w.z, a.weights, a.ids, a.topk, a.E, a.rows, moe_parts(a.cols / 32), slots,
                              a.out_stride, a.residual_stride, a.status, a.fault};
     return launch_join(join, a.T, dtype, true, s);
@@ -874,8 +901,8 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a, int dtype, void* workspace, 
     up.qs0 = a.w.gate_qs, up.qs1 = a.w.up_qs, up.d0 = a.w.gate_d, up.d1 = a.w.up_d;
     up.in = w.xn, up.in_max = w.x_max, up.out = w.h, up.out_max = w.down.h_max, up.ids = ids;
     up.E = E, up.rows = N, up.blocks = K / 32, up.slots = slots, up.per_in = a.topk;
-    if ((e = launch_experts<true>(up, di, true, s)) != cudaSuccess) return e;
-    if ((e = launch_down(w.down, w.h, a.w.down_qs, a.w.down_d, ids, slots, E, K, N, di, s)) != cudaSuccess) return e;
+    if ((e = launch_experts<true>(up, dtype, di, true, s)) != cudaSuccess) return e;
+    if ((e = launch_down(w.down, w.h, a.w.down_qs, a.w.down_d, ids, slots, E, K, N, dtype, di, s)) != cudaSuccess) return e;
     const JoinParams join = {a.out, a.residual, w.down.z, weights, ids, a.topk, E, K, moe_parts(N / 32), slots, a.out_stride,
                              a.residual_stride, nullptr, a.fault};
     return launch_join(join, a.T, dtype, true, s);

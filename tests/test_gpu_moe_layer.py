@@ -42,7 +42,7 @@ def check_down(a, out, keep=None):
     want, err = ref.down(a["h"].double(), torch.zeros_like(a["h"], dtype=torch.float64),
                          lambda e: ref.q4_matrix(a["qs"][e], a["d"][e]) if 0 <= e < E else None, a["expert_ids"].long(),
                          a["expert_weights"].double(), torch.zeros_like(a["expert_weights"], dtype=torch.float64), a["residual"],
-                         out.shape[1])
+                         out.shape[1], ref.one_part(out.dtype))
     lim = err + ref.rounded(want, out.dtype) * (1 + 2.0 ** -7)
     if keep is not None:
         out, want, lim = out[keep], want[keep], lim[keep]
