@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const PrepParams p) {
 // instruction's 8 columns, with more each part has its own and both add into the same sums. bf16 layers hold one part: 11
 // bits, an error of 2^-11 at most where the layer's own output is rounded by 2^-8, and twice the slots in an instruction. The
 // parts lie in shared memory in the order in which lanes take them.
-constexpr int kStages = 3;                       // of a warp's ring; 2 where the vectors leave no room
+constexpr int kStages = 3;                       // of a warp's ring
 constexpr int kChunk = 4;                        // blocks of a chunk
 constexpr uint32_t kStageBytes = 2048;           // a stage: 32 rows x 64 bytes of codes
 constexpr uint32_t kGroupBytes = 512;            // 32 rows x 8 scales: those of two chunks, in a ring of their own
@@ -126,7 +126,7 @@ struct ExpertParams {
     unsigned* out_max;         // as in_max, of the outputs (gate and up)
     const int32_t* ids;
     int E, rows, blocks, slots, per_in;  // slot s reads input row s / per_in
-    int units, parts, part_blocks, cap, stages, scale_bytes, table_bits;
+    int units, parts, part_blocks, cap, scale_bytes, table_bits;
     uint32_t ring_at, deposits_at, frags_at;
 };
 
@@ -193,13 +193,6 @@ __device__ __forceinline__ int vector_exponent(unsigned m) {
     return m == 0u ? 0 : m >= 0x7f800000u ? kNotFinite : min(141 - (int)(m >> 23), 126);
 }
 
-// A warp's chunks of one segment and part: the items [at, end) of (unit, chunk), counted from the CTA's first unit there.
-struct Cursor {
-    int v, at, end;    // v: segment * parts + part
-    int unit, chunk;   // of `at`
-    int chunks, block0, blocks;  // of the part
-};
-
 // PER: slots of a thread. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
 // that finishes a unit): a call runs each instruction few times, and fetching them costs as much as running them.
 template <bool GateUp, int Parts, int W, int PER>
@@ -209,8 +202,8 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     constexpr int kTiles = Parts == 2 ? 1 : 2;     // sums of 8 slots that a warp keeps
     extern __shared__ __align__(128) uint8_t smem[];
     Tables& tab = *reinterpret_cast<Tables*>(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t base = smem_addr(smem), ring = base + p.ring_at + (uint32_t)(warp * p.stages) * kSlotBytes, frags = base + p.frags_at;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const uint32_t base = smem_addr(smem), ring = base + p.ring_at + (uint32_t)(warp * kStages) * kSlotBytes, frags = base + p.frags_at;
     float* deposits = reinterpret_cast<float*>(smem + p.deposits_at);
 
     // Segments: the slots of an expert in their order, `cap` at a time, experts in the order of their first slots. A hash
@@ -232,7 +225,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         for (int i = 0; i < PER; ++i) {
             const int s = tid * PER + i;
             e[i] = s < p.slots ? __ldcg(p.ids + s) : -1;
-            if (GateUp && s < p.slots) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + s / p.per_in));
+            if (GateUp && s < p.slots) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + (unsigned)s / (unsigned)p.per_in));
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -298,44 +291,73 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         __syncthreads();
     }
 
-    // The CTA's piece of the line of units.
+    // The CTA's piece of the line of units. What is the same in a warp is passed through a shuffle, so that branches on it
+    // need no reconvergence.
+    segs = __shfl_sync(0xffffffffu, segs, 0);
     const unsigned all = (unsigned)(segs * p.parts * p.units), quotient = all / gridDim.x, rest = all - quotient * gridDim.x;
-    const int u_lo = (int)(quotient * blockIdx.x + rest * blockIdx.x / gridDim.x);
-    const int u_hi = (int)(quotient * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / gridDim.x);
+    const unsigned u_lo = quotient * blockIdx.x + rest * blockIdx.x / gridDim.x;
+    const unsigned u_hi = quotient * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / gridDim.x;
     if (u_lo >= u_hi) {
         if (!GateUp) grid_dependency_wait();
         return;
     }
-    const int v_lo = u_lo / p.units, v_hi = (u_hi - 1) / p.units;
-    auto first_unit = [&](int v) { return v == v_lo ? u_lo - v * p.units : 0; };
-    auto items_of = [&](int v, int chunks) { return ((v == v_hi ? u_hi - v * p.units : p.units) - first_unit(v)) * chunks; };
-    auto enter = [&](Cursor& c, int v) {
-        const int part = v % p.parts;
-        c.v = v;
-        c.block0 = part * p.part_blocks;
+    const unsigned units = (unsigned)p.units, v_lo = u_lo / units, v_hi = (u_hi - 1) / units;  // v: segment * parts + part
+    auto first_unit = [&](unsigned v) { return v == v_lo ? u_lo - v * units : 0u; };
+    auto unit_count = [&](unsigned v) { return (v == v_hi ? u_hi - v * units : units) - first_unit(v); };
+    auto segment_of = [&](unsigned v) { return GateUp ? v : v / (unsigned)p.parts; };
+    auto part_of = [&](unsigned v) { return GateUp ? 0u : v % (unsigned)p.parts; };
+    // A warp's chunks of one segment and part: items of (unit, chunk), counted from the CTA's first unit there.
+    struct Piece {
+        unsigned at, end, chunks;
+        int unit, chunk, block0, blocks;  // unit and chunk of `at`
+    };
+    auto piece_of = [&](unsigned v) {
+        Piece c;
+        c.block0 = (int)part_of(v) * p.part_blocks;
         c.blocks = min(p.part_blocks, p.blocks - c.block0);
-        c.chunks = (c.blocks + kChunk - 1) / kChunk;
-        const unsigned items = (unsigned)items_of(v, c.chunks);
-        c.at = (int)(items * (unsigned)warp / W);
-        c.end = (int)(items * (unsigned)(warp + 1) / W);
-        const int unit = c.at / c.chunks;
-        c.chunk = c.at - unit * c.chunks;
-        c.unit = first_unit(v) + unit;
+        c.chunks = (unsigned)(c.blocks + kChunk - 1) / kChunk;
+        const unsigned items = unit_count(v) * c.chunks;
+        c.at = items * (unsigned)warp / W, c.end = items * (unsigned)(warp + 1) / W;
+        const unsigned unit = c.at / c.chunks;
+        c.chunk = c.at == c.end ? 0 : (int)(c.at - unit * c.chunks);
+        c.unit = (int)(first_unit(v) + unit);
+        return c;
     };
 
     // ---- the ring: stages are filled in the order in which they are used, across segments
-    Cursor f = {};
-    f.v = v_lo - 1;
-    const uint32_t ring_bytes = (uint32_t)p.stages * kStageBytes, group_bytes = (uint32_t)p.stages * kGroupBytes;
-    uint32_t fill_at = 0, use_at = 0;  // stages of the ring, as offsets
-    uint32_t group_fill = 0, group_use = 0;  // groups of scales: a group is new at every even chunk and at a piece's first
-    bool fresh = true;
+    constexpr uint32_t kRing = kStages * kStageBytes, kGroups = kStages * kGroupBytes;
+    constexpr int kRows = GateUp ? 16 : 32;  // of one matrix in a unit
+    unsigned f_v = v_lo, f_left = 0;         // items left of the piece
+    int f_chunk = 0, f_chunks = 0, f_blocks = 0;  // the next item's chunk
+    uint32_t fill_at = 0, group_fill = 0;    // offsets in the two rings
+    bool group = true;                       // the next item needs the scales of its two chunks
     const int r4 = lane >> 2, c4 = lane & 3;
-    const uint32_t to_codes = ring + r4 * 64 + ((c4 ^ ((r4 >> 1) & 3)) << 4), to_scales = ring + ring_bytes + lane * 16;
+    const uint32_t to_codes = ring + r4 * 64 + ((c4 ^ ((r4 >> 1) & 3)) << 4), to_scales = ring + kRing + lane * 16;
     const long long row_bytes = (long long)p.blocks * 16;
-    const char *src0 = nullptr, *src1 = nullptr, *src_d = nullptr;  // of this lane, at the cursor
-    int rows_left = 32;                                        // of the unit, all of them for gate and up
-    auto fill_edge = [&](int left, bool group, int group_left) {  // past the last column or row: zeros
+    const char *src0 = nullptr, *src1 = nullptr, *src_d = nullptr;  // of this lane, of the next item
+    long long code_step = 0, scale_step = 0;  // from the last chunk of a unit to the next unit
+    int rows_left = 32;                       // of the unit, all of them for gate and up
+    auto next_piece = [&]() {  // f_v: the first that is not begun
+        for (; f_left == 0 && f_v <= v_hi; ++f_v) {
+            const Piece c = piece_of(f_v);
+            f_left = c.end - c.at;
+            if (f_left == 0) continue;
+            f_chunk = c.chunk, f_chunks = (int)c.chunks, f_blocks = c.blocks;
+            const int e = __shfl_sync(0xffffffffu, tab.seg_e[segment_of(f_v)], 0);
+            const long long first = (long long)e * p.rows + c.unit * kRows, second = GateUp ? first : first + 16;
+            const int block = c.block0 + c.chunk * kChunk, pair = block & ~(2 * kChunk - 1);
+            src0 = reinterpret_cast<const char*>(p.qs0) + (first + r4) * row_bytes + (block + c4) * 16;
+            src1 = reinterpret_cast<const char*>(p.qs1) + (second + r4) * row_bytes + (block + c4) * 16;
+            src_d = reinterpret_cast<const char*>(lane < 16 ? p.d0 : p.d1) +
+                    (((lane < 16 ? first : second) + (lane & 15)) * p.blocks + pair) * 2;
+            code_step = kRows * row_bytes - (f_chunks - 1) * (kChunk * 16);
+            scale_step = ((long long)kRows * p.blocks - (f_chunks - 1) / 2 * (2 * kChunk)) * 2;
+            if (!GateUp) rows_left = p.rows - c.unit * 32;
+            group = true;
+        }
+    };
+    auto fill_edge = [&]() {  // past the last column or row: zeros
+        const int left = f_blocks - f_chunk * kChunk;
         const char* none = reinterpret_cast<const char*>(p.qs0);
         const uint32_t to = to_codes + fill_at;
 #pragma unroll 1
@@ -346,7 +368,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         }
         if (!group) return;
         const uint32_t to_d = to_scales + group_fill;
-        const int valid = lane < rows_left ? min(group_left, 8) : 0;
+        const int valid = lane < rows_left ? min(f_blocks - (f_chunk & ~1) * kChunk, 8) : 0;
         if (p.scale_bytes == 2) {
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
@@ -359,22 +381,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         }
     };
     auto fill = [&]() {
-        if (f.at >= f.end) {
-            while (f.at >= f.end && f.v < v_hi) enter(f, f.v + 1);
-            if (f.at < f.end) {
-                const long long first = (long long)tab.seg_e[f.v / p.parts] * p.rows + (GateUp ? f.unit * 16 : f.unit * 32);
-                const long long second = GateUp ? first : first + 16;
-                const int block = f.block0 + f.chunk * kChunk, group = block & ~(2 * kChunk - 1);
-                src0 = reinterpret_cast<const char*>(p.qs0) + (first + r4) * row_bytes + (block + c4) * 16;
-                src1 = reinterpret_cast<const char*>(p.qs1) + (second + r4) * row_bytes + (block + c4) * 16;
-                src_d = reinterpret_cast<const char*>(lane < 16 ? p.d0 : p.d1) +
-                        (((lane < 16 ? first : second) + (lane & 15)) * p.blocks + group) * 2;
-                if (!GateUp) rows_left = p.rows - f.unit * 32;
-                fresh = true;
-            }
-        }
-        if (f.at < f.end) {
-            const bool group = fresh || (f.chunk & 1) == 0;
+        if (f_left != 0) {
             if (p.scale_bytes >= 8 && (GateUp || rows_left >= 32)) {  // 8, 16: rows of whole chunks
                 const uint32_t to = to_codes + fill_at, to_d = to_scales + group_fill;
                 copy_async<16>(to, src0, 16u);
@@ -385,250 +392,131 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                     if (p.scale_bytes == 16) {
                         copy_async<16>(to_d, src_d, 16u);
                     } else {
+                        const bool more = (f_chunk | 1) < f_chunks;
                         copy_async<8>(to_d, src_d, 8u);
-                        const bool more = (f.chunk | 1) < f.chunks;
                         copy_async<8>(to_d + 8, more ? src_d + 8 : src_d, more ? 8u : 0u);
                     }
                 }
             } else {
-                fill_edge(f.blocks - f.chunk * kChunk, group, f.blocks - (f.chunk & ~1) * kChunk);
+                fill_edge();
             }
-            if (group) group_fill = group_fill + kGroupBytes == group_bytes ? 0u : group_fill + kGroupBytes;
-            fresh = false;
-            src0 += kChunk * 16, src1 += kChunk * 16;
-            if (f.chunk & 1) src_d += 2 * kChunk * 2;
-            ++f.at;
-            if (++f.chunk == f.chunks) {  // on to the next unit of the part
-                const int rows = GateUp ? 16 : 32;
-                src_d += ((long long)rows * p.blocks - f.chunks / 2 * (2 * kChunk)) * 2;
-                src0 += rows * row_bytes - f.chunks * (kChunk * 16), src1 += rows * row_bytes - f.chunks * (kChunk * 16);
-                f.chunk = 0;
-                ++f.unit;
+            fill_at = fill_at + kStageBytes == kRing ? 0u : fill_at + kStageBytes;
+            if (group) group_fill = group_fill + kGroupBytes == kGroups ? 0u : group_fill + kGroupBytes;
+            group = f_chunk & 1;
+            if (++f_chunk == f_chunks) {  // on to the next unit
+                src0 += code_step, src1 += code_step, src_d += scale_step;
+                f_chunk = 0;
+                group = true;
                 if (!GateUp) rows_left -= 32;
+            } else {
+                src0 += kChunk * 16, src1 += kChunk * 16;
+                if (group) src_d += 2 * kChunk * 2;
             }
+            if (--f_left == 0) next_piece();
         }
-        fill_at = fill_at + kStageBytes == ring_bytes ? 0u : fill_at + kStageBytes;
         cp_async_commit();
     };
+    next_piece();
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) fill();
 
     uint32_t k1024;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
     const int g = lane >> 2, t4 = lane & 3;
     // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8: rows 0-7 and 8-15 of a block, then of the next one
     const int lm_row = (lane & 7) + (lane & 8);
-    const uint32_t from_codes = ring + lm_row * 64 + (((lane >> 4) ^ ((lm_row >> 1) & 3)) << 4), from_scales = ring + ring_bytes + g * 16;
-
-    Cursor c = {};
-    c.v = v_lo - 1;
-    bool begun = false, waited = GateUp;  // a part is under way; the vectors are there
-    bool head = false;                    // the unit was begun by a warp before this one, which joins it
-    bool entered = false;                 // the next item is the part's first
-    int ahead = 0, n = 0, at = 0, np = 1, staged = -1;
-    uint32_t per_block = 0, column = 0, vec = 0, scales = 0;
-    const float* back = tab.back[0];
+    const uint32_t from_codes = ring + lm_row * 64 + (((lane >> 4) ^ ((lm_row >> 1) & 3)) << 4), from_scales = ring + kRing + g * 16;
+    uint32_t use_at = 0, group_use = 0;
     const int sums = Parts == 1 && p.cap > kNarrow ? 16 : 8;  // that a warp may deposit
     float acc[kTiles][2][4] = {};
-    auto deposit = [&]() {
-#pragma unroll
-        for (int i = 0; i < 8 * kTiles; ++i) {
-            if (i >= 8 && np <= kNarrow) break;
-            deposits[(warp * sums + i) * 32 + lane] = acc[i >> 3][i >> 2 & 1][i & 3];
-            acc[i >> 3][i >> 2 & 1][i & 3] = 0.f;
-        }
-    };
-    // One chunk. Everything that it needs from shared memory is asked for before any of it is used (the second columns of
-    // wide segments excepted, for which there are no registers).
-    auto multiply = [&](auto wide) {
-        constexpr bool Wide = decltype(wide)::value;  // 16 columns: two parts of 8 slots, or 16 slots
-        const uint32_t codes = from_codes + use_at, sc = scales + ((c.chunk & 1) << 3);
-        uint32_t w[2][2][4], scale[2][2][2];  // codes of (pair of blocks, tile); scales of (tile, rows g or g + 8)
-#pragma unroll
-        for (int pair = 0; pair < 2; ++pair)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) ldsm4((pair ? codes ^ 32u : codes) + m * 1024, w[pair][m]);
-        uint4 x[kChunk];
-#pragma unroll
-        for (int b = 0; b < kChunk; ++b) x[b] = lds128(vec + b * (Wide ? 1024u : per_block));
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                             : "=r"(scale[m][h][0]), "=r"(scale[m][h][1])
-                             : "r"(sc + m * 256 + h * 128));
-#pragma unroll
-        for (int b = 0; b < kChunk; ++b) {
-            uint4 l = x[b];
-            if (Wide) l = lds128(vec + b * 1024u + 512u);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint32_t ra[4], rb[4];
-                codes_of(w[b >> 1][m][2 * (b & 1)], k1024, ra);
-                codes_of(w[b >> 1][m][2 * (b & 1) + 1], k1024, rb);
-                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                float s[4], s2[4];
-                mma(s, ra[0], rb[0], ra[1], rb[1], x[b].x, x[b].y, zero);
-                mma(s, ra[2], rb[2], ra[3], rb[3], x[b].z, x[b].w, s);
-                if (Wide) {
-                    if (Parts == 1) {
-                        mma(s2, ra[0], rb[0], ra[1], rb[1], l.x, l.y, zero);
-                        mma(s2, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s2);
-                    } else {
-                        mma(s, ra[0], rb[0], ra[1], rb[1], l.x, l.y, s);
-                        mma(s, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s);
-                    }
-                }
-                const __half2 pa = half2_of(scale[m][0][b >> 1]), pb = half2_of(scale[m][1][b >> 1]);
-                const float da = (b & 1) ? __high2float(pa) : __low2float(pa), db = (b & 1) ? __high2float(pb) : __low2float(pb);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[0][m][i] = fmaf(i < 2 ? da : db, s[i], acc[0][m][i]);
-                    if (Wide && Parts == 1) acc[kTiles - 1][m][i] = fmaf(i < 2 ? da : db, s2[i], acc[kTiles - 1][m][i]);
-                }
-            }
-        }
-    };
-    for (;;) {
-        int done = -1;  // a unit whose sums are complete in acc
-        if (ahead < p.stages - 1 || c.at < c.end) {
-            __syncwarp();
-            fill();
-            if (ahead < p.stages - 1) {
-                ++ahead;
-                continue;
-            }
-            if (p.stages == kStages) cp_async_wait<kStages - 1>();
-            else cp_async_wait<1>();
-            __syncwarp();
-            if (entered || (c.chunk & 1) == 0) {
-                scales = from_scales + group_use;
-                group_use = group_use + kGroupBytes == group_bytes ? 0u : group_use + kGroupBytes;
-                entered = false;
-            }
-            if (np > kNarrow) multiply(std::true_type());
-            else multiply(std::false_type());
-            use_at = use_at + kStageBytes == ring_bytes ? 0u : use_at + kStageBytes;
-            vec += kChunk * per_block;
-            ++c.at;
-            if (++c.chunk == c.chunks) {
-                if (head) deposit();
-                else done = c.unit;
-                head = false;
-                c.chunk = 0;
-                vec = column;
-                ++c.unit;
-            }
-        } else if (begun) {
-            // ---- the part's end: a unit cut between warps is joined by the one that began it
-            begun = false;
-            bool open = c.chunk != 0;
-            if (open && head) {
-                deposit();
-                open = false;
-            }
-            __syncthreads();
-            if (open) {
-                const int unit_end = c.at - c.chunk + c.chunks;  // as items
-                const unsigned items = (unsigned)items_of(c.v, c.chunks);
+    int staged = -1;
+    bool waited = GateUp;  // the vectors are there
 #pragma unroll 1
-                for (int w = warp + 1, end = c.end; w < W && end < unit_end; ++w) {
-                    const int to = (int)(items * (unsigned)(w + 1) / W);
-                    if (to == end) continue;
-                    end = to;
-#pragma unroll
-                    for (int i = 0; i < 8 * kTiles; ++i) {
-                        if (i >= 8 && np <= kNarrow) break;
-                        acc[i >> 3][i >> 2 & 1][i & 3] += deposits[(w * sums + i) * 32 + lane];
-                    }
-                }
-                done = c.unit;
-            }
-        } else {
-            // ---- the next part: the segment's vectors, in two parts
-            if (c.v == v_hi) break;
-            enter(c, c.v + 1);
-            if (!waited) {
-                grid_dependency_wait();
-                for (int s = tid; s < p.slots; s += kThreads) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + s / p.per_in));
-                waited = true;
-                __syncthreads();
-            }
-            begun = true;
-            if (c.at >= c.end) c.chunk = 0;
-            head = c.chunk != 0;
-            entered = true;
-            const int seg = c.v / p.parts;
-            n = tab.seg_n[seg], at = tab.seg_at[seg];
-            np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16;  // columns kept of each part
-            per_block = (uint32_t)np * (Parts * 64u);
-            // A lane's column of a block: slot g of the first part, and of the second behind it; with up to 4 slots the second
-            // part has columns 4 to 7, and with fewer the columns behind them repeat them.
-            column = frags + (Parts == 1 || np == 8 ? g & (np - 1) : (g >> 2) * np + (g & (np - 1))) * 64 + t4 * 16;
-            vec = column + (uint32_t)c.chunk * (kChunk * per_block);
-            float* const to_back = tab.back[c.v & 1];
-            back = to_back;
-            if (tid < n) {
-                const int k = tab.exponent[tab.list[at + tid]];
-                to_back[tid] = k == kNotFinite ? qnan() : pow2i(-k);
-            }
-            const int only = GateUp && n == 1 ? tab.list[at] / p.per_in : -1;
-            if (only < 0 || only != staged) {
-                // Four lanes take a block of a vector; a thread's loads of two blocks are in flight together.
-                const int per_vector = c.chunks * kChunk * 4;
-                int j = 0, i = tid;
-#pragma unroll 1
-                for (bool more = true; more;) {
-                    float4 x[kStageLoads][2];
-                    uint32_t to[kStageLoads];
-                    float scale[kStageLoads];
-                    int loads = 0;
-#pragma unroll
-                    for (int u = 0; u < kStageLoads; ++u) {
-                        while (i >= per_vector) i -= per_vector, ++j;
-                        x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (j < n) {
-                            const int slot = tab.list[at + j], b = i >> 2, t = i & 3;
-                            scale[u] = pow2i(tab.exponent[slot]);
-                            to[u] = frags + b * per_block + j * 64 + t * 16;
-                            if (b < c.blocks) {
-                                const float* from = p.in + (long long)(slot / p.per_in) * (p.blocks * 32) + (c.block0 + b) * 32 + t * 4;
-                                x[u][0] = __ldcg(reinterpret_cast<const float4*>(from));
-                                x[u][1] = __ldcg(reinterpret_cast<const float4*>(from + 16));
-                            }
-                            ++loads;
-                        }
-                        i += kThreads;
-                    }
-                    more = loads == kStageLoads;
-#pragma unroll
-                    for (int u = 0; u < kStageLoads; ++u) {
-                        if (u >= loads) break;
-                        const float pair[4][2] = {{x[u][0].x, x[u][0].z}, {x[u][1].x, x[u][1].z}, {x[u][0].y, x[u][0].w}, {x[u][1].y, x[u][1].w}};
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float a = pair[q][0] * scale[u], b = pair[q][1] * scale[u];
-                            const __half2 h = __floats2half2_rn(a, b);
-                            const float2 f2 = __half22float2(h);
-                            hi[q] = bits_of(h);
-                            lo[q] = bits_of(__floats2half2_rn(a - f2.x, b - f2.y));
-                        }
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u]), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
-                                     "r"(hi[3])
-                                     : "memory");
-                        if (Parts == 2)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u] + np * 64), "r"(lo[0]), "r"(lo[1]),
-                                     "r"(lo[2]), "r"(lo[3])
-                                     : "memory");
-                    }
-                }
-                staged = only;
-            }
+    for (unsigned v = v_lo; v <= v_hi; ++v) {
+        const Piece c = piece_of(v);
+        if (!waited) {
+            grid_dependency_wait();
+            for (int s = tid; s < p.slots; s += kThreads) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + s / p.per_in));
+            waited = true;
             __syncthreads();
         }
 
-        if (done >= 0) {
-            // ---- a unit's sums leave: joined over the parts of the vectors, scaled back, for gate and up as silu(g) * u
+        // ---- the segment's vectors, in their parts
+        const int seg = (int)segment_of(v);
+        const int n = __shfl_sync(0xffffffffu, (int)tab.seg_n[seg], 0), at = __shfl_sync(0xffffffffu, (int)tab.seg_at[seg], 0);
+        const int np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16;  // columns kept of each part
+        const uint32_t per_block = (uint32_t)np * (Parts * 64u);
+        float* const back = tab.back[v & 1];
+        if (tid < n) {
+            const int k = tab.exponent[tab.list[at + tid]];
+            back[tid] = k == kNotFinite ? qnan() : pow2i(-k);
+        }
+        const int only = GateUp && n == 1 ? (int)((unsigned)tab.list[at] / (unsigned)p.per_in) : -1;
+        if (only < 0 || only != staged) {
+            // Four lanes take a block of a vector; a thread's loads of two blocks are in flight together.
+            const int per_vector = (int)c.chunks * kChunk * 4;
+            int j = 0, i = tid;
+#pragma unroll 1
+            for (bool more = true; more;) {
+                float4 x[kStageLoads][2];
+                uint32_t to[kStageLoads];
+                float scale[kStageLoads];
+                int loads = 0;
+#pragma unroll
+                for (int u = 0; u < kStageLoads; ++u) {
+                    while (i >= per_vector) i -= per_vector, ++j;
+                    x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (j < n) {
+                        const int slot = tab.list[at + j], b = i >> 2, t = i & 3;
+                        scale[u] = pow2i(tab.exponent[slot]);
+                        to[u] = frags + b * per_block + j * 64 + t * 16;
+                        if (b < c.blocks) {
+                            const int row = GateUp ? (int)((unsigned)slot / (unsigned)p.per_in) : slot;
+                            const float* from = p.in + (long long)row * (p.blocks * 32) + (c.block0 + b) * 32 + t * 4;
+                            x[u][0] = __ldcg(reinterpret_cast<const float4*>(from));
+                            x[u][1] = __ldcg(reinterpret_cast<const float4*>(from + 16));
+                        }
+                        ++loads;
+                    }
+                    i += kThreads;
+                }
+                more = loads == kStageLoads;
+#pragma unroll
+                for (int u = 0; u < kStageLoads; ++u) {
+                    if (u >= loads) break;
+                    const float pair[4][2] = {{x[u][0].x, x[u][0].z}, {x[u][1].x, x[u][1].z}, {x[u][0].y, x[u][0].w}, {x[u][1].y, x[u][1].w}};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float a = pair[q][0] * scale[u], b = pair[q][1] * scale[u];
+                        const __half2 h = __floats2half2_rn(a, b);
+                        const float2 f2 = __half22float2(h);
+                        hi[q] = bits_of(h);
+                        lo[q] = bits_of(__floats2half2_rn(a - f2.x, b - f2.y));
+                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u]), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                                 : "memory");
+                    if (Parts == 2)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u] + np * 64), "r"(lo[0]), "r"(lo[1]),
+                                     "r"(lo[2]), "r"(lo[3])
+                                     : "memory");
+                }
+            }
+            staged = only;
+        }
+        __syncthreads();
+
+        // ---- products
+        auto deposit = [&]() {
+#pragma unroll
+            for (int i = 0; i < 8 * kTiles; ++i) {
+                if (i >= 8 && np <= kNarrow) break;
+                deposits[(warp * sums + i) * 32 + lane] = acc[i >> 3][i >> 2 & 1][i & 3];
+                acc[i >> 3][i >> 2 & 1][i & 3] = 0.f;
+            }
+        };
+        // A unit's sums leave: joined over the parts of the vectors, scaled back, for gate and up as silu(g) * u.
+        auto finish = [&](int unit) {
             const bool joined = Parts == 2 && np <= kNarrow;  // columns 4 to 7 are the second part of columns 0 to 3
 #pragma unroll
             for (int tile = 0; tile < kTiles; ++tile) {
@@ -650,13 +538,13 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                     const long long slot = tab.list[at + j];
                     if (GateUp) {
                         const float h = silu(u[0] * b) * (u[1] * b);
-                        p.out[slot * p.rows + done * 16 + r] = h;
+                        p.out[slot * p.rows + unit * 16 + r] = h;
                         big[i & 1] = max(big[i & 1], __float_as_uint(h) & 0x7fffffffu);
                     } else {
-                        float* out = p.out + ((long long)(c.v % p.parts) * p.slots + slot) * p.rows + done * 32;
+                        float* out = p.out + ((long long)part_of(v) * p.slots + slot) * p.rows + unit * 32;
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
-                            if (done * 32 + m * 16 + r < p.rows) out[m * 16 + r] = u[m] * b;
+                            if (unit * 32 + m * 16 + r < p.rows) out[m * 16 + r] = u[m] * b;
                     }
                 }
                 if (GateUp) {
@@ -669,13 +557,119 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                     }
                 }
             }
-        }
+        };
+        // A lane's column of a block: slot g of the first part, and of the second behind it; with up to 4 slots the second
+        // part has columns 4 to 7, and with fewer the columns behind them repeat them.
+        const uint32_t column = frags + (Parts == 1 || np == 8 ? g & (np - 1) : (g >> 2) * np + (g & (np - 1))) * 64 + t4 * 16;
+        // A warp's chunks. What a chunk needs from shared memory is asked for before any of it is used (the second columns of
+        // wide segments excepted, for which there are no registers).
+        auto run = [&](auto wide) {
+            constexpr bool Wide = decltype(wide)::value;  // 16 columns: two parts of 8 slots, or 16 slots
+            int chunk = c.chunk, unit = c.unit;
+            bool head = chunk != 0;  // the unit was begun by a warp before this one, which joins it
+            uint32_t vec = column + (uint32_t)chunk * (kChunk * per_block), sc = from_scales + group_use + ((chunk & 1) << 3);
+#pragma unroll 1
+            for (unsigned left = c.end - c.at; left != 0; --left) {
+                cp_async_wait<kStages - 2>();
+                __syncwarp();
+                fill();
+                const uint32_t codes = from_codes + use_at;
+                uint32_t w[2][2][4], scale[2][2][2];  // codes of (pair of blocks, tile); scales of (tile, rows g or g + 8)
+#pragma unroll
+                for (int pair = 0; pair < 2; ++pair)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) ldsm4((pair ? codes ^ 32u : codes) + m * 1024, w[pair][m]);
+                uint4 x[kChunk];
+#pragma unroll
+                for (int b = 0; b < kChunk; ++b) x[b] = lds128(vec + b * (Wide ? 1024u : per_block));
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(scale[m][h][0]), "=r"(scale[m][h][1])
+                                     : "r"(sc + m * 256 + h * 128));
+#pragma unroll
+                for (int b = 0; b < kChunk; ++b) {
+                    uint4 l = x[b];
+                    if (Wide) l = lds128(vec + b * 1024u + 512u);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t ra[4], rb[4];
+                        codes_of(w[b >> 1][m][2 * (b & 1)], k1024, ra);
+                        codes_of(w[b >> 1][m][2 * (b & 1) + 1], k1024, rb);
+                        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                        float s[4], s2[4];
+                        mma(s, ra[0], rb[0], ra[1], rb[1], x[b].x, x[b].y, zero);
+                        mma(s, ra[2], rb[2], ra[3], rb[3], x[b].z, x[b].w, s);
+                        if (Wide) {
+                            if (Parts == 1) {
+                                mma(s2, ra[0], rb[0], ra[1], rb[1], l.x, l.y, zero);
+                                mma(s2, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s2);
+                            } else {
+                                mma(s, ra[0], rb[0], ra[1], rb[1], l.x, l.y, s);
+                                mma(s, ra[2], rb[2], ra[3], rb[3], l.z, l.w, s);
+                            }
+                        }
+                        const __half2 pa = half2_of(scale[m][0][b >> 1]), pb = half2_of(scale[m][1][b >> 1]);
+                        const float da = (b & 1) ? __high2float(pa) : __low2float(pa), db = (b & 1) ? __high2float(pb) : __low2float(pb);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            acc[0][m][i] = fmaf(i < 2 ? da : db, s[i], acc[0][m][i]);
+                            if (Wide && Parts == 1) acc[kTiles - 1][m][i] = fmaf(i < 2 ? da : db, s2[i], acc[kTiles - 1][m][i]);
+                        }
+                    }
+                }
+                use_at = use_at + kStageBytes == kRing ? 0u : use_at + kStageBytes;
+                const bool last = chunk + 1 == (int)c.chunks;
+                if ((chunk & 1) || last || left == 1) {
+                    group_use = group_use + kGroupBytes == kGroups ? 0u : group_use + kGroupBytes;
+                    sc = from_scales + group_use;
+                } else {
+                    sc += 8;
+                }
+                ++chunk;
+                vec += kChunk * per_block;
+                if (last) {
+                    if (head) deposit();
+                    else finish(unit);
+                    head = false;
+                    chunk = 0;
+                    vec = column;
+                    ++unit;
+                }
+            }
+            // a unit cut between warps is joined by the one that began it
+            bool open = chunk != 0 && c.end != c.at;
+            if (open && head) {
+                deposit();
+                open = false;
+            }
+            __syncthreads();
+            if (open) {
+                const unsigned items = unit_count(v) * c.chunks, unit_end = c.end - (unsigned)chunk + c.chunks;
+#pragma unroll 1
+                for (unsigned w = (unsigned)warp + 1, end = c.end; w < W && end < unit_end; ++w) {
+                    const unsigned to = items * (w + 1) / W;
+                    if (to == end) continue;
+                    end = to;
+#pragma unroll
+                    for (int i = 0; i < 8 * kTiles; ++i) {
+                        if (i >= 8 && np <= kNarrow) break;
+                        acc[i >> 3][i >> 2 & 1][i & 3] += deposits[((int)w * sums + i) * 32 + lane];
+                    }
+                }
+                finish(unit);
+            }
+        };
+        if (np > kNarrow) run(std::true_type());
+        else run(std::false_type());
     }
 }
 
 // The launch shape of one matrix (or gate and up): parts, slots of a segment, shared memory.
 struct ExpertPlan {
-    int parts, part_blocks, cap, stages;
+    int parts, part_blocks, cap;
     uint32_t ring_at, deposits_at, frags_at, smem;
 };
 int moe_parts(int blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
@@ -683,18 +677,14 @@ ExpertPlan plan_experts(int blocks, bool cut, int vector_parts, int warps, int m
     ExpertPlan l;
     l.parts = cut ? moe_parts(blocks) : 1;
     const int per = l.part_blocks = ((blocks + l.parts - 1) / l.parts + 7) / 8 * 8;  // whole groups of scales
-    l.cap = 0;
-    for (int stages = kStages; stages >= 2; --stages)
-        for (int cap = vector_parts == 1 ? 16 : 8; cap >= 1; cap /= 2) {
-            l.cap = cap, l.stages = stages;
-            l.ring_at = (sizeof(Tables) + 127) / 128 * 128;
-            l.deposits_at = l.ring_at + (uint32_t)(warps * stages) * kSlotBytes;
-            l.frags_at = l.deposits_at + (uint32_t)warps * (cap > 8 ? 16 : 8) * 32 * 4;
-            l.smem = l.frags_at + (uint32_t)(per * cap * vector_parts) * 64u;
-            if (l.smem <= (uint32_t)max_smem) return l;
-        }
-    l.cap = 0;
-    return l;
+    for (l.cap = vector_parts == 1 ? 16 : 8; l.cap >= 1; l.cap /= 2) {
+        l.ring_at = (sizeof(Tables) + 127) / 128 * 128;
+        l.deposits_at = l.ring_at + (uint32_t)(warps * kStages) * kSlotBytes;
+        l.frags_at = l.deposits_at + (uint32_t)warps * (l.cap > 8 ? 16 : 8) * 32 * 4;
+        l.smem = l.frags_at + (uint32_t)(per * l.cap * vector_parts) * 64u;
+        if (l.smem <= (uint32_t)max_smem) break;
+    }
+    return l;  // cap 0: one vector does not fit
 }
 
 template <bool GateUp, int Parts, int W, int PER>
@@ -713,13 +703,13 @@ template <bool GateUp, int Parts>
 cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
     const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
     ExpertPlan l = plan_experts(p.blocks, !GateUp, Parts, 8, half);
-    const bool two = l.cap >= 8 / Parts && l.stages == kStages && 2 * p.slots <= l.cap * p.E && p.slots <= 256;
+    const bool two = l.cap >= 8 / Parts && 2 * p.slots <= l.cap * p.E && p.slots <= 256;
     if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 16, di.max_smem_optin);
     const bool eight = l.cap == 0;  // the longest vectors leave room for 8 warps
     if (eight) l = plan_experts(p.blocks, !GateUp, Parts, 8, di.max_smem_optin);
     if (l.cap == 0) return cudaErrorNotSupported;
     p.units = GateUp ? p.rows / 16 : (p.rows + 31) / 32;
-    p.parts = l.parts, p.part_blocks = l.part_blocks, p.cap = l.cap, p.stages = l.stages;
+    p.parts = l.parts, p.part_blocks = l.part_blocks, p.cap = l.cap;
     p.table_bits = 1;
     while ((1 << p.table_bits) < 2 * p.slots) ++p.table_bits;
     p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
