@@ -47,6 +47,19 @@ struct MoeLayerArgs {
     float* weights;  // nullable
     unsigned* fault;
 };
+
+// The layer's input, and what its router's kernel leaves for the experts' kernels.
+struct LayerInput {
+    const void* x;
+    const float* gamma;  // nullable: no norm
+    float* xn;           // [T][K]: x or its norm
+    unsigned *x_max, *h_max;  // bits of the largest size in a row of xn; zeros for T * topk rows
+    float eps;
+    long long x_stride;
+};
+cudaError_t launch_moe_layer_router(int32_t* ids, float* weights, const uint8_t* qs, const uint16_t* d, const LayerInput& layer,
+                                    int dtype, int T, int E, int K, int topk, bool normalize, cudaStream_t s);
+
 size_t moe_layer_workspace_bytes(int T, int topk, int N, int K);
 cudaError_t launch_moe_layer(const MoeLayerArgs& a, int dtype, void* workspace, const DeviceInfo& di, cudaStream_t s);
 

@@ -25,72 +25,6 @@ struct Carve {  // parts of a workspace, each 16-byte aligned
     }
 };
 
-struct PrepParams {
-    const void* x;
-    const float* gamma;
-    float* xn;
-    unsigned *x_max, *h_max;
-    float eps;
-    int K, topk;
-    long long x_stride;
-};
-
-// xn[t] = x[t], or its norm, in fp32, and the bits of its largest size; the maxima of the token's h start from 0.
-template <typename T>
-__global__ void __launch_bounds__(256) moe_prep_kernel(const PrepParams p) {
-    constexpr int V = Vec<T>::N;
-    __shared__ float part[8];
-    __shared__ unsigned part_max[8];
-    const T* x = static_cast<const T*>(p.x) + (long long)blockIdx.x * p.x_stride;
-    float* xn = p.xn + (long long)blockIdx.x * p.K;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    float r = 1.f;
-    if (p.gamma) {
-        float sum = 0.f;
-        for (int k = threadIdx.x * V; k < p.K; k += 256 * V) {
-            float v[V];
-            load_floats(x + k, v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum = fmaf(v[j], v[j], sum);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-        __syncthreads();
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += part[i];
-        r = rsqrtf(sum / (float)p.K + p.eps);
-    }
-    unsigned m = 0u;
-    for (int k = threadIdx.x * V; k < p.K; k += 256 * V) {
-        float v[V];
-        load_floats(x + k, v);
-        if (p.gamma) {
-            float g[V];
-            load_floats(p.gamma + k, g);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = v[j] * r * g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-#pragma unroll
-        for (int j = 0; j < V; j += 4)
-            *reinterpret_cast<float4*>(xn + k + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) part_max[threadIdx.x >> 5] = m;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) m = max(m, part_max[i]);
-        p.x_max[blockIdx.x] = m;
-    }
-    for (int i = threadIdx.x; i < p.topk; i += 256) p.h_max[blockIdx.x * p.topk + i] = 0u;
-}
-
-
 // ---- the experts' products -------------------------------------------------------------------------------------------
 //
 // One kernel for gate and up (with SwiGLU) and for down. Slots that go to the same expert form a segment of up to `cap`
@@ -759,39 +693,58 @@ struct JoinParams {
     unsigned* fault;
 };
 
-// out[t] = residual[t] + sum_s weights[t][s] * z[t][s], in the order of the slots.
+// out[t] = residual[t] + sum_s weights[t][s] * z[t][s], in the order of the slots. The picks and the residual were written
+// before the kernel before this one began, so they are read while it runs.
 template <typename T>
 __global__ void __launch_bounds__(128) moe_join_kernel(const JoinParams p) {
     const int t = blockIdx.y, n = (blockIdx.x * 128 + threadIdx.x) * 4;
+    const bool in = n < p.rows;
+    constexpr int kAtOnce = 8;
+    int e[kAtOnce];
+    float w[kAtOnce];
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s) {
+        const bool there = in && s < p.topk;
+        e[s] = there ? __ldcg(p.ids + t * p.topk + s) : 0;
+        w[s] = there ? __ldcg(p.weights + t * p.topk + s) : 0.f;
+    }
+    float v[4] = {};
+    if (in && p.residual) {
+        const T* r = static_cast<const T*>(p.residual) + t * p.residual_stride + n;
+        if constexpr (sizeof(T) == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(r));
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else {
+            const uint2 u = __ldcg(reinterpret_cast<const uint2*>(r));
+            const float2 a = unpack2(u.x, T()), b = unpack2(u.y, T());
+            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        }
+    }
     grid_dependency_wait();
     grid_launch_dependents();
-    if (n >= p.rows) return;
-    float v[4] = {};
-    if (p.residual) {
-        const T* r = static_cast<const T*>(p.residual) + t * p.residual_stride + n;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (float)r[j];
-    }
+    if (!in) return;
     bool bad = false;
-    for (int s = 0; s < p.topk; ++s) {
-        const long long slot = (long long)t * p.topk + s;
-        const int e = p.ids[slot];
+    auto add = [&](int s, int e, float w) {
         if (e < 0 || e >= p.E) {
             bad = true;
-            continue;
+            return;
         }
-        const float w = p.weights[slot];
+        const float* from = p.z + ((long long)t * p.topk + s) * p.rows + n;
         float z[4];
-        load_floats(p.z + slot * p.rows + n, z);
+        load_floats(from, z);
         for (int q = 1; q < p.parts; ++q) {
             float more[4];
-            load_floats(p.z + ((long long)q * p.slots + slot) * p.rows + n, more);
+            load_floats(from + (long long)q * p.slots * p.rows, more);
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[j] += more[j];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf(w, z[j], v[j]);
-    }
+    };
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s)
+        if (s < p.topk) add(s, e[s], w[s]);
+    for (int s = kAtOnce; s < p.topk; ++s) add(s, p.ids[t * p.topk + s], p.weights[t * p.topk + s]);
     if (bad) {  // an expert that is not there: the token's row is NaN
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = qnan();
@@ -879,14 +832,10 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a, int dtype, void* workspace, 
     const LayerSpace w(c, a.T, a.topk, N, K);
     int32_t* ids = a.ids ? a.ids : w.ids;
     float* weights = a.weights ? a.weights : w.weights;
-    const PrepParams prep = {a.x, a.gamma, w.xn, w.x_max, w.down.h_max, a.eps, K, a.topk, a.x_stride};
-    cudaError_t e = with_dtype(dtype, [&](auto tag) {
-        return launch_grid(moe_prep_kernel<decltype(tag)>, dim3((unsigned)a.T), dim3(256), 0, s, launch_overlap(), prep);
-    });
+    const LayerInput in = {a.x, a.gamma, w.xn, w.x_max, w.down.h_max, a.eps, a.x_stride};
+    cudaError_t e = launch_moe_layer_router(ids, weights, a.w.router_qs, a.w.router_d, in, dtype, a.T, E, K, a.topk,
+                                            a.normalize != 0, s);
     if (e != cudaSuccess) return e;
-    if ((e = launch_moe_router(ids, weights, nullptr, a.w.router_qs, a.w.router_d, w.xn, a.T, E, K, a.topk, a.normalize != 0,
-                               s)) != cudaSuccess)
-        return e;
     ExpertParams up = {};
     up.qs0 = a.w.gate_qs, up.qs1 = a.w.up_qs, up.d0 = a.w.gate_d, up.d1 = a.w.up_d;
     up.in = w.xn, up.in_max = w.x_max, up.out = w.h, up.out_max = w.down.h_max, up.ids = ids;

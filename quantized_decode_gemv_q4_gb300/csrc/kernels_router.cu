@@ -2,7 +2,8 @@
 //
 // Problem (spark_model `gemm_quant.rs`, moe_gate_topk_fused): gate[e] = x . Wgate[e] for every expert, then the
 // indices of the K largest logits and their softmax weights (optionally renormalised over the K). Here Wgate is
-// planar Q4 (E rows of K weights, the library's format) and x is fp32; one token per CTA row of the grid.
+// planar Q4 (E rows of K weights, the library's format) and x is fp32; one token per CTA row of the grid. The layer form takes
+// x in the layer's type, norms it first, and leaves the fp32 vector, its largest size and zeroed maxima for the experts.
 //
 // Kernel shape (one cluster of CS CTAs per token; the router matrix is small and stays in L2 after the first
 // cluster reads it):
@@ -21,8 +22,8 @@
 #include <algorithm>
 #include <mutex>
 
-#include "device_common.cuh"
-#include "launch.h"
+#include "block.h"
+#include "kv_common.cuh"
 
 namespace q4 {
 
@@ -37,6 +38,7 @@ struct RouterParams {
     const float* x;
     int T, E, K, nblk, topk, normalize;
     uint32_t xs_off, aux_off, lg_off;
+    LayerInput layer;
 };
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -57,8 +59,13 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank) {
     return v;
 }
 
-template <int W, int CS>
+// In: the layer form's type of x; void: the plain form.
+template <int W, int CS, typename In>
 __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParams p) {
+    constexpr bool Layer = !std::is_same_v<In, void>;
+    using X = std::conditional_t<Layer, In, float>;
+    __shared__ float part_sum[W];
+    __shared__ unsigned part_max[W];
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -78,12 +85,52 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
         const float* xt = p.x + (size_t)t * p.K;
         const int t4 = lane & 3;
         const int nthr = (p.nblk * 4 + 31) & ~31;
+        const X* const row = Layer ? static_cast<const X*>(p.layer.x) + (long long)t * p.layer.x_stride : nullptr;
+        float r = 1.f;
+        unsigned largest = 0u;
+        if (Layer && p.layer.gamma) {
+            float sum = 0.f;
+            for (int i = threadIdx.x; i < p.nblk * 4; i += W * 32) {
+                float v[8];
+                load_floats(row + i * 8, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) part_sum[warp] = sum;
+            __syncthreads();
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum += part_sum[i];
+            r = rsqrtf(sum / (float)p.K + p.layer.eps);
+        }
         for (int thr = threadIdx.x; thr < nthr; thr += W * 32) {
             const int blk = thr >> 2;
             const bool in = blk < p.nblk;
             const float4* src = reinterpret_cast<const float4*>(xt) + (size_t)blk * 8 + 2 * t4;
-            const float4 a = in ? __ldg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 b = in ? __ldg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if constexpr (!Layer) {
+                a = in ? __ldg(src) : a;
+                b = in ? __ldg(src + 1) : b;
+            } else if (in) {
+                const int k = thr * 8;
+                float v[8];
+                load_floats(row + k, v);
+                if (p.layer.gamma) {
+                    float gm[8];
+                    load_floats(p.layer.gamma + k, gm);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * gm[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) largest = max(largest, __float_as_uint(v[j]) & 0x7fffffffu);
+                a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
+                if (c == 0) {
+                    float4* to = reinterpret_cast<float4*>(p.layer.xn + (size_t)t * p.K + k);
+                    to[0] = a, to[1] = b;
+                }
+            }
             const Stage4 st = stage_block4(a, b, t4 >> 1);
             if (in) {
                 const uint32_t a0 = xs + xs_chunk_offset(0u, (uint32_t)(2 * t4), (uint32_t)blk, 1u);
@@ -99,7 +146,19 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
                                  : "memory");
             }
         }
+        if (Layer) {
+            largest = __reduce_max_sync(0xffffffffu, largest);
+            if (lane == 0) part_max[warp] = largest;
+        }
         __syncthreads();
+        if (Layer && c == 0) {
+            if (threadIdx.x == 0) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) largest = max(largest, part_max[i]);
+                p.layer.x_max[t] = largest;
+            }
+            for (int i = threadIdx.x; i < p.topk; i += W * 32) p.layer.h_max[t * p.topk + i] = 0u;
+        }
         // each block's -8 offset term: the unit chain on codes of 8 over its staged quads
         for (int b = threadIdx.x; b < p.nblk; b += W * 32) {
             float4 xq[8];
@@ -270,13 +329,14 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
 
 }  // namespace
 
-cudaError_t launch_moe_router(int32_t* ids, float* weights, float* logits, const uint8_t* qs, const uint16_t* d,
-                              const float* x, int T, int E, int K, int topk, bool normalize, cudaStream_t s) {
+static cudaError_t launch_router(int32_t* ids, float* weights, float* logits, const uint8_t* qs, const uint16_t* d,
+                                 const float* x, const LayerInput* layer, int dtype, int T, int E, int K, int topk,
+                                 bool normalize, cudaStream_t s) {
     DeviceInfo di;
     cudaError_t e = current_device_info(&di);
     if (e != cudaSuccess) return e;
     constexpr int W = 8, CS = 8;
-    RouterParams p;
+    RouterParams p = {};
     p.ids = ids;
     p.weights = weights;
     p.logits = logits;
@@ -289,35 +349,60 @@ cudaError_t launch_moe_router(int32_t* ids, float* weights, float* logits, const
     p.nblk = K / 32;
     p.topk = topk;
     p.normalize = normalize ? 1 : 0;
+    if (layer) p.layer = *layer;
     const uint32_t xsb = xs_chunk_bytes(1u, (uint32_t)p.nblk);
     const uint32_t axb = aux_bytes(1u, (uint32_t)p.nblk);
     p.xs_off = 0;
     p.aux_off = xsb;
     p.lg_off = xsb + axb;
     const uint32_t smem = p.lg_off + (uint32_t)E * 4u;
-    if (smem > (uint32_t)di.max_smem_optin) return cudaErrorNotSupported;
-    auto kern = moe_router_kernel<W, CS>;
-    static std::once_flag attr_once[64];
-    std::call_once(attr_once[di.device & 63], [&] {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin);
+    auto launch = [&](auto kern, std::once_flag* attr_once) {
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaSuccess;
+        std::call_once(attr_once[di.device & 63], [&] {
+            e = cudaFuncGetAttributes(&fa, kern);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         di.max_smem_optin - (int)fa.sharedSizeBytes);
+        });
+        if (e != cudaSuccess) return e;
+        // one cluster of CS CTAs per token (CS = 8 is the portable cluster size)
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(T * CS));
+        cfg.blockDim = dim3((unsigned)(W * 32));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CS;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = launch_overlap() ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, kern, p);
+    };
+    constexpr uint32_t kPartBytes = W * 8;  // the layer form's sums and maxima
+    if (smem + (layer ? kPartBytes : 0u) > (uint32_t)di.max_smem_optin) return cudaErrorNotSupported;
+    if (!layer) {
+        static std::once_flag once[64];
+        return launch(moe_router_kernel<W, CS, void>, once);
+    }
+    return with_dtype(dtype, [&](auto tag) {
+        static std::once_flag once[64];
+        return launch(moe_router_kernel<W, CS, decltype(tag)>, once);
     });
-    if (e != cudaSuccess) return e;
-    // one cluster of CS CTAs per token (CS = 8 is the portable cluster size)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(T * CS));
-    cfg.blockDim = dim3((unsigned)(W * 32));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = launch_overlap() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+cudaError_t launch_moe_router(int32_t* ids, float* weights, float* logits, const uint8_t* qs, const uint16_t* d,
+                              const float* x, int T, int E, int K, int topk, bool normalize, cudaStream_t s) {
+    return launch_router(ids, weights, logits, qs, d, x, nullptr, Q4_F32, T, E, K, topk, normalize, s);
+}
+
+cudaError_t launch_moe_layer_router(int32_t* ids, float* weights, const uint8_t* qs, const uint16_t* d, const LayerInput& layer,
+                                    int dtype, int T, int E, int K, int topk, bool normalize, cudaStream_t s) {
+    return launch_router(ids, weights, nullptr, qs, d, nullptr, &layer, dtype, T, E, K, topk, normalize, s);
 }
 
 }  // namespace q4
