@@ -49,6 +49,7 @@ constexpr uint32_t kSlotBytes = kStageBytes + kGroupBytes;
 constexpr int kMaxSlots = 512;
 constexpr int kStageLoads = 2;
 constexpr int kMaxCap = 16;
+constexpr unsigned kNarrowCost = 4, kWideCost = 5;  // of a unit of a segment whose columns fill one instruction, or two
 constexpr int kPartBlocks = 88;                  // most blocks of a part: 8 slots' fit beside the ring
 
 struct ExpertParams {
@@ -140,7 +141,8 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     const uint32_t base = smem_addr(smem), ring = base + p.ring_at + (uint32_t)(warp * kStages) * kSlotBytes, frags = base + p.frags_at;
     float* deposits = reinterpret_cast<float*>(smem + p.deposits_at);
 
-    // Segments: the slots of an expert in their order, `cap` at a time, experts in the order of their first slots. A hash
+    // Segments: the slots of an expert in their order, `cap` at a time, experts in the order of their first slots, those with
+    // more columns than one instruction's behind the others. A hash
     // table of experts, each with the bits of its slots, lies where the ring and the vectors lie later.
     const int words = (p.slots + 31) / 32, entries = 1 << p.table_bits;
     uint16_t* const list_base = reinterpret_cast<uint16_t*>(smem + p.ring_at);
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     // itself before it lets this kernel start), so everything up to the first vectors runs while it ends.
     if (GateUp) grid_dependency_wait();
     grid_launch_dependents();
-    int segs = 0;
+    int narrows = 0, wides = 0;
     {
         int e[PER], entry[PER];
 #pragma unroll
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
             }
         }
         __syncthreads();
-        int first[PER], rank[PER], total[PER], mine = 0, slots = 0;
+        int first[PER], rank[PER], total[PER], narrow = 0, wide = 0, slots = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int s = tid * PER + i;
@@ -188,10 +190,16 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                     rank[i] += w < s >> 5 ? __popc(m) : w == s >> 5 ? __popc(m & ((1u << (s & 31)) - 1u)) : 0;
                     if (m) first[i] = w * 32 + __ffs(m) - 1;
                 }
-                if (rank[i] == 0) mine += (total[i] + p.cap - 1) / p.cap, slots += total[i];
+                if (rank[i] == 0) {
+                    const int full = total[i] / p.cap, more = total[i] - full * p.cap;
+                    wide += (p.cap > kNarrow ? full : 0) + (more > kNarrow);
+                    narrow += (p.cap > kNarrow ? 0 : full) + (more > 0 && more <= kNarrow);
+                    slots += total[i];
+                }
             }
         }
-        int both = mine << 16 | slots;  // sums up to 512 each
+        const int mine = narrow << 20 | wide << 10 | slots;  // sums up to 512 each
+        int both = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, both, o);
@@ -199,22 +207,24 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         }
         if (lane == 31) tab.warp_sums[warp] = both;
         __syncthreads();
-        int before = both - (mine << 16 | slots);
+        int before = both - mine, sum = 0;
 #pragma unroll 4
         for (int w = 0; w < W; ++w) {
             if (w < warp) before += tab.warp_sums[w];
-            segs += tab.warp_sums[w] >> 16;
+            sum += tab.warp_sums[w];
         }
-        int seg = before >> 16, at = before & 0xffff;
+        narrows = sum >> 20, wides = sum >> 10 & 1023;
+        int seg_narrow = before >> 20, seg_wide = narrows + (before >> 10 & 1023), at = before & 1023;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (total[i] == 0 || rank[i] != 0) continue;
             list_base[tid * PER + i] = (uint16_t)at;
 #pragma unroll 1
-            for (int o = 0; o < total[i]; o += p.cap, ++seg) {
+            for (int o = 0; o < total[i]; o += p.cap) {
+                const int count = min(p.cap, total[i] - o), seg = count > kNarrow ? seg_wide++ : seg_narrow++;
                 tab.seg_e[seg] = e[i];
                 tab.seg_at[seg] = (uint16_t)(at + o);
-                tab.seg_n[seg] = (uint8_t)min(p.cap, total[i] - o);
+                tab.seg_n[seg] = (uint8_t)count;
             }
             at += total[i];
         }
@@ -227,10 +237,16 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
 
     // The CTA's piece of the line of units. What is the same in a warp is passed through a shuffle, so that branches on it
     // need no reconvergence.
-    segs = __shfl_sync(0xffffffffu, segs, 0);
-    const unsigned all = (unsigned)(segs * p.parts * p.units), quotient = all / gridDim.x, rest = all - quotient * gridDim.x;
-    const unsigned u_lo = quotient * blockIdx.x + rest * blockIdx.x / gridDim.x;
-    const unsigned u_hi = quotient * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / gridDim.x;
+    const unsigned per_segment = (unsigned)(p.parts * p.units);
+    const unsigned narrow_units = (unsigned)__shfl_sync(0xffffffffu, narrows, 0) * per_segment;
+    const unsigned cost_narrow = narrow_units * kNarrowCost;
+    const unsigned cost = cost_narrow + (unsigned)__shfl_sync(0xffffffffu, wides, 0) * per_segment * kWideCost;
+    const unsigned quotient = cost / gridDim.x, rest = cost - quotient * gridDim.x;
+    auto cut = [&](unsigned i) {  // the first unit of piece i
+        const unsigned at = quotient * i + rest * i / gridDim.x;
+        return at <= cost_narrow ? at / kNarrowCost : narrow_units + (at - cost_narrow) / kWideCost;
+    };
+    const unsigned u_lo = cut(blockIdx.x), u_hi = cut(blockIdx.x + 1);
     if (u_lo >= u_hi) {
         if (!GateUp) grid_dependency_wait();
         return;
@@ -513,9 +529,12 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                 for (int pair = 0; pair < 2; ++pair)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) ldsm4((pair ? codes ^ 32u : codes) + m * 1024, w[pair][m]);
-                uint4 x[kChunk];
+                uint4 x[kChunk], y[kChunk];
 #pragma unroll
-                for (int b = 0; b < kChunk; ++b) x[b] = lds128(vec + b * (Wide ? 1024u : per_block));
+                for (int b = 0; b < kChunk; ++b) {
+                    x[b] = lds128(vec + b * (Wide ? 1024u : per_block));
+                    if (Wide) y[b] = lds128(vec + b * 1024u + 512u);
+                }
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -525,8 +544,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                                      : "r"(sc + m * 256 + h * 128));
 #pragma unroll
                 for (int b = 0; b < kChunk; ++b) {
-                    uint4 l = x[b];
-                    if (Wide) l = lds128(vec + b * 1024u + 512u);
+                    const uint4 l = Wide ? y[b] : x[b];
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         uint32_t ra[4], rb[4];
