@@ -366,9 +366,12 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         }
         cp_async_commit();
     };
-    next_piece();
+    auto start = [&]() {
+        next_piece();
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) fill();
+        for (int i = 0; i < kStages - 1; ++i) fill();
+    };
+    start();
 
     uint32_t k1024;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
@@ -380,80 +383,89 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     const int sums = Parts == 1 && p.cap > kNarrow ? 16 : 8;  // that a warp may deposit
     float acc[kTiles][2][4] = {};
     int staged = -1;
-    bool waited = GateUp;  // the vectors are there
 #pragma unroll 1
     for (unsigned v = v_lo; v <= v_hi; ++v) {
         const Piece c = piece_of(v);
-        if (!waited) {
+        unsigned max_bits[PER];
+        if (!GateUp && v == v_lo) {
             grid_dependency_wait();
-            for (int s = tid; s < p.slots; s += kThreads) tab.exponent[s] = (int8_t)vector_exponent(__ldcg(p.in_max + s / p.per_in));
-            waited = true;
-            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) max_bits[i] = tid * PER + i < p.slots ? __ldcg(p.in_max + tid * PER + i) : 0u;
         }
 
-        // ---- the segment's vectors, in their parts
+        // ---- the segment's vectors, in their parts. Four lanes take a block of a vector; a thread's loads of two blocks are in
+        // flight together, and what else there is to do before the first products is done while they are.
         const int seg = (int)segment_of(v);
         const int n = __shfl_sync(0xffffffffu, (int)tab.seg_n[seg], 0), at = __shfl_sync(0xffffffffu, (int)tab.seg_at[seg], 0);
         const int np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16;  // columns kept of each part
         const uint32_t per_block = (uint32_t)np * (Parts * 64u);
+        const int only = GateUp && n == 1 ? (int)((unsigned)tab.list[at] / (unsigned)p.per_in) : -1;
+        const bool fresh = only < 0 || only != staged;
+        const int per_vector = (int)c.chunks * kChunk * 4;
+        int j = fresh ? 0 : n, i = tid;
+        float4 x[kStageLoads][2];
+        int where[kStageLoads];  // vector and task within it, or -1
+        auto load = [&]() {
+#pragma unroll
+            for (int u = 0; u < kStageLoads; ++u) {
+                while (i >= per_vector) i -= per_vector, ++j;
+                x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                where[u] = -1;
+                if (j < n) {
+                    const int slot = tab.list[at + j], b = i >> 2, t = i & 3;
+                    where[u] = j << 16 | i;
+                    if (b < c.blocks) {
+                        const int row = GateUp ? (int)((unsigned)slot / (unsigned)p.per_in) : slot;
+                        const float* from = p.in + (long long)row * (p.blocks * 32) + (c.block0 + b) * 32 + t * 4;
+                        x[u][0] = __ldcg(reinterpret_cast<const float4*>(from));
+                        x[u][1] = __ldcg(reinterpret_cast<const float4*>(from + 16));
+                    }
+                }
+                i += kThreads;
+            }
+        };
+        load();
+        if (v == v_lo) {
+            if (!GateUp) {
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    if (tid * PER + q < p.slots) tab.exponent[tid * PER + q] = (int8_t)vector_exponent(max_bits[q]);
+                __syncthreads();
+            }
+        }
         float* const back = tab.back[v & 1];
         if (tid < n) {
             const int k = tab.exponent[tab.list[at + tid]];
             back[tid] = k == kNotFinite ? qnan() : pow2i(-k);
         }
-        const int only = GateUp && n == 1 ? (int)((unsigned)tab.list[at] / (unsigned)p.per_in) : -1;
-        if (only < 0 || only != staged) {
-            // Four lanes take a block of a vector; a thread's loads of two blocks are in flight together.
-            const int per_vector = (int)c.chunks * kChunk * 4;
-            int j = 0, i = tid;
 #pragma unroll 1
-            for (bool more = true; more;) {
-                float4 x[kStageLoads][2];
-                uint32_t to[kStageLoads];
-                float scale[kStageLoads];
-                int loads = 0;
+        while (where[0] >= 0) {
 #pragma unroll
-                for (int u = 0; u < kStageLoads; ++u) {
-                    while (i >= per_vector) i -= per_vector, ++j;
-                    x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (j < n) {
-                        const int slot = tab.list[at + j], b = i >> 2, t = i & 3;
-                        scale[u] = pow2i(tab.exponent[slot]);
-                        to[u] = frags + b * per_block + j * 64 + t * 16;
-                        if (b < c.blocks) {
-                            const int row = GateUp ? (int)((unsigned)slot / (unsigned)p.per_in) : slot;
-                            const float* from = p.in + (long long)row * (p.blocks * 32) + (c.block0 + b) * 32 + t * 4;
-                            x[u][0] = __ldcg(reinterpret_cast<const float4*>(from));
-                            x[u][1] = __ldcg(reinterpret_cast<const float4*>(from + 16));
-                        }
-                        ++loads;
-                    }
-                    i += kThreads;
+            for (int u = 0; u < kStageLoads; ++u) {
+                if (where[u] < 0) break;
+                const int vector = where[u] >> 16, task = where[u] & 0xffff;
+                const float scale = pow2i(tab.exponent[tab.list[at + vector]]);
+                const float pair[4][2] = {{x[u][0].x, x[u][0].z}, {x[u][1].x, x[u][1].z}, {x[u][0].y, x[u][0].w}, {x[u][1].y, x[u][1].w}};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float a = pair[q][0] * scale, b = pair[q][1] * scale;
+                    const __half2 h = __floats2half2_rn(a, b);
+                    const float2 f2 = __half22float2(h);
+                    hi[q] = bits_of(h);
+                    lo[q] = bits_of(__floats2half2_rn(a - f2.x, b - f2.y));
                 }
-                more = loads == kStageLoads;
-#pragma unroll
-                for (int u = 0; u < kStageLoads; ++u) {
-                    if (u >= loads) break;
-                    const float pair[4][2] = {{x[u][0].x, x[u][0].z}, {x[u][1].x, x[u][1].z}, {x[u][0].y, x[u][0].w}, {x[u][1].y, x[u][1].w}};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float a = pair[q][0] * scale[u], b = pair[q][1] * scale[u];
-                        const __half2 h = __floats2half2_rn(a, b);
-                        const float2 f2 = __half22float2(h);
-                        hi[q] = bits_of(h);
-                        lo[q] = bits_of(__floats2half2_rn(a - f2.x, b - f2.y));
-                    }
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u]), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                const uint32_t to = frags + (task >> 2) * per_block + vector * 64 + (task & 3) * 16;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                             : "memory");
+                if (Parts == 2)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + np * 64), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
+                                 "r"(lo[3])
                                  : "memory");
-                    if (Parts == 2)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to[u] + np * 64), "r"(lo[0]), "r"(lo[1]),
-                                     "r"(lo[2]), "r"(lo[3])
-                                     : "memory");
-                }
             }
-            staged = only;
+            load();
         }
+        staged = only;
         __syncthreads();
 
         // ---- products
