@@ -571,18 +571,20 @@ def kv4_attention(out, q, cache: KV4Cache, block_table, seq_lens, scale: float |
 
 # ---- around and inside a mixture-of-experts block ----
 
-def _mat(t: torch.Tensor, T: int, K: int, dtype: torch.dtype, dev: int, name: str):
-    """(address, elements from one token to the next) of token rows [T, K] on device `dev`."""
+def _mat(t: torch.Tensor, shape, dtype: torch.dtype, dev: int, name: str):
+    """(address, elements from one token to the next) of token rows of `shape` [T, K] on device `dev`."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on device {dev}, got {t.device}")
-    if t.shape != (T, K):
-        raise ValueError(f"{name}: expected [{T}, {K}], got {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     step, one = t.stride()
-    if one != 1 and K > 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: a token's row must be contiguous")
-    return t.data_ptr(), step if T > 1 else K
+    return t.data_ptr(), step if shape[0] > 1 else shape[1]
 
 
 def _on_stream(dev: int, stream, make):
@@ -601,21 +603,21 @@ def residual_norm(h_out, y_out, x, residual=None, post_gamma=None, gate=None, pr
     code, dev = _act(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [T, K]")
-    (T, K), dt = x.shape, x.dtype
-    xp, xs = _mat(x, T, K, dt, dev, "x")
-    hp, hs = _mat(h_out, T, K, dt, dev, "h_out")
-    yp, ys = (None, 0) if y_out is None else _mat(y_out, T, K, dt, dev, "y_out")
-    rp, rs = (None, 0) if residual is None else _mat(residual, T, K, dt, dev, "residual")
+    shape, dt = x.shape, x.dtype
+    T, K = shape
+    xp, xs = _mat(x, shape, dt, dev, "x")
+    hp, hs = _mat(h_out, shape, dt, dev, "h_out")
+    yp, ys = (None, 0) if y_out is None else _mat(y_out, shape, dt, dev, "y_out")
+    rp, rs = (None, 0) if residual is None else _mat(residual, shape, dt, dev, "residual")
     gp, gs, width = None, 0, K
     if gate is not None:
         if gate.shape == (K,):
             gp = _flat(gate, dt, dev, "gate", K)
         elif gate.dim() == 2 and gate.shape[1] == 1 and K > 1:
             width = 1
-            gp, gs = _mat(gate, T, 1, dt, dev, "gate")
-            gs = gs if T > 1 else 1
+            gp, gs = _mat(gate, (T, 1), dt, dev, "gate")
         else:
-            gp, gs = _mat(gate, T, K, dt, dev, "gate")
+            gp, gs = _mat(gate, shape, dt, dev, "gate")
     _call(load().residual_norm, dev, hp, yp, xp, rp,
           None if post_gamma is None else _flat(post_gamma, torch.float32, dev, "post_gamma", K), gp,
           None if pre_gamma is None else _flat(pre_gamma, torch.float32, dev, "pre_gamma", K), eps, residual_scale, branch_scale,
@@ -646,8 +648,8 @@ def moe_q4_down_gemv(out, qs, d, h, expert_ids, expert_weights, residual=None, d
         raise ValueError("out must be [T, N], d [E, N, K/32] and h [T, topk, K]")
     T, topk, K = h.shape
     E, N, _ = d.shape
-    op, os_ = _mat(out, T, N, dt, dev, "out")
-    rp, rs = (None, 0) if residual is None else _mat(residual, T, N, dt, dev, "residual")
+    op, os_ = _mat(out, (T, N), dt, dev, "out")
+    rp, rs = (None, 0) if residual is None else _mat(residual, (T, N), dt, dev, "residual")
     if workspace is None:
         workspace = _on_stream(dev, stream, lambda: moe_q4_down_workspace(out, h))
     size = workspace.numel()
@@ -714,11 +716,12 @@ def moe_q4_layer(out, x, moe: MoEWeights, topk: int, gamma=None, eps: float = 1e
     if x.dim() != 2:
         raise ValueError("x must be [T, K]")
     T, K, dt = x.shape[0], moe.K, x.dtype
+    shape = (T, K)
     if dev != moe.device.index:
         raise ValueError(f"x: expected a tensor on {moe.device}, got {x.device}")
-    xp, xs = _mat(x, T, K, dt, dev, "x")
-    op, os_ = _mat(out, T, K, dt, dev, "out")
-    rp, rs = (None, 0) if residual is None else _mat(residual, T, K, dt, dev, "residual")
+    xp, xs = _mat(x, shape, dt, dev, "x")
+    op, os_ = _mat(out, shape, dt, dev, "out")
+    rp, rs = (None, 0) if residual is None else _mat(residual, shape, dt, dev, "residual")
     if workspace is None:
         workspace = _on_stream(dev, stream, lambda: moe_q4_layer_workspace(moe, x, topk))
     size = workspace.numel()
