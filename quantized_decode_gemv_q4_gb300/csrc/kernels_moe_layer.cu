@@ -128,9 +128,10 @@ __device__ __forceinline__ int vector_exponent(unsigned m) {
     return m == 0u ? 0 : m >= 0x7f800000u ? kNotFinite : min(141 - (int)(m >> 23), 126);
 }
 
-// PER: slots of a thread. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
+// PER: slots of a thread. Scales: bytes of a row's scales that one copy may move, 16 or 8 (rows of whole chunks then), or 0: see
+// scale_bytes. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
 // that finishes a unit): a call runs each instruction few times, and fetching them costs as much as running them.
-template <bool GateUp, int Parts, int W, int PER>
+template <bool GateUp, int Parts, int W, int PER, int Scales>
 __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const ExpertParams p) {
     constexpr int kThreads = W * 32;
     constexpr int kNarrow = Parts == 2 ? 4 : 8;    // slots in one instruction's columns
@@ -332,14 +333,14 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     };
     auto fill = [&]() {
         if (f_left != 0) {
-            if (p.scale_bytes >= 8 && (GateUp || rows_left >= 32)) {  // 8, 16: rows of whole chunks
+            if (Scales >= 8 && (GateUp || rows_left >= 32)) {
                 const uint32_t to = to_codes + fill_at, to_d = to_scales + group_fill;
                 copy_async<16>(to, src0, 16u);
                 copy_async<16>(to + 512, src0 + 8 * row_bytes, 16u);
                 copy_async<16>(to + 1024, src1, 16u);
                 copy_async<16>(to + 1536, src1 + 8 * row_bytes, 16u);
                 if (group) {
-                    if (p.scale_bytes == 16) {
+                    if (Scales == 16) {
                         copy_async<16>(to_d, src_d, 16u);
                     } else {
                         const bool more = (f_chunk | 1) < f_chunks;
@@ -350,7 +351,6 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
             } else {
                 fill_edge();
             }
-            fill_at = fill_at + kStageBytes == kRing ? 0u : fill_at + kStageBytes;
             if (group) group_fill = group_fill + kGroupBytes == kGroups ? 0u : group_fill + kGroupBytes;
             group = f_chunk & 1;
             if (++f_chunk == f_chunks) {  // on to the next unit
@@ -369,7 +369,10 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     auto start = [&]() {
         next_piece();
 #pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) fill();
+        for (int i = 0; i < kStages - 1; ++i) {
+        fill();
+        fill_at += kStageBytes;
+    }
     };
     start();
 
@@ -584,6 +587,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                         }
                     }
                 }
+                fill_at = use_at;  // the stage that the next copies go to
                 use_at = use_at + kStageBytes == kRing ? 0u : use_at + kStageBytes;
                 const bool last = chunk + 1 == (int)c.chunks;
                 if ((chunk & 1) || last || left == 1) {
@@ -651,10 +655,10 @@ ExpertPlan plan_experts(int blocks, bool cut, int vector_parts, int warps, int m
     return l;  // cap 0: one vector does not fit
 }
 
-template <bool GateUp, int Parts, int W, int PER>
+template <bool GateUp, int Parts, int W, int PER, int Scales>
 cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ctas, const DeviceInfo& di, bool overlap,
                               cudaStream_t s) {
-    auto kern = moe_expert_kernel<GateUp, Parts, W, PER>;
+    auto kern = moe_expert_kernel<GateUp, Parts, W, PER, Scales>;
     static std::once_flag once[64];
     cudaError_t e = cudaSuccess;
     std::call_once(once[di.device & 63],
@@ -679,9 +683,15 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
     const uintptr_t d = reinterpret_cast<uintptr_t>(p.d0) | reinterpret_cast<uintptr_t>(p.d1);
     p.scale_bytes = p.blocks % 8 == 0 && d % 16 == 0 ? 16 : p.blocks % 4 == 0 && d % 8 == 0 ? 8 : p.blocks % 2 == 0 && d % 4 == 0 ? 4 : 2;
-    if (two) return launch_experts_as<GateUp, Parts, 8, 1>(p, l, 2, di, overlap, s);
-    return eight ? launch_experts_as<GateUp, Parts, 8, 2>(p, l, 1, di, overlap, s)
-                 : launch_experts_as<GateUp, Parts, 16, 1>(p, l, 1, di, overlap, s);
+    if (eight) return launch_experts_as<GateUp, Parts, 8, 2, 0>(p, l, 1, di, overlap, s);
+    auto go = [&](auto scales) {
+        constexpr int S = decltype(scales)::value;
+        return two ? launch_experts_as<GateUp, Parts, 8, 1, S>(p, l, 2, di, overlap, s)
+                   : launch_experts_as<GateUp, Parts, 16, 1, S>(p, l, 1, di, overlap, s);
+    };
+    return p.scale_bytes == 16 ? go(std::integral_constant<int, 16>())
+           : p.scale_bytes == 8 ? go(std::integral_constant<int, 8>())
+                                : go(std::integral_constant<int, 0>());
 }
 
 template <bool GateUp>
