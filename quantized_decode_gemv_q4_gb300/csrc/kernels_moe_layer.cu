@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
     constexpr int kThreads = W * 32;
     constexpr int kNarrow = Parts == 2 ? 4 : 8;    // slots in one instruction's columns
     constexpr int kTiles = Parts == 2 ? 1 : 2;     // sums of 8 slots that a warp keeps
+    constexpr bool kRoom = W == 8 && PER == 1;     // of two CTAs an SM: see launch_experts_of
     extern __shared__ __align__(128) uint8_t smem[];
     Tables& tab = *reinterpret_cast<Tables*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         const int seg = (int)segment_of(v);
         const int n = __shfl_sync(0xffffffffu, (int)tab.seg_n[seg], 0), at = __shfl_sync(0xffffffffu, (int)tab.seg_at[seg], 0);
         const int np = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16;  // columns kept of each part
-        const uint32_t per_block = (uint32_t)np * (Parts * 64u);
+        // With room for them, the columns of narrow segments lie at the distance of a full set.
+        const uint32_t per_block = kRoom && np <= kNarrow ? 512u : (uint32_t)np * (Parts * 64u);
         const int only = GateUp && n == 1 ? (int)((unsigned)tab.list[at] / (unsigned)p.per_in) : -1;
         const bool fresh = only < 0 || only != staged;
         const int per_vector = (int)c.chunks * kChunk * 4;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
                              : "memory");
                 if (Parts == 2)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + np * 64), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (kRoom ? per_block / 2 : np * 64)), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
                                  "r"(lo[3])
                                  : "memory");
             }
@@ -525,14 +527,15 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
         };
         // A lane's column of a block: slot g of the first part, and of the second behind it; with up to 4 slots the second
         // part has columns 4 to 7, and with fewer the columns behind them repeat them.
-        const uint32_t column = frags + (Parts == 1 || np == 8 ? g & (np - 1) : (g >> 2) * np + (g & (np - 1))) * 64 + t4 * 16;
+        const uint32_t column = frags + (Parts == 1 || np == 8 ? g & (np - 1) : (g >> 2) * (kRoom ? 4 : np) + (g & (np - 1))) * 64 + t4 * 16;
         // A warp's chunks. What a chunk needs from shared memory is asked for before any of it is used (the second columns of
         // wide segments excepted, for which there are no registers).
         auto run = [&](auto wide) {
             constexpr bool Wide = decltype(wide)::value;  // 16 columns: two parts of 8 slots, or 16 slots
+            const uint32_t step = !kRoom ? per_block : Wide ? 1024u : 512u;
             int chunk = c.chunk, unit = c.unit;
             bool head = chunk != 0;  // the unit was begun by a warp before this one, which joins it
-            uint32_t vec = column + (uint32_t)chunk * (kChunk * per_block), sc = from_scales + group_use + ((chunk & 1) << 3);
+            uint32_t vec = column + (uint32_t)chunk * (kChunk * step), sc = from_scales + group_use + ((chunk & 1) << 3);
 #pragma unroll 1
             for (unsigned left = c.end - c.at; left != 0; --left) {
                 cp_async_wait<kStages - 2>();
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                 uint4 x[kChunk], y[kChunk];
 #pragma unroll
                 for (int b = 0; b < kChunk; ++b) {
-                    x[b] = lds128(vec + b * (Wide ? 1024u : per_block));
+                    x[b] = lds128(vec + b * (Wide ? 1024u : step));
                     if (Wide) y[b] = lds128(vec + b * 1024u + 512u);
                 }
 #pragma unroll
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const Expert
                     sc += 8;
                 }
                 ++chunk;
-                vec += kChunk * per_block;
+                vec += kChunk * step;
                 if (last) {
                     if (head) deposit();
                     else finish(unit);
