@@ -18,6 +18,26 @@ struct ResidualNormArgs {
 };
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, int dtype, cudaStream_t s);
 
+// The experts' products (moe_experts.cuh): gate and up with SwiGLU, or down. The callers fill what comes before `units`.
+struct ExpertParams {
+    const uint8_t *qs0, *qs1;  // gate and up, or down twice
+    const uint16_t *d0, *d1;
+    const float* in;
+    const unsigned* in_max;    // bits of the largest size in an input row
+    float* out;                // [parts][slots][rows]
+    unsigned* out_max;         // as in_max, of the outputs (gate and up)
+    const int32_t* ids;
+    int E, rows, blocks, slots, per_in;  // slot s reads input row s / per_in
+    int units, parts, part_blocks, cap, scale_bytes, table_bits;
+    uint32_t ring_at, deposits_at, frags_at;
+};
+// Parts that a down projection's input is cut into (their sums are added by the join), of at most so many blocks: 8 vectors'
+// parts fit beside the rings.
+constexpr int kPartBlocks = 88;
+inline int moe_parts(int blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
+cudaError_t launch_moe_gate_up(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s);
+cudaError_t launch_moe_down_products(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s);
+
 // Down projections of T * topk slots and their weighted sum per token: rows = outputs, cols = inputs of an expert's matrix.
 struct MoeDownArgs {
     void* out;

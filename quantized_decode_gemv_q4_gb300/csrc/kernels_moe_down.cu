@@ -1,0 +1,10 @@
+// Down projections of a mixture of experts: see moe_experts.cuh.
+#include "moe_experts.cuh"
+
+namespace q4 {
+
+cudaError_t launch_moe_down_products(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s) {
+    return launch_experts<false>(p, dtype, di, true, s);
+}
+
+}  // namespace q4
