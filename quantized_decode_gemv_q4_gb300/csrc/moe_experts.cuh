@@ -102,11 +102,11 @@ __device__ __forceinline__ int vector_exponent(unsigned m) {
 // scale_bytes. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
 // that finishes a unit): a call runs each instruction few times, and fetching them costs as much as running them.
 template <bool GateUp, int Parts, int W, int PER, int Scales>
-__global__ void __launch_bounds__(W * 32, 16 / W) moe_expert_kernel(const ExpertParams p) {
+__global__ void __launch_bounds__(W * 32, W == 6 ? 2 : 1) moe_expert_kernel(const ExpertParams p) {
     constexpr int kThreads = W * 32;
     constexpr int kNarrow = Parts == 2 ? 4 : 8;    // slots in one instruction's columns
     constexpr int kTiles = Parts == 2 ? 1 : 2;     // sums of 8 slots that a warp keeps
-    constexpr bool kRoom = W == 8 && PER == 1;     // of two CTAs an SM: see launch_experts_of
+    constexpr bool kRoom = W == 6 && PER == 1;     // of two CTAs an SM: see launch_experts_of
     extern __shared__ __align__(128) uint8_t smem[];
     Tables& tab = *reinterpret_cast<Tables*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -642,9 +642,9 @@ cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ct
 template <bool GateUp, int Parts>
 cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
     const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
-    ExpertPlan l = plan_experts(p.blocks, !GateUp, Parts, 8, half);
-    const bool two = l.cap >= 8 / Parts && 2 * p.slots <= l.cap * p.E && p.slots <= 256;
-    if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 16, di.max_smem_optin);
+    ExpertPlan l = plan_experts(p.blocks, !GateUp, Parts, 6, half);
+    const bool two = l.cap >= 8 / Parts && 2 * p.slots <= l.cap * p.E && p.slots <= 192;
+    if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 12, di.max_smem_optin);
     const bool eight = l.cap == 0;  // the longest vectors leave room for 8 warps
     if (eight) l = plan_experts(p.blocks, !GateUp, Parts, 8, di.max_smem_optin);
     if (l.cap == 0) return cudaErrorNotSupported;
@@ -658,8 +658,8 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     if (eight) return launch_experts_as<GateUp, Parts, 8, 2, 0>(p, l, 1, di, overlap, s);
     auto go = [&](auto scales) {
         constexpr int S = decltype(scales)::value;
-        return two ? launch_experts_as<GateUp, Parts, 8, 1, S>(p, l, 2, di, overlap, s)
-                   : launch_experts_as<GateUp, Parts, 16, 1, S>(p, l, 1, di, overlap, s);
+        return two ? launch_experts_as<GateUp, Parts, 6, 1, S>(p, l, 2, di, overlap, s)
+                   : launch_experts_as<GateUp, Parts, 12, 2, S>(p, l, 1, di, overlap, s);
     };
     return p.scale_bytes == 16 ? go(std::integral_constant<int, 16>())
            : p.scale_bytes == 8 ? go(std::integral_constant<int, 8>())
