@@ -33,7 +33,7 @@ constexpr uint32_t kSlotBytes = kStageBytes + kGroupBytes;
 constexpr int kMaxSlots = 512;
 constexpr int kStageLoads = 2;
 constexpr int kMaxCap = 16;
-constexpr unsigned kNarrowCost = 4, kWideCost = 5;  // of a unit of a segment whose columns fill one instruction, or two
+constexpr unsigned kNarrowCost = 2, kWideCost = 3;  // of a unit of a segment whose columns fill one instruction, or two
 
 struct Tables {
     int seg_e[kMaxSlots];
