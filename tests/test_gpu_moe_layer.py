@@ -134,6 +134,35 @@ def test_down_values_far_apart():
     check_down(a, out)
 
 
+def test_down_weights_past_32_bits():
+    """Experts whose codes lie more than 2^32 bytes from the first's, among memory that is never read."""
+    E, N, K, T = 1200, 1024, 8192, 3
+    qs = torch.empty(E, N, K // 32, 16, dtype=torch.uint8, device="cuda")
+    d = torch.empty(E, N, K // 32, dtype=torch.float16, device="cuda")
+    assert qs.numel() > 1 << 32
+    r = Rand(4)
+    ids = torch.tensor([[0, E - 1], [E - 2, E - 1], [E // 2, 1]], dtype=torch.int32)
+    for e in sorted(set(ids.flatten().tolist())):
+        qs[e], d[e] = r.weights(N, K)
+    a = dict(qs=qs, d=d, h=r.normal(T, 2, K), expert_ids=ids.cuda(), expert_weights=torch.rand(T, 2, device="cuda"), residual=None)
+    out = torch.empty(T, N, device="cuda")
+    q4.moe_q4_down_gemv(out, **a)
+    check_down(a, out)
+
+
+def test_down_scales_at_any_alignment():
+    """Scales 2, 4 and 8 bytes past a 16-byte boundary: other copies, the same bits."""
+    a = down_case(5, 3, 7, 96, 1024, torch.float32)
+    out, again = torch.empty(5, 96, device="cuda"), torch.empty(5, 96, device="cuda")
+    q4.moe_q4_down_gemv(out, **a)
+    check_down(a, out)
+    for shift in (1, 2, 4):
+        d = torch.empty(a["d"].numel() + 8, dtype=torch.float16, device="cuda")[shift:shift + a["d"].numel()].view(a["d"].shape)
+        d.copy_(a["d"])
+        q4.moe_q4_down_gemv(again, **dict(a, d=d))
+        assert torch.equal(out, again), shift
+
+
 # ------------------------------------------------------------------------------------------------
 
 def layer_case(T, topk, E, N, K, dt, norm=True, seed=0):
@@ -173,7 +202,7 @@ def check_layer(a, out, ids, w, normalize=True, keep=None):
 
 LAYER = [(1, 1, 1, 32, 32), (1, 8, 64, 96, 256), (5, 3, 10, 1056, 672), (8, 8, 64, 320, 512), (64, 8, 16, 64, 2048),
          (31, 2, 4, 32, 4128), (512, 1, 3, 32, 64), (2, 2, 200, 32, 64), (1, 2, 2, 32, 32768), (1, 1, 1, 65536, 32),
-         (6, 4, 4, 288, 8224), (40, 1, 2, 160, 96)]
+         (6, 4, 4, 288, 8224), (40, 1, 2, 160, 96), (64, 8, 64, 32, 256), (19, 8, 128, 64, 224)]
 
 
 @pytest.mark.parametrize("T,topk,E,N,K", LAYER)
@@ -184,6 +213,40 @@ def test_layer_against_64_bits(T, topk, E, N, K, dt, norm):
     out, ids, w = run_layer(a, normalize=norm)
     check_layer(a, out, ids, w, norm)
     assert torch.equal(run_layer(a, normalize=norm)[0], out)
+
+
+def test_layer_of_the_longest_vectors_and_most_slots():
+    a = layer_case(128, 4, 5, 32, 24576, torch.float32)
+    a["residual"] = None
+    out, ids, w = run_layer(a)
+    keep = list(range(0, 128, 9))
+    check_layer(a, out, ids, w, keep=keep)
+
+
+def test_two_graphs_and_streams_at_the_same_time():
+    """Calls that run at the same time, each with its workspace."""
+    cases = [layer_case(T, 4, 16, 256, 512, dt, seed=T) for T, dt in ((3, torch.bfloat16), (30, torch.float32))]
+    outs, want, graphs, streams = [], [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for a, side in zip(cases, streams):
+        ws = q4.moe_q4_layer_workspace(a["moe"], a["x"], 4)
+        out = torch.empty_like(a["x"])
+        call = lambda: q4.moe_q4_layer(out, a["x"], a["moe"], 4, gamma=a["gamma"], residual=a["residual"], workspace=ws)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            for _ in range(20):
+                call()
+        outs.append(out.zero_())
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, side in zip(graphs, streams):
+            with torch.cuda.stream(side):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
 def test_layer_in_place_strides_and_workspace():
