@@ -344,7 +344,7 @@ typedef struct {
  *   expert_ids int32[T][topk], expert_weights float[T][topk]: the picks, each written when not NULL.
  *   1 <= topk <= E <= 4096; T*topk <= 512; N % 32 == 0, N <= 65536; K % 32 == 0, K <= 32768; E*N, E*K < 2^31.
  *   A token whose x, logits or h hold a NaN or an infinity gets a NaN row (its ids are valid all the same); no other token
- *   is touched. workspace: as above, of the bytes that moe_q4_layer_workspace states; x and h are held as h is in
+ *   is touched. With gamma the sum of squares is fp32, with residual_norm's range. workspace: as above, of the bytes that moe_q4_layer_workspace states; x and h are held as h is in
  *   moe_q4_down_gemv.
  */
 int moe_q4_layer_workspace(size_t *bytes, int T, int topk, int E, int N, int K);
