@@ -75,6 +75,27 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
     const uint32_t xs = s_base + p.xs_off;
     const uint32_t aux = s_base + p.aux_off;
     float* lg = reinterpret_cast<float*>(smem + p.lg_off);
+    // behind the first picks' weights, where the staged input was
+    uint32_t* const keys = reinterpret_cast<uint32_t*>(smem + p.xs_off + 2048u);
+    int* const ranks = reinterpret_cast<int*>(keys + 64);
+
+    // Loads of two rows' two units, issued before any is used.
+    auto load_units = [&](int ea, int eb, int u0, uint4 (&w)[4], uint32_t (&db)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = (j & 2) ? eb : ea;
+            const int u = (j & 1) ? u0 + 32 : u0;
+            const bool in = e < p.E && u < p.nblk;
+            const size_t blk = (size_t)e * p.nblk + u;
+            w[j] = in ? __ldg(reinterpret_cast<const uint4*>(p.qs) + blk) : make_uint4(0u, 0u, 0u, 0u);
+            db[j] = in ? (uint32_t)__ldg(p.d + blk) : 0u;
+        }
+    };
+    // The layer form for few tokens reads a warp's first rows while the previous kernel ends.
+    constexpr bool kEarly = Layer && CS == 8;
+    uint4 first_w[4];
+    uint32_t first_db[4];
+    if (kEarly) load_units(c + CS * warp, c + CS * warp + CS * W, lane, first_w, first_db);
 
     // x belongs to the previous kernel in the stream when launches overlap.
     grid_dependency_wait();
@@ -88,9 +109,27 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
         const X* const row = Layer ? static_cast<const X*>(p.layer.x) + (long long)t * p.layer.x_stride : nullptr;
         float r = 1.f;
         unsigned largest = 0u;
+        constexpr int kKept = 2;  // rounds of elements that stay in registers between the norm and the staging
+        float kept[kKept][8], gammas[kKept][8];
+        if (Layer) {
+#pragma unroll
+            for (int q = 0; q < kKept; ++q) {
+                const int i = threadIdx.x + q * W * 32;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) kept[q][j] = 0.f;
+                if (i < p.nblk * 4) {
+                    load_floats(row + i * 8, kept[q]);
+                    if (p.layer.gamma) load_floats(p.layer.gamma + i * 8, gammas[q]);
+                }
+            }
+        }
         if (Layer && p.layer.gamma) {
             float sum = 0.f;
-            for (int i = threadIdx.x; i < p.nblk * 4; i += W * 32) {
+#pragma unroll
+            for (int q = 0; q < kKept; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(kept[q][j], kept[q][j], sum);
+            for (int i = threadIdx.x + kKept * W * 32; i < p.nblk * 4; i += W * 32) {
                 float v[8];
                 load_floats(row + i * 8, v);
 #pragma unroll
@@ -115,11 +154,16 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
                 b = in ? __ldg(src + 1) : b;
             } else if (in) {
                 const int k = thr * 8;
-                float v[8];
-                load_floats(row + k, v);
+                const int round = thr / (W * 32);
+                float v[8], gm[8];
+                if (round < kKept) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = round ? kept[1][j] : kept[0][j], gm[j] = round ? gammas[1][j] : gammas[0][j];
+                } else {
+                    load_floats(row + k, v);
+                    if (p.layer.gamma) load_floats(p.layer.gamma + k, gm);
+                }
                 if (p.layer.gamma) {
-                    float gm[8];
-                    load_floats(p.layer.gamma + k, gm);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = v[j] * r * gm[j];
                 }
@@ -183,14 +227,11 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
             const bool h1 = u1 < p.nblk;
             uint4 w[4];
             uint32_t db[4];
+            if (kEarly && e0 == c + CS * warp && u0 == lane) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int e = (j & 2) ? eb : ea;
-                const int u = (j & 1) ? u1 : u0;
-                const bool in = ((j & 2) ? hb : true) && ((j & 1) ? h1 : true);
-                const size_t blk = (size_t)e * p.nblk + u;
-                w[j] = in ? __ldg(reinterpret_cast<const uint4*>(p.qs) + blk) : make_uint4(0u, 0u, 0u, 0u);
-                db[j] = in ? (uint32_t)__ldg(p.d + blk) : 0u;
+                for (int j = 0; j < 4; ++j) w[j] = first_w[j], db[j] = first_db[j];
+            } else {
+                load_units(ea, eb, u0, w, db);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -235,6 +276,30 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
     cluster_sync();
     if (c != 0) return;
     __syncthreads();
+    // Up to 64 experts: each expert's rank is the number of larger keys (all keys differ), counted by the whole CTA: thread
+    // (e, q) compares expert e with the q-th share of the others. A key is the logit's order-preserving bits (-0 ranks with +0,
+    // a NaN below every other value); equal logits go to the lower index.
+    if (p.E <= 64) {
+        constexpr int kShare = 64 * 64 / (W * 32);
+        const int e = threadIdx.x & 63, q = threadIdx.x >> 6;
+        auto bits_of = [&](int i) {
+            const float v = lg[i];
+            const uint32_t u = v == 0.0f ? 0u : __float_as_uint(v);
+            return v != v ? 1u : ((u & 0x80000000u) ? ~u : (u | 0x80000000u));
+        };
+        if (threadIdx.x < 64) keys[e] = e < p.E ? bits_of(e) : 0u, ranks[e] = 0;
+        __syncthreads();
+        const uint32_t mine = keys[e];
+        int larger = 0;
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
+            const int o = q * kShare + i;
+            const uint32_t other = keys[o];
+            larger += other > mine || (other == mine && o < e);
+        }
+        atomicAdd(ranks + e, larger);
+        __syncthreads();
+    }
 
     // softmax over all E logits and the top K (warp 0 of CTA 0)
     if (warp == 0) {
@@ -255,18 +320,10 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
             return ((unsigned long long)key << 32) | (0xFFFFFFFFu - (uint32_t)e);
         };
         if (p.E <= 64) {
-            // Up to 64 experts: lane l holds experts l and l + 32; each expert's rank is the number of larger keys
-            // (all keys differ), and the experts of rank < K are the picks in order. The K weights are summed in
+            // Lane l holds experts l and l + 32; the experts of rank < K are the picks in order. The K weights are summed in
             // pick order, as the passes below do.
             const bool h0 = lane < p.E, h1 = lane + 32 < p.E;
-            const unsigned long long k0 = h0 ? key_of(lane) : 0ull, k1 = h1 ? key_of(lane + 32) : 0ull;
-            int r0 = 0, r1 = 0;
-#pragma unroll 8
-            for (int sl = 0; sl < 32; ++sl) {
-                const unsigned long long a = __shfl_sync(0xffffffffu, k0, sl), b = __shfl_sync(0xffffffffu, k1, sl);
-                r0 += (int)(a > k0) + (int)(b > k0);
-                r1 += (int)(a > k1) + (int)(b > k1);
-            }
+            const int r0 = ranks[lane], r1 = ranks[lane + 32];
             float* const pk = reinterpret_cast<float*>(smem + p.xs_off);  // the staged input is no longer needed
             const float pw0 = h0 ? expf(lg[lane] - mx) / z : 0.f;
             const float pw1 = h1 ? expf(lg[lane + 32] - mx) / z : 0.f;
@@ -356,7 +413,7 @@ static cudaError_t launch_router(int32_t* ids, float* weights, float* logits, co
     p.aux_off = xsb;
     p.lg_off = xsb + axb;
     const uint32_t smem = p.lg_off + (uint32_t)E * 4u;
-    auto launch = [&](auto kern, std::once_flag* attr_once) {
+    auto launch = [&](auto kern, int cs, std::once_flag* attr_once) {
         cudaFuncAttributes fa;
         cudaError_t e = cudaSuccess;
         std::call_once(attr_once[di.device & 63], [&] {
@@ -366,15 +423,15 @@ static cudaError_t launch_router(int32_t* ids, float* weights, float* logits, co
                                          di.max_smem_optin - (int)fa.sharedSizeBytes);
         });
         if (e != cudaSuccess) return e;
-        // one cluster of CS CTAs per token (CS = 8 is the portable cluster size)
+        // one cluster of CTAs per token (8 is the portable cluster size)
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(T * CS));
+        cfg.gridDim = dim3((unsigned)(T * cs));
         cfg.blockDim = dim3((unsigned)(W * 32));
         cfg.dynamicSmemBytes = smem;
         cfg.stream = s;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = CS;
+        attr[0].val.clusterDim.x = (unsigned)cs;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -387,11 +444,14 @@ static cudaError_t launch_router(int32_t* ids, float* weights, float* logits, co
     if (smem + (layer ? kPartBytes : 0u) > (uint32_t)di.max_smem_optin) return cudaErrorNotSupported;
     if (!layer) {
         static std::once_flag once[64];
-        return launch(moe_router_kernel<W, CS, void>, once);
+        return launch(moe_router_kernel<W, CS, void>, CS, once);
     }
     return with_dtype(dtype, [&](auto tag) {
-        static std::once_flag once[64];
-        return launch(moe_router_kernel<W, CS, decltype(tag)>, once);
+        using X = decltype(tag);
+        static std::once_flag once[64], once_many[64];
+        // 64 tokens as clusters of 8 come in two waves: 11.8 us, as clusters of 2 XX us
+        return T * CS <= 2 * di.sm_count ? launch(moe_router_kernel<W, CS, X>, CS, once)
+                                         : launch(moe_router_kernel<W, 2, X>, 2, once_many);
     });
 }
 
