@@ -281,7 +281,8 @@ int kv4_attention(void *out, float *lse, const void *q, const kv4_cache *cache, 
 /*
  * ---- Around and inside a mixture-of-experts block ----
  * (No counterpart in the source pages.) Activations as in the section above: Q4_F32, Q4_F16 or Q4_BF16, rows of a token
- * `stride` elements apart and 16-byte aligned, fp32 sums, one rounding when a value is stored.
+ * `stride` elements apart and 16-byte aligned, fp32 sums, one rounding when a value is stored (but see moe_q4_down_gemv for
+ * the vectors of bf16 layers).
  *
  * residual_norm: the norm behind a block, its gate and scales, the residual sum and the norm before the next block.
  *   b = x (post_gamma NULL) or x_i * post_gamma_i / sqrt(sum_j x_j^2 / K + eps);
@@ -406,7 +407,9 @@ const char *q4_last_error(void);
  * the visibility of its writes) before they read x, gamma or expert ids or write any output; the MoE kernel
  * waits before it reads the expert ids. The norm/rotation, cache and attention calls launch the same way and wait before
  * they read anything, so their caches and page tables may come from the call before. So a chain of calls where each x is the previous output stays
- * exact, and each call's weight streaming overlaps the previous call's tail.
+ * exact, and each call's weight streaming overlaps the previous call's tail. residual_norm, moe_q4_down_gemv and moe_q4_layer
+ * likewise (the layer may read router weights before the wait); the kernels within one of their calls overlap each other in any
+ * case.
  * Requirement while it is on: the kernel that runs directly before a call in the same stream must not
  * write that call's weight bytes (qs, d or the Q4_K blocks); weights written earlier in the stream, or on
  * another stream with ordinary event or stream synchronisation, are fine.

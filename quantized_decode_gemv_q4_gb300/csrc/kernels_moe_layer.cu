@@ -4,6 +4,11 @@
 //   xn = x, or x * r * gamma;  logits = Wr xn, top-k and softmax weights (the router's kernel);
 //   h[t, s] = silu(Wg xn) * (Wu xn) and z[t, s] = Wd h[t, s] of expert e(t, s);
 //   out[t] = residual[t] + sum over s of weight[t, s] * z[t, s].
+//
+// Four kernels for a layer: the router (kernels_router.cu), gate and up, down (moe_experts.cuh) and the join here; three for the
+// down projections alone, whose first takes the largest size of each slot's vector, which gate and up leaves by itself. Each may
+// start while the one before it ends (programmatic dependent launch within the call, whatever the overlap setting says about
+// the call's first kernel) and waits for it before it touches what it wrote. h, z, the picks and xn stay in the workspace.
 #include "block.h"
 #include "kv_common.cuh"
 

@@ -1,19 +1,33 @@
 // The experts' products of a mixture of experts over planar Q4: gate and up with SwiGLU, and down.
 //
-// One kernel for gate and up (with SwiGLU) and for down. Slots that go to the same expert form a segment of up to `cap`
-// (8, of one part 16, or fewer where the vectors are long); long inputs of the down projection are cut into parts whose sums the join adds. A
-// segment's rows are units of 32: 16 of gate and the same 16 of up, or 32 of down. All units lie on one line that is cut
-// into equal pieces, one for each CTA (one CTA an SM), and a piece's chunks of 4 blocks (128 columns) are cut into equal
-// pieces for its warps. So every weight is read once a segment, and a warp adds a unit's chunks in registers; a unit cut
-// between warps is joined through shared memory in the order of its chunks, so that the same call gives the same bits.
+// Work. Slots that go to the same expert form a segment of up to `cap` (8, of vectors in one part 16, or fewer where the
+// vectors are long); long inputs of the down projection are cut into parts whose sums the join adds. A segment's rows are
+// units of 32: 16 of gate and the same 16 of up, or 32 of down. All units lie on one line, weighted by what they cost and cut
+// into pieces, one for each CTA, and a piece's chunks of 4 blocks (128 columns) are cut into equal pieces for its warps. So
+// every weight is read once a segment, and a warp adds a unit's chunks in registers; a unit cut between warps is joined through
+// shared memory in the order of its chunks, so that the same call gives the same bits.
 //
 // Products run on m16n8k16 matrix instructions with the weights as rows: ldmatrix brings a block's word to each lane, eight
 // codes become eight exact f16 values code - 8 with nine instructions, and a block's fp32 sums are multiplied by the block's
 // scale in fp32. The columns are the segment's vectors in f16, scaled by a power of two that puts a vector's largest element
 // near 2^14. fp32 and f16 layers hold a vector in two parts (x = hi + lo to 2^-22): with up to 4 slots both parts share an
 // instruction's 8 columns, with more each part has its own and both add into the same sums. bf16 layers hold one part: 11
-// bits, an error of 2^-11 at most where the layer's own output is rounded by 2^-8, and twice the slots in an instruction. The
-// parts lie in shared memory in the order in which lanes take them.
+// bits, an error of 2^-11 at most where the layer's own output is rounded by 2^-8, and twice the slots in an instruction (64
+// tokens over 64 experts of 1408 x 2048: 147 us with two parts, 127 us with one). The parts lie in shared memory in the order
+// in which lanes take them. tcgen05 is not used: its operands would have to be decoded into f16 tiles in shared memory first,
+// which costs the instructions that bind here and the writes besides, and at these few columns the matrix unit is a sixth busy.
+//
+// Copies. Each warp streams its chunks by cp.async through a ring of three stages of its own, across units and segments
+// (16-byte chunks XOR-swizzled so that ldmatrix is free of bank conflicts); the scales of two chunks travel together. Four
+// stages: 8 tokens 61.6 us instead of 59.8.
+//
+// What bounds it (8 tokens, 42 experts, 137 MB of gate and up in 35 us, 25 us of them at 5.4 TB/s): between the starts and the
+// ends, instructions. A chunk costs a warp about 360, of which 220 are the products themselves (144 decode, 16 matrix, 48 scale),
+// where the copy rate would leave a scheduler about 400 issue slots. So loops are kept straight and branches uniform (69 -> 62
+// us), and there are fewer warps than would fit, with more registers each: 6 and 6 in two CTAs an SM, or 12 in one (16: 8 tokens
+// 60.5 us, a down projection of 14336 columns 60.5 instead of 57.4 us; 10 or 14: slower). Some 6 us go by from the kernel's
+// inputs to the first products (ids, segments, the first copies and vectors) and about 4 us at its end, where CTAs that share
+// an SM finish at different times; down hides most of its start behind the kernel before it.
 #pragma once
 
 #include <mutex>
@@ -31,7 +45,7 @@ constexpr uint32_t kStageBytes = 2048;           // a stage: 32 rows x 64 bytes 
 constexpr uint32_t kGroupBytes = 512;            // 32 rows x 8 scales: those of two chunks, in a ring of their own
 constexpr uint32_t kSlotBytes = kStageBytes + kGroupBytes;
 constexpr int kMaxSlots = 512;
-constexpr int kStageLoads = 2;
+constexpr int kStageLoads = 2;                   // of a thread that are in flight together; with 4, 8 tokens take 64 us, not 62
 constexpr int kMaxCap = 16;
 
 struct Tables {
@@ -641,6 +655,8 @@ cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ct
     return launch_grid(kern, dim3((unsigned)(di.sm_count * ctas)), dim3(W * 32), l.smem, s, overlap, p);
 }
 
+// Two CTAs of 6 warps an SM where the experts get few slots each (a CTA's start, its vectors and its end overlap with the other
+// one's products: 8 tokens over 64 experts 61.5 us with 8 + 8 warps, 64.2 us with 16 in one CTA) and the vectors fit beside two rings; else one of 12.
 template <bool GateUp, int Parts>
 cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
     const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
