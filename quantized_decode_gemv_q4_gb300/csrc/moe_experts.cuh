@@ -97,12 +97,12 @@ __device__ __forceinline__ __half2 masked_or(uint32_t w, uint32_t or_) {
 // (4t + 1, 4t + 3), (4t + 17, 4t + 19). 1024 + q and 1024 + 16 q are exact in f16, and so are q - 8 and (..) / 16 - 72.
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t k1024, uint32_t (&x)[4]) {
     const __half2 lo = __floats2half2_rn(-1032.f, -1032.f), hi = __floats2half2_rn(-72.f, -72.f),
-                  six = __floats2half2_rn(0.0625f, 0.0625f);
+                  sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
     x[0] = bits_of(__hadd2(masked_or<0x000f000fu>(w, k1024), lo));
-    x[1] = bits_of(__hfma2(masked_or<0x00f000f0u>(w, k1024), six, hi));
+    x[1] = bits_of(__hfma2(masked_or<0x00f000f0u>(w, k1024), sixteenth, hi));
     w >>= 8;
     x[2] = bits_of(__hadd2(masked_or<0x000f000fu>(w, k1024), lo));
-    x[3] = bits_of(__hfma2(masked_or<0x00f000f0u>(w, k1024), six, hi));
+    x[3] = bits_of(__hfma2(masked_or<0x00f000f0u>(w, k1024), sixteenth, hi));
 }
 
 // The power of two that takes a vector whose largest size has the bits `m` to at most 2^15, as its exponent.
@@ -112,8 +112,7 @@ __device__ __forceinline__ int vector_exponent(unsigned m) {
 }
 
 // PER: slots of a thread. Scales: bytes of a row's scales that one copy may move, 16 or 8 (rows of whole chunks then), or 0: see
-// scale_bytes. The code is kept short (one place that copies, one that multiplies for each kind of columns, one
-// that finishes a unit): a call runs each instruction few times, and fetching them costs as much as running them.
+// scale_bytes. What every warp works out for itself is kept short: at the start of a kernel it costs all warps issue slots.
 template <bool GateUp, int Parts, int W, int PER, int Scales>
 __global__ void __launch_bounds__(W * 32, W == 6 ? 2 : 1) moe_expert_kernel(const ExpertParams p) {
     constexpr int kThreads = W * 32;
@@ -130,8 +129,8 @@ __global__ void __launch_bounds__(W * 32, W == 6 ? 2 : 1) moe_expert_kernel(cons
     float* deposits = reinterpret_cast<float*>(smem + p.deposits_at);
 
     // Segments: the slots of an expert in their order, `cap` at a time, experts in the order of their first slots, those with
-    // more columns than one instruction's behind the others. A hash
-    // table of experts, each with the bits of its slots, lies where the ring and the vectors lie later.
+    // more columns than one instruction's behind the others. A hash table of experts, each with the bits of its slots, lies where
+    // the ring and the vectors lie later.
     const int words = (p.slots + 31) / 32, entries = 1 << p.table_bits;
     uint16_t* const list_base = reinterpret_cast<uint16_t*>(smem + p.ring_at);
     int* const keys = reinterpret_cast<int*>(list_base + kMaxSlots);
@@ -353,15 +352,12 @@ __global__ void __launch_bounds__(W * 32, W == 6 ? 2 : 1) moe_expert_kernel(cons
         }
         cp_async_commit();
     };
-    auto start = [&]() {
-        next_piece();
+    next_piece();
 #pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) {
+    for (int i = 0; i < kStages - 1; ++i) {
         fill();
         fill_at += kStageBytes;
     }
-    };
-    start();
 
     uint32_t k1024;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
