@@ -408,8 +408,8 @@ const char *q4_last_error(void);
  * waits before it reads the expert ids. The norm/rotation, cache and attention calls launch the same way and wait before
  * they read anything, so their caches and page tables may come from the call before. So a chain of calls where each x is the previous output stays
  * exact, and each call's weight streaming overlaps the previous call's tail. residual_norm, moe_q4_down_gemv and moe_q4_layer
- * likewise (the layer may read router weights before the wait); the kernels within one of their calls overlap each other in any
- * case.
+ * likewise (the layer may read router weights before the wait). Those three are launched so in any case, but with the setting
+ * off they touch nothing before the previous kernel has completed, so that it is free to write whatever they read.
  * Requirement while it is on: the kernel that runs directly before a call in the same stream must not
  * write that call's weight bytes (qs, d or the Q4_K blocks); weights written earlier in the stream, or on
  * another stream with ordinary event or stream synchronisation, are fine.

@@ -76,6 +76,7 @@ struct LayerInput {
     unsigned *x_max, *h_max;  // bits of the largest size in a row of xn; zeros for T * topk rows
     float eps;
     long long x_stride;
+    bool early;  // router weights may be read before the previous kernel ends (launch overlap is on)
 };
 cudaError_t launch_moe_layer_router(int32_t* ids, float* weights, const uint8_t* qs, const uint16_t* d, const LayerInput& layer,
                                     int dtype, int T, int E, int K, int topk, bool normalize, cudaStream_t s);

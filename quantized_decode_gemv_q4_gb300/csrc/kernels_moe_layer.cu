@@ -7,8 +7,9 @@
 //
 // Four kernels for a layer: the router (kernels_router.cu), gate and up, down (moe_experts.cuh) and the join here; three for the
 // down projections alone, whose first takes the largest size of each slot's vector, which gate and up leaves by itself. Each may
-// start while the one before it ends (programmatic dependent launch within the call, whatever the overlap setting says about
-// the call's first kernel) and waits for it before it touches what it wrote. h, z, the picks and xn stay in the workspace.
+// start while the one before it ends (programmatic dependent launch) and waits for it before it touches what it wrote; a call's
+// first kernel touches nothing before it has waited, so it is launched so whatever the overlap setting (1 token 29.0 us a call,
+// 26.9 us so). h, z, the picks and xn stay in the workspace.
 #include "block.h"
 #include "kv_common.cuh"
 
@@ -169,7 +170,7 @@ cudaError_t launch_moe_down(const MoeDownArgs& a, int dtype, void* workspace, co
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)slots), cfg.blockDim = dim3(256), cfg.stream = s;
-    cfg.attrs = attr, cfg.numAttrs = launch_overlap() ? 1 : 0;
+    cfg.attrs = attr, cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, moe_max_kernel, a.h, w.h_max, a.cols);
     if (e != cudaSuccess) return e;
     if ((e = launch_down(w, a.h, a.qs, a.d, a.ids, slots, a.E, a.rows, a.cols, dtype, di, s)) != cudaSuccess) return e;
@@ -200,7 +201,7 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a, int dtype, void* workspace, 
     const LayerSpace w(c, a.T, a.topk, N, K);
     int32_t* ids = a.ids ? a.ids : w.ids;
     float* weights = a.weights ? a.weights : w.weights;
-    const LayerInput in = {a.x, a.gamma, w.xn, w.x_max, w.down.h_max, a.eps, a.x_stride};
+    const LayerInput in = {a.x, a.gamma, w.xn, w.x_max, w.down.h_max, a.eps, a.x_stride, launch_overlap()};
     cudaError_t e = launch_moe_layer_router(ids, weights, a.w.router_qs, a.w.router_d, in, dtype, a.T, E, K, a.topk,
                                             a.normalize != 0, s);
     if (e != cudaSuccess) return e;

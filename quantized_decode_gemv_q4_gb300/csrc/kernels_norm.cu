@@ -141,10 +141,11 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, int dtype, cudaStrea
     return with_dtype(dtype, [&](auto tag) {
         using T = decltype(tag);
         const int vecs = (a.K + Vec<T>::N - 1) / Vec<T>::N;
+        // launched ahead whatever the overlap setting: the kernel touches nothing before it has waited
         auto go = [&](auto threads, auto vpt) {
             constexpr int P = decltype(threads)::value, VPT = decltype(vpt)::value;
             const dim3 grid((unsigned)(P == 32 ? (a.T - 1) / 4 + 1 : a.T)), block(P == 32 ? 128 : P);
-            return launch_grid(residual_norm_kernel<T, P, VPT>, grid, block, 0, s, launch_overlap(), a);
+            return launch_grid(residual_norm_kernel<T, P, VPT>, grid, block, 0, s, true, a);
         };
         auto threads = [&](int vpt) { return (vecs + vpt - 1) / vpt; };
         constexpr auto one = std::integral_constant<int, 1>();

@@ -92,11 +92,11 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
             db[j] = in ? (uint32_t)__ldg(p.d + blk) : 0u;
         }
     };
-    // The layer form for few tokens reads a warp's first rows while the previous kernel ends.
+    // The layer form for few tokens reads a warp's first rows while the previous kernel ends, where launch overlap allows it.
     constexpr bool kEarly = Layer && CS == 8;
     uint4 first_w[4];
     uint32_t first_db[4];
-    if (kEarly) load_units(c + CS * warp, c + CS * warp + CS * W, lane, first_w, first_db);
+    if (kEarly && p.layer.early) load_units(c + CS * warp, c + CS * warp + CS * W, lane, first_w, first_db);
 
     // x belongs to the previous kernel in the stream when launches overlap.
     grid_dependency_wait();
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
             const bool h1 = u1 < p.nblk;
             uint4 w[4];
             uint32_t db[4];
-            if (kEarly && e0 == c + CS * warp && u0 == lane) {
+            if (kEarly && p.layer.early && e0 == c + CS * warp && u0 == lane) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = first_w[j], db[j] = first_db[j];
             } else {
@@ -438,7 +438,7 @@ static cudaError_t launch_router(int32_t* ids, float* weights, float* logits, co
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = launch_overlap() ? 2 : 1;
+        cfg.numAttrs = layer || launch_overlap() ? 2 : 1;
         return cudaLaunchKernelEx(&cfg, kern, p);
     };
     constexpr uint32_t kPartBytes = W * 8;  // the layer form's sums and maxima

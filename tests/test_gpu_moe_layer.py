@@ -249,6 +249,40 @@ def test_two_graphs_and_streams_at_the_same_time():
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+def test_everything_written_directly_before_the_calls():
+    """With launch overlap off, the kernel before a call may write all that the call reads, weights among it."""
+    sets = [layer_case(6, 3, 8, 640, 1024, torch.float32, seed=s) for s in (1, 2)]
+    hid = [Rand(s).normal(6, 3, 640) for s in (1, 2)]
+    names = [f"{m}_{part}" for m in ("router", "gate", "up", "down") for part in ("qs", "d")]
+    live = {n: torch.empty_like(getattr(sets[0]["moe"], n)) for n in names}
+    moe = q4.MoEWeights(**live)
+    x, res, h = torch.empty(6, 1024, device="cuda"), torch.empty(6, 1024, device="cuda"), torch.empty_like(hid[0])
+    out, down = torch.empty_like(x), torch.empty_like(x)
+    ids, w = torch.empty(6, 3, dtype=torch.int32, device="cuda"), torch.empty(6, 3, device="cuda")
+    ws, ws2 = q4.moe_q4_layer_workspace(moe, x, 3), q4.moe_q4_down_workspace(down, h)
+
+    def load(a, hidden, wait):
+        for src, dst in [(a["x"], x), (a["residual"], res), *((getattr(a["moe"], n), live[n]) for n in names)]:
+            dst.copy_(src)
+            if wait:
+                torch.cuda.synchronize()
+        q4.moe_q4_layer(out, x, moe, 3, gamma=a["gamma"], residual=res, expert_ids=ids, expert_weights=w, workspace=ws)
+        first = out.clone()
+        h.copy_(hidden)
+        live["down_d"].mul_(2)
+        if wait:
+            torch.cuda.synchronize()
+        q4.moe_q4_down_gemv(down, live["down_qs"], live["down_d"], h, ids, w, residual=res, workspace=ws2)
+        q4.residual_norm(out, res, down, res, pre_gamma=a["gamma"])
+        return first, down.clone(), out.clone(), res.clone()
+
+    want = [load(a, hd, True) for a, hd in zip(sets, hid)]
+    torch.cuda.synchronize()
+    for i in range(40):
+        got = load(sets[i % 2], hid[i % 2], False)
+        assert all(torch.equal(g, v) for g, v in zip(got, want[i % 2])), i
+
+
 def test_layer_in_place_strides_and_workspace():
     T, K = 7, 288
     a = layer_case(T, 2, 5, 96, K, torch.float16)
