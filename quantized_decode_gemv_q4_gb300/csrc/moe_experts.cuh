@@ -17,7 +17,7 @@
 // in which lanes take them. tcgen05 is not used: its operands would have to be decoded into f16 tiles in shared memory first,
 // which costs the instructions that bind here and the writes besides, and at these few columns the matrix unit is a sixth busy.
 //
-// Copies. Each warp streams its chunks by cp.async through a ring of three stages of its own, across units and segments
+// Copies. Each warp streams its chunks by cp.async through a ring of three (or two) stages of its own, across units and segments
 // (16-byte chunks XOR-swizzled so that ldmatrix is free of bank conflicts); the scales of two chunks travel together. Four
 // stages: 8 tokens 61.6 us instead of 59.8.
 //
@@ -39,7 +39,6 @@ namespace q4 {
 
 namespace {
 
-constexpr int kStages = 3;                       // of a warp's ring
 constexpr int kChunk = 4;                        // blocks of a chunk
 constexpr uint32_t kStageBytes = 2048;           // a stage: 32 rows x 64 bytes of codes
 constexpr uint32_t kGroupBytes = 512;            // 32 rows x 8 scales: those of two chunks, in a ring of their own
@@ -112,8 +111,8 @@ __device__ __forceinline__ int vector_exponent(unsigned m) {
 }
 
 // PER: slots of a thread. Scales: bytes of a row's scales that one copy may move, 16 or 8 (rows of whole chunks then), or 0: see
-// scale_bytes. What every warp works out for itself is kept short: at the start of a kernel it costs all warps issue slots.
-template <bool GateUp, int Parts, int W, int PER, int Scales>
+// scale_bytes. kStages: of a warp's ring. What every warp works out for itself is kept short: at the start of a kernel it costs all warps issue slots.
+template <bool GateUp, int Parts, int W, int PER, int Scales, int kStages>
 __global__ void __launch_bounds__(W * 32, W == 6 ? 2 : 1) moe_expert_kernel(const ExpertParams p) {
     constexpr int kThreads = W * 32;
     constexpr int kNarrow = Parts == 2 ? 4 : 8;    // slots in one instruction's columns
@@ -625,13 +624,13 @@ struct ExpertPlan {
     int parts, part_blocks, cap;
     uint32_t ring_at, deposits_at, frags_at, smem;
 };
-ExpertPlan plan_experts(int blocks, bool cut, int vector_parts, int warps, int max_smem) {
+ExpertPlan plan_experts(int blocks, bool cut, int vector_parts, int warps, int stages, int max_smem) {
     ExpertPlan l;
     l.parts = cut ? moe_parts(blocks) : 1;
     const int per = l.part_blocks = ((blocks + l.parts - 1) / l.parts + 7) / 8 * 8;  // whole groups of scales
     for (l.cap = vector_parts == 1 ? 16 : 8; l.cap >= 1; l.cap /= 2) {
         l.ring_at = (sizeof(Tables) + 127) / 128 * 128;
-        l.deposits_at = l.ring_at + (uint32_t)(warps * kStages) * kSlotBytes;
+        l.deposits_at = l.ring_at + (uint32_t)(warps * stages) * kSlotBytes;
         l.frags_at = l.deposits_at + (uint32_t)warps * (l.cap > 8 ? 16 : 8) * 32 * 4;
         l.smem = l.frags_at + (uint32_t)(per * l.cap * vector_parts) * 64u;
         if (l.smem <= (uint32_t)max_smem) break;
@@ -639,10 +638,10 @@ ExpertPlan plan_experts(int blocks, bool cut, int vector_parts, int warps, int m
     return l;  // cap 0: one vector does not fit
 }
 
-template <bool GateUp, int Parts, int W, int PER, int Scales>
+template <bool GateUp, int Parts, int W, int PER, int Scales, int Stages>
 cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ctas, const DeviceInfo& di, bool overlap,
                               cudaStream_t s) {
-    auto kern = moe_expert_kernel<GateUp, Parts, W, PER, Scales>;
+    auto kern = moe_expert_kernel<GateUp, Parts, W, PER, Scales, Stages>;
     static std::once_flag once[64];
     cudaError_t e = cudaSuccess;
     std::call_once(once[di.device & 63],
@@ -656,11 +655,20 @@ cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ct
 template <bool GateUp, int Parts>
 cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
     const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
-    ExpertPlan l = plan_experts(p.blocks, !GateUp, Parts, 6, half);
-    const bool two = l.cap >= 8 / Parts && 2 * p.slots <= l.cap * p.E && p.slots <= 192;
-    if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 12, di.max_smem_optin);
+    ExpertPlan l = plan_experts(p.blocks, !GateUp, Parts, 6, 3, half);
+    const bool two = l.cap >= 8 / Parts && 2LL * p.slots <= (long long)l.cap * p.E && p.slots <= 192;
+    if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 12, 3, di.max_smem_optin);
+    // Where experts get more slots than half a segment's, a ring of two stages may make room for twice the slots: 64 f16 tokens, 64
+    // slots for each of 4 experts of 14336 x 4096, 900 us with 4 slots a segment, 654 us with 8; 32 bf16 tokens, 8 slots for
+    // each of 8 such experts, 213 us with 8 and 209 us with 16.
+    bool two_stages = false;
+    if (!two && 2LL * p.slots > (long long)l.cap * p.E) {
+        const ExpertPlan s = plan_experts(p.blocks, !GateUp, Parts, 12, 2, di.max_smem_optin);
+        two_stages = s.cap > l.cap;
+        if (two_stages) l = s;
+    }
     const bool eight = l.cap == 0;  // the longest vectors leave room for 8 warps
-    if (eight) l = plan_experts(p.blocks, !GateUp, Parts, 8, di.max_smem_optin);
+    if (eight) l = plan_experts(p.blocks, !GateUp, Parts, 8, 3, di.max_smem_optin);
     if (l.cap == 0) return cudaErrorNotSupported;
     p.units = GateUp ? p.rows / 16 : (p.rows + 31) / 32;
     p.parts = l.parts, p.part_blocks = l.part_blocks, p.cap = l.cap;
@@ -669,11 +677,12 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
     const uintptr_t d = reinterpret_cast<uintptr_t>(p.d0) | reinterpret_cast<uintptr_t>(p.d1);
     p.scale_bytes = p.blocks % 8 == 0 && d % 16 == 0 ? 16 : p.blocks % 4 == 0 && d % 8 == 0 ? 8 : p.blocks % 2 == 0 && d % 4 == 0 ? 4 : 2;
-    if (eight) return launch_experts_as<GateUp, Parts, 8, 2, 0>(p, l, 1, di, overlap, s);
+    if (eight) return launch_experts_as<GateUp, Parts, 8, 2, 0, 3>(p, l, 1, di, overlap, s);
     auto go = [&](auto scales) {
         constexpr int S = decltype(scales)::value;
-        return two ? launch_experts_as<GateUp, Parts, 6, 1, S>(p, l, 2, di, overlap, s)
-                   : launch_experts_as<GateUp, Parts, 12, 2, S>(p, l, 1, di, overlap, s);
+        return two          ? launch_experts_as<GateUp, Parts, 6, 1, S, 3>(p, l, 2, di, overlap, s)
+               : two_stages ? launch_experts_as<GateUp, Parts, 12, 2, S, 2>(p, l, 1, di, overlap, s)
+                            : launch_experts_as<GateUp, Parts, 12, 2, S, 3>(p, l, 1, di, overlap, s);
     };
     return p.scale_bytes == 16 ? go(std::integral_constant<int, 16>())
            : p.scale_bytes == 8 ? go(std::integral_constant<int, 8>())
