@@ -9,7 +9,7 @@
 // A thread reads its elements of x and residual before it writes any of them, so the outputs may be these inputs.
 //
 // Long prompts are bound by memory: 8191 bf16 rows of 4096 take 48 us, 5.6 TB/s of two reads and two writes, 0.82 of what a
-// copy (one of each) reaches. Few rows are bound by the launch and two chains of load, sum and store: 2.1 us for one.
+// copy (one of each) reaches. Few rows are bound by the launch and two chains of load, sum and store: 1.9 us for one.
 #include <algorithm>
 
 #include "block.h"
