@@ -283,6 +283,60 @@ def test_everything_written_directly_before_the_calls():
         assert all(torch.equal(g, v) for g, v in zip(got, want[i % 2])), i
 
 
+@pytest.mark.parametrize("overlap", [False, True])
+def test_graphs_whose_calls_follow_copies_fills_and_joined_streams(overlap):
+    """What a captured call may follow: another library's kernel, a copy, a fill, two streams that meet."""
+    a = layer_case(5, 2, 6, 96, 256, torch.bfloat16)
+    src = {n: t.clone() for n, t in (("x", a["x"]), ("residual", a["residual"]))}
+    h, y, out, down = (torch.empty_like(a["x"]) for _ in range(4))
+    hid, ids, w = Rand(2).normal(5, 2, 96), Rand(3).picks(5, 2, 6), torch.rand(5, 2, device="cuda")
+    moved = torch.empty_like(hid)
+    ws, ws2 = q4.moe_q4_layer_workspace(a["moe"], a["x"], 2), q4.moe_q4_down_workspace(down, hid)
+    other = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            a["residual"].copy_(src["residual"])
+            moved.zero_()
+            moved.add_(hid)
+        a["x"].copy_(src["x"])
+        here.wait_stream(other)
+        q4.residual_norm(h, y, a["x"], a["residual"], pre_gamma=a["gamma"])
+        y.mul_(2)
+        q4.moe_q4_layer(out, y, a["moe"], 2, gamma=a["gamma"], residual=h, workspace=ws)
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            q4.moe_q4_down_gemv(down, a["moe"].down_qs, a["moe"].down_d, moved, ids, w, residual=out, workspace=ws2)
+        h.fill_(1)
+        q4.residual_norm(h, y, out, h, pre_gamma=a["gamma"])
+        here.wait_stream(other)
+        q4.residual_norm(down, y, down, h, pre_gamma=a["gamma"])
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (h, y, out, down)]
+
+    q4.q4_set_launch_overlap(overlap)
+    try:
+        step()
+        want = results()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+        for _ in range(3):
+            for t in (a["x"], a["residual"], h, y, out, down, moved):
+                t.fill_(-3)
+            g.replay()
+            assert all(torch.equal(r, v) for r, v in zip(results(), want))
+    finally:
+        q4.q4_set_launch_overlap(False)
+    assert q4.q4_device_faults() == 0
+
+
 def test_layer_in_place_strides_and_workspace():
     T, K = 7, 288
     a = layer_case(T, 2, 5, 96, K, torch.float16)
