@@ -16,10 +16,10 @@
 //    the warp sums the lanes; the logits go to the CTA's own shared memory;
 //  * after a cluster barrier, CTA 0 gathers the other CTAs' logits through distributed shared memory; a second
 //    barrier releases them; its warp 0 then takes the softmax over all E logits (max subtracted) and the top K
-//    by a 64-bit key (the logit's order-preserving bits, a NaN below every other value, then the complement of
-//    the index, so ties go to the lower index): up to 64 experts by each expert's rank among all keys (one
-//    pass of shuffles), otherwise by K arg-max passes with taken experts marked in per-lane bit masks; it
-//    writes ids and weights (the logits, when asked, come from every CTA).
+//    by the logit's order-preserving bits (a NaN below every other value), ties to the lower index: up to 64
+//    experts by each expert's rank among all keys, which the whole CTA counts in shared memory, otherwise by K
+//    arg-max passes over 64-bit keys with taken experts marked in per-lane bit masks; it writes ids and weights
+//    (the logits, when asked, come from every CTA).
 #include <algorithm>
 #include <mutex>
 
