@@ -281,8 +281,8 @@ int kv4_attention(void *out, float *lse, const void *q, const kv4_cache *cache, 
 /*
  * ---- Around and inside a mixture-of-experts block ----
  * (No counterpart in the source pages.) Activations as in the section above: Q4_F32, Q4_F16 or Q4_BF16, rows of a token
- * `stride` elements apart and 16-byte aligned, fp32 sums, one rounding when a value is stored (but see moe_q4_down_gemv for
- * the vectors of bf16 layers).
+ * `stride` elements apart and 16-byte aligned, fp32 sums, one rounding when a value is stored (for how the experts'
+ * products hold their vectors see moe_q4_down_gemv).
  *
  * residual_norm: the norm behind a block, its gate and scales, the residual sum and the norm before the next block.
  *   b = x (post_gamma NULL) or x_i * post_gamma_i / sqrt(sum_j x_j^2 / K + eps);
@@ -303,7 +303,7 @@ int residual_norm(void *h_out, void *y_out, const void *x, const void *residual,
 /*
  * moe_q4_down_gemv: the down projections of the selected experts and their weighted sum, behind moe_q4_swiglu_gemv.
  *   out[t][n] = residual[t][n] + sum_{s < topk} expert_weights[t][s] * sum_k W[e*N + n][k] * h[t][s][k],
- *   e = expert_ids[t*topk + s]. Each selected expert's rows are read once for up to 8 (bf16: 16) slots.
+ *   e = expert_ids[t*topk + s]. Each selected expert's rows are read once for up to 8 slots.
  *   out [T][N]; residual [T][N] or NULL, which out may be (same pointer and stride); qs uint8[E*N][K/32][16], d
  *   uint16[E*N][K/32]; h float[T][topk][K] (16-byte aligned); expert_ids int32[T][topk], expert_weights float[T][topk]
  *   (device). 1 <= topk <= E; T*topk <= 512; N a multiple of 8 up to 2^20; K % 32 == 0, K <= 65536;
@@ -312,7 +312,7 @@ int residual_norm(void *h_out, void *y_out, const void *x, const void *residual,
  *   stored there. An expert may be given twice to a token.
  *   workspace: as for kv4_attention, of at least the bytes that moe_q4_down_workspace states for these sizes.
  *   A slot whose h holds a NaN or an infinity makes its token's row NaN. An element of h is held to 2^-33 of its slot's
- *   largest, or to 2^-22 of itself where that is more; for a bf16 out, which is rounded by 2^-8 itself, to 2^-11 of itself.
+ *   largest, or to 2^-22 of itself where that is more, whatever the type of out.
  */
 int moe_q4_down_workspace(size_t *bytes, int T, int topk, int N, int K);
 int moe_q4_down_gemv(void *out, const uint8_t *qs, const uint16_t *d, const float *h, const int32_t *expert_ids,

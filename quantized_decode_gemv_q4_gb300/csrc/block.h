@@ -35,8 +35,9 @@ struct ExpertParams {
 // parts fit beside the rings.
 constexpr int kPartBlocks = 88;
 inline int moe_parts(int blocks) { return (blocks + kPartBlocks - 1) / kPartBlocks; }
-cudaError_t launch_moe_gate_up(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s);
-cudaError_t launch_moe_down_products(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s);
+// bf16_values: the inputs are bf16 numbers (x as it is), which one f16 part holds.
+cudaError_t launch_moe_gate_up(const ExpertParams& p, bool bf16_values, const DeviceInfo& di, cudaStream_t s);
+cudaError_t launch_moe_down_products(const ExpertParams& p, const DeviceInfo& di, cudaStream_t s);
 
 // Down projections of T * topk slots and their weighted sum per token: rows = outputs, cols = inputs of an expert's matrix.
 struct MoeDownArgs {

@@ -3,8 +3,8 @@
 
 namespace q4 {
 
-cudaError_t launch_moe_down_products(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s) {
-    return launch_experts<false>(p, dtype, di, true, s);
+cudaError_t launch_moe_down_products(const ExpertParams& p, const DeviceInfo& di, cudaStream_t s) {
+    return launch_experts_of<false, 2>(p, di, true, s);
 }
 
 }  // namespace q4

@@ -145,12 +145,12 @@ struct DownSpace {
 };
 
 cudaError_t launch_down(const DownSpace& w, const float* h, const uint8_t* qs, const uint16_t* d, const int32_t* ids, int slots,
-                        int E, int rows, int cols, int dtype, const DeviceInfo& di, cudaStream_t s) {
+                        int E, int rows, int cols, const DeviceInfo& di, cudaStream_t s) {
     ExpertParams p = {};
     p.qs0 = p.qs1 = qs, p.d0 = p.d1 = d;
     p.in = h, p.in_max = w.h_max, p.out = w.z, p.ids = ids;
     p.E = E, p.rows = rows, p.blocks = cols / 32, p.slots = slots, p.per_in = 1;
-    return launch_moe_down_products(p, dtype, di, s);
+    return launch_moe_down_products(p, di, s);
 }
 
 }  // namespace
@@ -173,7 +173,7 @@ cudaError_t launch_moe_down(const MoeDownArgs& a, int dtype, void* workspace, co
     cfg.attrs = attr, cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, moe_max_kernel, a.h, w.h_max, a.cols);
     if (e != cudaSuccess) return e;
-    if ((e = launch_down(w, a.h, a.qs, a.d, a.ids, slots, a.E, a.rows, a.cols, dtype, di, s)) != cudaSuccess) return e;
+    if ((e = launch_down(w, a.h, a.qs, a.d, a.ids, slots, a.E, a.rows, a.cols, di, s)) != cudaSuccess) return e;
     const JoinParams join = {a.out, a.residual, w.z, a.weights, a.ids, a.topk, a.E, a.rows, moe_parts(a.cols / 32), slots,
                              a.out_stride, a.residual_stride, a.status, a.fault};
     return launch_join(join, a.T, dtype, true, s);
@@ -209,8 +209,8 @@ cudaError_t launch_moe_layer(const MoeLayerArgs& a, int dtype, void* workspace, 
     up.qs0 = a.w.gate_qs, up.qs1 = a.w.up_qs, up.d0 = a.w.gate_d, up.d1 = a.w.up_d;
     up.in = w.xn, up.in_max = w.x_max, up.out = w.h, up.out_max = w.down.h_max, up.ids = ids;
     up.E = E, up.rows = N, up.blocks = K / 32, up.slots = slots, up.per_in = a.topk;
-    if ((e = launch_moe_gate_up(up, dtype, di, s)) != cudaSuccess) return e;
-    if ((e = launch_down(w.down, w.h, a.w.down_qs, a.w.down_d, ids, slots, E, K, N, dtype, di, s)) != cudaSuccess) return e;
+    if ((e = launch_moe_gate_up(up, dtype == Q4_BF16 && !a.gamma, di, s)) != cudaSuccess) return e;
+    if ((e = launch_down(w.down, w.h, a.w.down_qs, a.w.down_d, ids, slots, E, K, N, di, s)) != cudaSuccess) return e;
     const JoinParams join = {a.out, a.residual, w.down.z, weights, ids, a.topk, E, K, moe_parts(N / 32), slots, a.out_stride,
                              a.residual_stride, nullptr, a.fault};
     return launch_join(join, a.T, dtype, true, s);

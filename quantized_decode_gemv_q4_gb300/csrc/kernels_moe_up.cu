@@ -3,8 +3,8 @@
 
 namespace q4 {
 
-cudaError_t launch_moe_gate_up(const ExpertParams& p, int dtype, const DeviceInfo& di, cudaStream_t s) {
-    return launch_experts<true>(p, dtype, di, true, s);
+cudaError_t launch_moe_gate_up(const ExpertParams& p, bool bf16_values, const DeviceInfo& di, cudaStream_t s) {
+    return bf16_values ? launch_experts_of<true, 1>(p, di, true, s) : launch_experts_of<true, 2>(p, di, true, s);
 }
 
 }  // namespace q4

@@ -10,11 +10,11 @@
 // Products run on m16n8k16 matrix instructions with the weights as rows: ldmatrix brings a block's word to each lane, eight
 // codes become eight exact f16 values code - 8 with nine instructions, and a block's fp32 sums are multiplied by the block's
 // scale in fp32. The columns are the segment's vectors in f16, scaled by a power of two that puts a vector's largest element
-// near 2^14. fp32 and f16 layers hold a vector in two parts (x = hi + lo to 2^-22): with up to 4 slots both parts share an
-// instruction's 8 columns, with more each part has its own and both add into the same sums. bf16 layers hold one part: 11
-// bits, an error of 2^-11 at most where the layer's own output is rounded by 2^-8, and twice the slots in an instruction (64
-// tokens over 64 experts of 1408 x 2048: 147 us with two parts, 127 us with one). The parts lie in shared memory in the order
-// in which lanes take them. tcgen05 is not used: its operands would have to be decoded into f16 tiles in shared memory first,
+// near 2^14. A vector is held in two parts (x = hi + lo to 2^-22): with up to 4 slots both parts share an instruction's 8
+// columns, with more each part has its own and both add into the same sums. A bf16 x that goes into gate and up as it is has
+// 8 bits, which one part holds exactly down to 2^-32 of the vector's largest element and to 2^-39 of it below: twice the slots
+// in an instruction. What is fp32 (h, and x behind its norm) takes two parts whatever the layer's type: one part's 11 bits
+// would show in the bf16 outputs, and h is the caller's. The parts lie in shared memory in the order in which lanes take them. tcgen05 is not used: its operands would have to be decoded into f16 tiles in shared memory first,
 // which costs the instructions that bind here and the writes besides, and at these few columns the matrix unit is a sixth busy.
 //
 // Copies. Each warp streams its chunks by cp.async through a ring of three (or two) stages of its own, across units and segments
@@ -687,11 +687,6 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     return p.scale_bytes == 16 ? go(std::integral_constant<int, 16>())
            : p.scale_bytes == 8 ? go(std::integral_constant<int, 8>())
                                 : go(std::integral_constant<int, 0>());
-}
-
-template <bool GateUp>
-cudaError_t launch_experts(const ExpertParams& p, int dtype, const DeviceInfo& di, bool overlap, cudaStream_t s) {
-    return dtype == Q4_BF16 ? launch_experts_of<GateUp, 1>(p, di, overlap, s) : launch_experts_of<GateUp, 2>(p, di, overlap, s);
 }
 
 }  // namespace

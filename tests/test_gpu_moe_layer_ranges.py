@@ -1,0 +1,111 @@
+"""The experts' products where precision or a range ends: sums that cancel, vectors of which more than f16's bits matter."""
+
+import pytest
+import torch
+
+import moe_ref as ref
+from test_gpu_moe_layer import Rand, down_case, layer_case, run_layer
+
+pytestmark = pytest.mark.gpu
+
+import quantized_decode_gemv_q4_gb300 as q4  # noqa: E402
+
+DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def pairs(*shape):
+    """Rows [..., K] (K = 32 n) of which only weights 2r and 2r + 1 (mod K) of row r are not zero: 1 and -1."""
+    *lead, rows, K = shape
+    qs = torch.full((*lead, rows, K // 32, 16), 0x88, dtype=torch.uint8, device="cuda")
+    for r in range(rows):
+        for k, code in ((2 * r % K, 9), ((2 * r + 1) % K, 7)):
+            byte = qs[..., r, k // 32, k % 16]
+            byte.copy_((byte & 0xF0) | code if k % 32 < 16 else (byte & 0x0F) | code << 4)
+    return qs, torch.ones(*lead, rows, K // 32, dtype=torch.float16, device="cuda")
+
+
+@pytest.mark.parametrize("T,topk,E", [(1, 1, 1), (3, 2, 2), (8, 2, 3), (40, 1, 2), (64, 4, 4)])
+@pytest.mark.parametrize("dt", DTYPES)
+def test_down_of_vectors_that_all_but_cancel(T, topk, E, dt):
+    """out = h[2r] - h[2r + 1], which differ from the 13th bit on: 22 bits of each leave a difference to 2^-9 of itself,
+    11 bits leave none of it."""
+    K, N = 96, 48
+    r = Rand(T)
+    qs, d = pairs(E, N, K)
+    h = r.normal(T, topk, K).abs() + 1
+    h[..., 1::2] = h[..., 0::2] * (1 + 2.0 ** -12 * (1 + torch.rand(T, topk, K // 2, generator=r.g, device="cuda")))
+    a = dict(qs=qs, d=d, h=h, expert_ids=r.picks(T, topk, E), expert_weights=torch.softmax(r.normal(T, topk), -1))
+    out = torch.empty(T, N, dtype=dt, device="cuda")
+    q4.moe_q4_down_gemv(out, **a)
+    z = h[..., 0::2].double() - h[..., 1::2].double()
+    w = a["expert_weights"].double().unsqueeze(-1)
+    want = (w * z).sum(1)
+    # each element is held to 2^-22, their difference and the sums add at most topk + 4 half steps of fp32
+    held = 2.0 ** -22 * (h[..., 0::2] + h[..., 1::2]).double()
+    lim = (w * (held + (topk + 4) * ref.U * z.abs())).sum(1) + ref.rounded(want, dt) * (1 + 2.0 ** -7)
+    off = (out.double() - want).abs()
+    assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
+
+
+@pytest.mark.parametrize("T,topk,E,N,K", [(1, 8, 8, 64, 96), (8, 8, 64, 256, 512), (64, 8, 16, 136, 352), (9, 2, 2, 72, 4128),
+                                          (33, 1, 1, 200, 224)])
+@pytest.mark.parametrize("dt", DTYPES)
+def test_down_behind_a_residual_that_takes_it_away(T, topk, E, N, K, dt):
+    """The residual is the sum's rounded opposite, so that the output shows what its own rounding hides otherwise."""
+    a = down_case(T, topk, E, N, K, dt, residual=False)
+    args = (a["h"].double(), torch.zeros_like(a["h"], dtype=torch.float64), lambda e: ref.q4_matrix(a["qs"][e], a["d"][e]),
+            a["expert_ids"].long(), a["expert_weights"].double(), torch.zeros_like(a["expert_weights"], dtype=torch.float64))
+    a["residual"] = -ref.down(*args, None, N)[0].to(dt)
+    out = torch.empty(T, N, dtype=dt, device="cuda")
+    q4.moe_q4_down_gemv(out, **a)
+    want, err = ref.down(*args, a["residual"], N)
+    off, lim = (out.double() - want).abs(), err + ref.rounded(want, dt) * (1 + 2.0 ** -7)
+    assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
+
+
+@pytest.mark.parametrize("T,topk,E,N,K", [(1, 1, 1, 32, 32), (5, 2, 3, 32, 64), (24, 1, 2, 64, 32), (64, 2, 2, 32, 32)])
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("norm", [True, False])
+def test_layer_behind_a_residual_that_takes_it_away(T, topk, E, N, K, dt, norm):
+    """As above, with the products' precision the same for every type of the layer."""
+    a = layer_case(T, topk, E, N, K, dt, norm)
+    a["residual"] = None
+    _, ids, _ = run_layer(a)
+
+    def exact(residual):  # x by its values: fp32 holds every type's
+        return ref.layer(a["x"].float(), a["mats"], a["gamma"], 1e-6, residual, ids.long(), True)[0]
+
+    a["residual"] = -exact(None)[0].to(dt)
+    out, again, _ = run_layer(a)
+    assert torch.equal(ids, again)
+    want, err = exact(a["residual"])
+    off, lim = (out.double() - want).abs(), err + ref.rounded(want, dt) * (1 + 2.0 ** -7)
+    assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
+
+
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_bf16_layer_of_inputs_that_all_but_cancel(T):
+    """A norm with weights of 24 bits in front of gate and up whose rows take differences of neighbouring elements."""
+    K, N = 96, 32
+    r = Rand(T)
+    parts = dict(router=pairs(1, K), gate=pairs(1, N, K), up=pairs(1, N, K), down=pairs(1, K, N))
+    parts["gate"][1].mul_(2048), parts["up"][1].mul_(2048)
+    moe = q4.MoEWeights(*(t for pair in parts.values() for t in pair))
+    x = (r.normal(T, K).abs() + 1).to(torch.bfloat16)
+    x[:, 1::2] = x[:, 0::2]
+    gamma = torch.ones(K, device="cuda")
+    gamma[1::2] += 2.0 ** -12 * (1 + torch.rand(K // 2, generator=r.g, device="cuda"))
+    out = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    q4.moe_q4_layer(out, x, moe, 1, gamma=gamma)
+    v, _ = ref.rms(x.double(), torch.zeros(T, K, dtype=torch.float64, device="cuda"), gamma.double(), 1e-6)
+    g = 2048 * (v[:, 0::2] - v[:, 1::2])[:, torch.arange(N) % (K // 2)]
+    # v is off by 46 U (one number for a row, which the differences keep) and 4 U of its own, and held to 2^-22 (4 U)
+    dg = 46 * ref.U * g.abs() + 2048 * 8 * ref.U * 2 * v.abs().amax(-1, keepdim=True)
+    a = g * torch.sigmoid(g)
+    h = a * g
+    dh = 1.1 * dg * (g.abs() + dg) + a.abs() * dg + (10 + g.abs()) * ref.U * h.abs()
+    down = torch.cat([h[:, 0::2] - h[:, 1::2]] * (K // (N // 2)), -1)[:, :K]
+    err = torch.cat([(dh + 2.0 ** -22 * h.abs())[:, 0::2] + (dh + 2.0 ** -22 * h.abs())[:, 1::2]] * (K // (N // 2)), -1)[:, :K]
+    lim = err + 6 * ref.U * down.abs() + ref.rounded(down, torch.bfloat16) * (1 + 2.0 ** -7)
+    off = (out.double() - down).abs()
+    assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
