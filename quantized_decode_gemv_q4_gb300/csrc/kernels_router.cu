@@ -125,17 +125,19 @@ __global__ void __launch_bounds__(W * 32, 1) moe_router_kernel(const RouterParam
             }
         }
         if (Layer && p.layer.gamma) {
-            float sum = 0.f;
+            // four sums a thread: a row of 32768 adds 32 squares to each, not 128 to one, and at most 47 steps in all
+            float four[4] = {};
 #pragma unroll
             for (int q = 0; q < kKept; ++q)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf(kept[q][j], kept[q][j], sum);
+                for (int j = 0; j < 8; ++j) four[j & 3] = fmaf(kept[q][j], kept[q][j], four[j & 3]);
             for (int i = threadIdx.x + kKept * W * 32; i < p.nblk * 4; i += W * 32) {
                 float v[8];
                 load_floats(row + i * 8, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+                for (int j = 0; j < 8; ++j) four[j & 3] = fmaf(v[j], v[j], four[j & 3]);
             }
+            float sum = (four[0] + four[1]) + (four[2] + four[3]);
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) part_sum[warp] = sum;

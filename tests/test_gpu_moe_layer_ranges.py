@@ -109,3 +109,26 @@ def test_bf16_layer_of_inputs_that_all_but_cancel(T):
     lim = err + 6 * ref.U * down.abs() + ref.rounded(down, torch.bfloat16) * (1 + 2.0 ** -7)
     off = (out.double() - down).abs()
     assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_norm_of_a_long_row_whose_first_squares_are_the_largest(T):
+    """A large element in the first vector that a thread adds, and squares behind it that are less than half a step of it: one
+    after the other they would all be lost, 127 half steps of the sum and as many again in silu(g) * u."""
+    K, N = 32768, 32
+    parts = {}
+    for name, rows, cols in (("router", 1, K), ("gate", N, K), ("up", N, K), ("down", K, N)):
+        qs = torch.full((1, rows, cols // 32, 16), 0x88, dtype=torch.uint8, device="cuda")
+        qs[0, :, 0, 0] = 0x89  # each row takes its vector's first element
+        parts[name] = qs, torch.ones(1, rows, cols // 32, dtype=torch.float16, device="cuda")
+    parts["router"] = tuple(t[0] for t in parts["router"])
+    x = torch.full((T, K), 2.0 ** -12 * (1 - 2.0 ** -10), device="cuda")
+    x[:, :2048:8] = 1
+    gamma, out = torch.ones(K, device="cuda"), torch.empty(T, K, device="cuda")
+    q4.moe_q4_layer(out, x, q4.MoEWeights(*(t for pair in parts.values() for t in pair)), 1, gamma=gamma)
+    g = 1 / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+    want = g * torch.sigmoid(g) * g
+    # The sum: at most 47 steps (halved by the root), 9 U for the root and the products, 4 U as it is held and 3 U more in each
+    # of gate and up (41 U); their product has both, silu's slope being 1 here, and 10 U of its own; 7 U more in down.
+    lim = (2 * (47 / 2 + 9 + 4 + 3) + 10 + 7) * ref.U * want
+    assert bool(((out.double() - want).abs() <= lim).all()), f"{float(((out.double() - want).abs() / want).max() / ref.U):.1f} U"
