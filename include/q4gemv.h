@@ -344,9 +344,10 @@ typedef struct {
  *   out, x [T][K]; residual [T][K] or NULL. out may be x or residual, residual may be x (same pointers and strides).
  *   expert_ids int32[T][topk], expert_weights float[T][topk]: the picks, each written when not NULL.
  *   1 <= topk <= E <= 4096; T*topk <= 512; N % 32 == 0, N <= 65536; K % 32 == 0, K <= 32768; E*N, E*K < 2^31.
- *   A token whose x, logits or h hold a NaN or an infinity gets a NaN row (its ids are valid all the same); no other token
- *   is touched. With gamma the sum of squares is fp32, with residual_norm's range. workspace: as above, of the bytes that moe_q4_layer_workspace states; x and h are held as h is in
- *   moe_q4_down_gemv.
+ *   A token whose x or h hold a NaN or an infinity, or whose logits hold a NaN or +infinity or are all -infinity, gets a NaN
+ *   row (its ids are valid all the same); no other token is touched. A logit of -infinity beside others is a share of zero.
+ *   With gamma the sum of squares is fp32, with residual_norm's range. workspace: as above, of the bytes that
+ *   moe_q4_layer_workspace states; x and h are held as h is in moe_q4_down_gemv.
  */
 int moe_q4_layer_workspace(size_t *bytes, int T, int topk, int E, int N, int K);
 int moe_q4_layer(void *out, const void *x, const moe_q4_weights *weights, const float *gamma, float eps, const void *residual,

@@ -132,3 +132,28 @@ def test_norm_of_a_long_row_whose_first_squares_are_the_largest(T):
     # of gate and up (41 U); their product has both, silu's slope being 1 here, and 10 U of its own; 7 U more in down.
     lim = (2 * (47 / 2 + 9 + 4 + 3) + 10 + 7) * ref.U * want
     assert bool(((out.double() - want).abs() <= lim).all()), f"{float(((out.double() - want).abs() / want).max() / ref.U):.1f} U"
+
+
+@pytest.mark.parametrize("topk", [2, 4])
+@pytest.mark.parametrize("T", [3, 64])
+def test_infinite_logits(T, topk):
+    """-infinity beside other logits: a share of zero, and the row that a very low logit gives. +infinity, or -infinity alone: a
+    NaN row, of valid picks."""
+    a = layer_case(T, topk, 4, 64, 96, torch.float32, norm=False)
+    m = a["moe"]
+    a["x"].abs_().add_(0.1)  # so that a block of equal codes has a sum of their sign
+    m.router_qs[1] = 0x99
+    m.router_d[1] = -60000.0  # a logit far below where a share is exactly zero
+    want = run_layer(a)
+    m.router_d[1, 0] = float("-inf")
+    got = run_layer(a)
+    assert all(torch.equal(g, w) for g, w in zip(got, want)) and bool(got[0].isfinite().all())
+    assert bool((got[2][got[1] == 1] == 0).all()) and bool((got[1] == 1).any()) == (topk == 4)
+    m.router_d[1, 0] = float("inf")
+    out, ids, _ = run_layer(a)
+    assert bool(out.isnan().all()) and bool(((ids >= 0) & (ids < 4)).all())
+    m.router_qs[:] = 0x99
+    m.router_d[:] = float("-inf")
+    out, ids, _ = run_layer(a)
+    assert bool(out.isnan().all()) and bool(((ids >= 0) & (ids < 4)).all())
+    assert q4.q4_device_faults() == 0
