@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import moe_ref as ref
-from test_gpu_moe_layer import Rand, down_case, layer_case, run_layer
+from test_gpu_moe_layer import Rand, check_down, down_case, layer_case, run_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -13,12 +13,12 @@ import quantized_decode_gemv_q4_gb300 as q4  # noqa: E402
 DTYPES = [torch.float32, torch.float16, torch.bfloat16]
 
 
-def pairs(*shape):
-    """Rows [..., K] (K = 32 n) of which only weights 2r and 2r + 1 (mod K) of row r are not zero: 1 and -1."""
+def pairs(*shape, second=7):
+    """Rows [..., K] (K = 32 n) of which only weights 2r and 2r + 1 (mod K) of row r are not zero: 1 and -1 (or second - 8)."""
     *lead, rows, K = shape
     qs = torch.full((*lead, rows, K // 32, 16), 0x88, dtype=torch.uint8, device="cuda")
     for r in range(rows):
-        for k, code in ((2 * r % K, 9), ((2 * r + 1) % K, 7)):
+        for k, code in ((2 * r % K, 9), ((2 * r + 1) % K, second)):
             byte = qs[..., r, k // 32, k % 16]
             byte.copy_((byte & 0xF0) | code if k % 32 < 16 else (byte & 0x0F) | code << 4)
     return qs, torch.ones(*lead, rows, K // 32, dtype=torch.float16, device="cuda")
@@ -157,3 +157,38 @@ def test_infinite_logits(T, topk):
     out, ids, _ = run_layer(a)
     assert bool(out.isnan().all()) and bool(((ids >= 0) & (ids < 4)).all())
     assert q4.q4_device_faults() == 0
+
+
+def test_down_of_the_smallest_numbers():
+    """Slots whose largest element lies near the least of fp32's range, subnormal ones among them."""
+    a = down_case(9, 2, 3, 64, 288, torch.float32, residual=False)
+    a["d"] = (a["d"].float() * 2.0 ** 21).half()  # whole numbers: what stays subnormal is exact but for the weighted sum
+    top = a["h"].abs().amax(-1, keepdim=True)
+    exponents = torch.tensor([-149, -140, -130, -127, -126, -125, -121, -118, -112], device="cuda", dtype=torch.float64)
+    a["h"] = (a["h"].double() / top * torch.exp2(exponents)[:, None, None]).float()
+    assert bool((a["h"].abs().amax(-1) > 0).all())
+    out = torch.empty(9, 64, device="cuda")
+    q4.moe_q4_down_gemv(out, **a)
+    check_down(a, out)
+
+
+@pytest.mark.parametrize("exponent", [-148, -140, -126, -125, -119, -112, 0, 100])
+def test_down_holds_small_elements_beside_large_ones(exponent):
+    """One element of 2^exponent or so, which scales its slot, beside smaller ones that the rows take alone."""
+    K, N, T = 96, 48, 8
+    r = Rand(exponent + 200)
+    qs, d = pairs(1, N, K, second=8)
+    d.mul_(8192)
+    h = torch.rand(T, 1, K, generator=r.g, device="cuda", dtype=torch.float64) + 0.5
+    h *= torch.exp2(torch.randint(-36, 1, h.shape, generator=r.g, device="cuda").double())
+    h[..., 1] = 1.9
+    h = (h * 2.0 ** exponent).float()
+    out = torch.empty(T, N, device="cuda")
+    one = torch.ones(T, 1, device="cuda")
+    q4.moe_q4_down_gemv(out, qs, d, h, torch.zeros(T, 1, dtype=torch.int32, device="cuda"), one)
+    want = 8192 * h[:, 0, 0::2].double()
+    top = h.abs().amax(-1).double()
+    # held to 2^-22 of itself or 2^-33 of the largest; one product, with 4 half steps for what is done to it
+    lim = torch.maximum(2.0 ** -22 * want.abs(), 8192 * 2.0 ** -33 * top) + 4 * ref.U * want.abs() + 2 * ref.TINY[torch.float32]
+    off = (out.double() - want).abs()
+    assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
