@@ -343,8 +343,8 @@ class KV4Cache:
 
     ``k_qs``, ``v_qs`` uint8 ``[num_pages, num_kv_heads, page_size, head_dim/2]`` and ``k_d``, ``v_d`` float16
     ``[num_pages, num_kv_heads, page_size, head_dim/32]``, contiguous on one CUDA device. The object keeps the tensors
-    (and the struct that the calls take, made once: its attributes cannot be set) and nothing else; :meth:`allocate` makes
-    an empty one, whose rows read as zeros.
+    (and the struct that the calls take, made once: its attributes cannot be set or deleted) and nothing else;
+    :meth:`allocate` makes an empty one, whose rows read as zeros.
     """
 
     class _Struct(ctypes.Structure):
@@ -368,6 +368,9 @@ class KV4Cache:
                              head_dim=half * 2, device=k_qs.device, _struct=struct, _ref=ctypes.addressof(struct))
 
     def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: a KV4Cache's tensors and sizes are fixed; make another one")
+
+    def __delattr__(self, name):  # the struct would go on pointing to freed memory
         raise AttributeError(f"{name}: a KV4Cache's tensors and sizes are fixed; make another one")
 
     @classmethod
@@ -666,7 +669,7 @@ class MoEWeights:
 
     ``router_qs`` uint8 ``[E, K/32, 16]`` and ``router_d`` float16 ``[E, K/32]``; ``gate`` and ``up`` ``[E, N, K/32, 16]`` and
     ``[E, N, K/32]``; ``down`` ``[E, K, N/32, 16]`` and ``[E, K, N/32]``; contiguous on one CUDA device. The object keeps the
-    tensors (and the struct that the calls take, made once: its attributes cannot be set) and nothing else.
+    tensors (and the struct that the calls take, made once: its attributes cannot be set or deleted) and nothing else.
     """
 
     class _Struct(ctypes.Structure):
@@ -694,6 +697,9 @@ class MoEWeights:
         self.__dict__.update(tensors, E=E, N=N, K=K, device=router_qs.device, _struct=struct, _ref=ctypes.addressof(struct))
 
     def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: MoEWeights' tensors and sizes are fixed; make another one")
+
+    def __delattr__(self, name):  # the struct would go on pointing to freed memory
         raise AttributeError(f"{name}: MoEWeights' tensors and sizes are fixed; make another one")
 
 

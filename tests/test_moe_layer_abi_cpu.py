@@ -137,3 +137,13 @@ def test_binding_refuses_cpu_tensors_and_shapes():
         q4.MoEWeights(*good[0], *q4_pair(4, 48, 96), *q4_pair(4, 48, 96), *good[3])
     with pytest.raises(TypeError, match="CUDA"):
         q4.MoEWeights(*(t for p in good for t in p))
+
+
+@pytest.mark.parametrize("handle", [q4.MoEWeights, q4.KV4Cache])
+def test_handles_keep_what_their_structs_point_to(handle):
+    made = object.__new__(handle)  # without a GPU: only what guards the attributes
+    made.__dict__["tensor"] = torch.zeros(1)
+    for change in (lambda: setattr(made, "tensor", None), lambda: delattr(made, "tensor"), lambda: delattr(made, "_struct")):
+        with pytest.raises(AttributeError, match="make another one"):
+            change()
+    assert made.tensor is not None
