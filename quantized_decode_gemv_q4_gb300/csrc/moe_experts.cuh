@@ -661,14 +661,13 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     // Where experts get more slots than half a segment's, a ring of two stages may make room for twice the slots: 64 f16 tokens, 64
     // slots for each of 4 experts of 14336 x 4096, 900 us with 4 slots a segment, 654 us with 8; 32 bf16 tokens, 8 slots for
     // each of 8 such experts, 213 us with 8 and 209 us with 16.
+    // Down's parts are short enough for full segments beside three stages.
     bool two_stages = false;
-    if (!two && 2LL * p.slots > (long long)l.cap * p.E) {
+    if (GateUp && !two && 2LL * p.slots > (long long)l.cap * p.E) {
         const ExpertPlan s = plan_experts(p.blocks, !GateUp, Parts, 12, 2, di.max_smem_optin);
         two_stages = s.cap > l.cap;
         if (two_stages) l = s;
     }
-    const bool eight = l.cap == 0;  // the longest vectors leave room for 8 warps
-    if (eight) l = plan_experts(p.blocks, !GateUp, Parts, 8, 3, di.max_smem_optin);
     if (l.cap == 0) return cudaErrorNotSupported;
     p.units = GateUp ? p.rows / 16 : (p.rows + 31) / 32;
     p.parts = l.parts, p.part_blocks = l.part_blocks, p.cap = l.cap;
@@ -677,12 +676,12 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     p.ring_at = l.ring_at, p.deposits_at = l.deposits_at, p.frags_at = l.frags_at;
     const uintptr_t d = reinterpret_cast<uintptr_t>(p.d0) | reinterpret_cast<uintptr_t>(p.d1);
     p.scale_bytes = p.blocks % 8 == 0 && d % 16 == 0 ? 16 : p.blocks % 4 == 0 && d % 8 == 0 ? 8 : p.blocks % 2 == 0 && d % 4 == 0 ? 4 : 2;
-    if (eight) return launch_experts_as<GateUp, Parts, 8, 2, 0, 3>(p, l, 1, di, overlap, s);
     auto go = [&](auto scales) {
         constexpr int S = decltype(scales)::value;
-        return two          ? launch_experts_as<GateUp, Parts, 6, 1, S, 3>(p, l, 2, di, overlap, s)
-               : two_stages ? launch_experts_as<GateUp, Parts, 12, 2, S, 2>(p, l, 1, di, overlap, s)
-                            : launch_experts_as<GateUp, Parts, 12, 2, S, 3>(p, l, 1, di, overlap, s);
+        if (two) return launch_experts_as<GateUp, Parts, 6, 1, S, 3>(p, l, 2, di, overlap, s);
+        if constexpr (GateUp)
+            if (two_stages) return launch_experts_as<GateUp, Parts, 12, 2, S, 2>(p, l, 1, di, overlap, s);
+        return launch_experts_as<GateUp, Parts, 12, 2, S, 3>(p, l, 1, di, overlap, s);
     };
     return p.scale_bytes == 16 ? go(std::integral_constant<int, 16>())
            : p.scale_bytes == 8 ? go(std::integral_constant<int, 8>())
