@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import moe_ref as ref
-from test_gpu_moe_layer import Rand, check_down, down_case, layer_case, run_layer
+from test_gpu_moe_layer import Rand, check_down, check_layer, down_case, layer_case, run_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +192,53 @@ def test_down_holds_small_elements_beside_large_ones(exponent):
     lim = torch.maximum(2.0 ** -22 * want.abs(), 8192 * 2.0 ** -33 * top) + 4 * ref.U * want.abs() + 2 * ref.TINY[torch.float32]
     off = (out.double() - want).abs()
     assert bool((off <= lim).all()), f"{float((off / lim).max()):.2f} of the limit"
+
+
+# Gate and up in every ring, with copies of 16, 8 and 2 bytes of scales and of few and many slots an expert. K of 4096 and 4224:
+# two stages where slots are many, three where they are few; rows of an odd number of 128-column chunks (4224, 896, 1152, 1920),
+# so that warps start and end on either half of a pair of chunks; enough rows that a ring goes round many times; parts of x
+# that fit once (15360, 15488) or four times (7680, 7808).
+FORMS = [(64, 4, 4, 512, 4096), (64, 4, 4, 512, 4224), (64, 2, 3, 256, 4128), (3, 1, 1, 1024, 4224), (2, 1, 1, 1024, 4096),
+         (1, 2, 2, 512, 4224), (1, 2, 2, 512, 4096), (100, 2, 64, 96, 4224), (64, 8, 16, 64, 896), (64, 8, 16, 320, 1408),
+         (48, 8, 16, 256, 1024), (5, 2, 6, 96, 1152), (12, 3, 40, 256, 1920), (12, 3, 40, 256, 2048), (24, 8, 32, 288, 640),
+         (7, 2, 2, 64, 15360), (7, 2, 2, 64, 15488), (1, 1, 4, 96, 15488), (9, 2, 2, 96, 7680), (9, 2, 2, 96, 7808),
+         (6, 1, 1, 32, 30720), (6, 1, 1, 32, 30848)]
+
+
+@pytest.mark.parametrize("T,topk,E,N,K", FORMS)
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_layer_in_every_form_of_its_products(T, topk, E, N, K, dt):
+    a = layer_case(T, topk, E, N, K, dt, norm=False)
+    out, ids, w = run_layer(a)
+    by_value = dict(a, x=a["x"].float())  # the same precision for every type
+    check_layer(by_value, out, ids, w, keep=list(range(0, T, max(1, T * topk // 48))))
+    assert torch.equal(run_layer(a)[0], out)
+
+
+@pytest.mark.parametrize("T,topk,E,N,K", [(12, 2, 6, 256, 1024), (13, 2, 8, 256, 1152), (9, 3, 8, 96, 672), (40, 3, 64, 96, 1920)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_layer_whose_tokens_meet_at_few_of_many_experts(T, topk, E, N, K, dt):
+    """Tokens that are multiples of one another pick the same experts: full segments in the form for few slots an expert."""
+    a = layer_case(T, topk, E, N, K, dt, norm=False)
+    a["x"] = (a["x"][:1].float() * torch.linspace(0.5, 2, T, device="cuda")[:, None]).to(dt)
+    out, ids, w = run_layer(a)
+    assert bool((ids[0].sort().values == ids.sort(-1).values).all(-1).sum() > 8)
+    check_layer(dict(a, x=a["x"].float()), out, ids, w)
+    assert torch.equal(run_layer(a)[0], out)
+
+
+@pytest.mark.parametrize("T,topk,E,N,K", [(5, 2, 6, 96, 1024), (48, 4, 4, 96, 1024), (64, 4, 4, 64, 4096)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_layer_with_scales_at_any_alignment(T, topk, E, N, K, dt):
+    """Scales of one matrix 2, 4 and 8 bytes past a 16-byte boundary: other copies, the same bits."""
+    a = layer_case(T, topk, E, N, K, dt, norm=False)
+    m, want = a["moe"], run_layer(a)
+    names = [f"{n}_{part}" for n in ("router", "gate", "up", "down") for part in ("qs", "d")]
+    for name in ("gate_d", "up_d", "down_d"):
+        for shift in (1, 2, 4):
+            d = getattr(m, name)
+            moved = torch.empty(d.numel() + 8, dtype=torch.float16, device="cuda")[shift:shift + d.numel()].view(d.shape)
+            moved.copy_(d)
+            moe = q4.MoEWeights(**dict({n: getattr(m, n) for n in names}, **{name: moved}))
+            got = run_layer(dict(a, moe=moe))
+            assert all(torch.equal(g, v) for g, v in zip(got, want)), (name, shift)
