@@ -452,7 +452,7 @@ static cudaError_t launch_router(int32_t* ids, float* weights, float* logits, co
     return with_dtype(dtype, [&](auto tag) {
         using X = decltype(tag);
         static std::once_flag once[64], once_many[64];
-        // more clusters of 8 than fit at once come in two waves (the layer of 64 tokens 96.0 us, 95.0 us with clusters of 2)
+        // more clusters of 8 than fit at once come in two waves (with clusters of 2 a layer of 64 tokens takes 1.0 us less)
         return T * CS <= 2 * di.sm_count ? launch(moe_router_kernel<W, CS, X>, CS, once)
                                          : launch(moe_router_kernel<W, 2, X>, 2, once_many);
     });

@@ -13,9 +13,12 @@
 // near 2^14. A vector is held in two parts (x = hi + lo to 2^-22): with up to 4 slots both parts share an instruction's 8
 // columns, with more each part has its own and both add into the same sums. A bf16 x that goes into gate and up as it is has
 // 8 bits, which one part holds exactly down to 2^-32 of the vector's largest element and to 2^-39 of it below: twice the slots
-// in an instruction. What is fp32 (h, and x behind its norm) takes two parts whatever the layer's type: one part's 11 bits
-// would show in the bf16 outputs, and h is the caller's. The parts lie in shared memory in the order in which lanes take them. tcgen05 is not used: its operands would have to be decoded into f16 tiles in shared memory first,
-// which costs the instructions that bind here and the writes besides, and at these few columns the matrix unit is a sixth busy.
+// in an instruction (64 tokens over 64 experts of 1408 x 2048: 117 us in two parts, 105 us in one). What is fp32 (h, and x
+// behind its norm) takes two parts whatever the layer's type: one part's 11 bits would show in the bf16 outputs, and h is the
+// caller's. The parts lie in shared memory in the order in which lanes take them. tcgen05 is not used: its operands would have to
+// be decoded into f16 tiles in shared memory first, which costs the instructions that bind here and the writes besides, and at
+// these few columns the matrix unit is a sixth busy. For segments of 32 slots and more, of which one decode could serve many
+// columns, it was not tried.
 //
 // Copies. Each warp streams its chunks by cp.async through a ring of three (or two) stages of its own, across units and segments
 // (16-byte chunks XOR-swizzled so that ldmatrix is free of bank conflicts); the scales of two chunks travel together. Four
@@ -117,8 +120,8 @@ __global__ void __launch_bounds__(W * 32, W == 6 ? 2 : 1) moe_expert_kernel(cons
     constexpr int kThreads = W * 32;
     constexpr int kNarrow = Parts == 2 ? 4 : 8;    // slots in one instruction's columns
     constexpr int kTiles = Parts == 2 ? 1 : 2;     // sums of 8 slots that a warp keeps
-    // Cost of a unit of a segment whose columns fill one instruction, or two: 64 tokens over 64 experts take 102 us with 4 : 5,
-    // 96 us with 4 : 6 and 101 us with 4 : 7 in bf16, in fp32 119, 127 and 139 us.
+    // Cost of a unit of a segment whose columns fill one instruction, or two: 64 fp32 tokens over 64 experts take 119 us with
+    // 4 : 5, 127 us with 4 : 6 and 139 us with 4 : 7; with x in one part 107 us with 4 : 5 and 105 us with 4 : 6.
     constexpr unsigned kNarrowCost = 4, kWideCost = Parts == 1 ? 6 : 5;
     constexpr bool kRoom = W == 6 && PER == 1;     // of two CTAs an SM: see launch_experts_of
     extern __shared__ __align__(128) uint8_t smem[];
@@ -651,7 +654,8 @@ cudaError_t launch_experts_as(const ExpertParams& p, const ExpertPlan& l, int ct
 }
 
 // Two CTAs of 6 warps an SM where the experts get few slots each (a CTA's start, its vectors and its end overlap with the other
-// one's products: 8 tokens over 64 experts 61.5 us with 8 + 8 warps, 64.2 us with 16 in one CTA) and the vectors fit beside two rings; else one of 12.
+// one's products: 8 tokens over 64 experts 59.2 us, 61.0 us with 12 warps in one CTA; 1 token 25.7 and 27.4 us) and the vectors
+// fit beside two rings; else one of 12.
 template <bool GateUp, int Parts>
 cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap, cudaStream_t s) {
     const int half = di.max_smem_optin / 2 - 1024;  // of two CTAs an SM
@@ -659,9 +663,9 @@ cudaError_t launch_experts_of(ExpertParams p, const DeviceInfo& di, bool overlap
     const bool two = l.cap >= 8 / Parts && 2LL * p.slots <= (long long)l.cap * p.E && p.slots <= 192;
     if (!two) l = plan_experts(p.blocks, !GateUp, Parts, 12, 3, di.max_smem_optin);
     // Where experts get more slots than half a segment's, a ring of two stages may make room for twice the slots: 64 f16 tokens, 64
-    // slots for each of 4 experts of 14336 x 4096, 900 us with 4 slots a segment, 654 us with 8; 32 bf16 tokens, 8 slots for
-    // each of 8 such experts, 213 us with 8 and 209 us with 16.
-    // Down's parts are short enough for full segments beside three stages.
+    // slots for each of 4 experts of 14336 x 4096, 900 us with 4 slots a segment, 653 us with 8; 32 bf16 tokens, 8 slots for
+    // each of 8 such experts, 309 us with 4 and 268 us with 8, with x in one part 229 us with 8 and 224 us with 16. Down's parts
+    // are short enough for full segments beside three stages.
     bool two_stages = false;
     if (GateUp && !two && 2LL * p.slots > (long long)l.cap * p.E) {
         const ExpertPlan s = plan_experts(p.blocks, !GateUp, Parts, 12, 2, di.max_smem_optin);
