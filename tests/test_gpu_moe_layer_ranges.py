@@ -202,7 +202,7 @@ FORMS = [(64, 4, 4, 512, 4096), (64, 4, 4, 512, 4224), (64, 2, 3, 256, 4128), (3
          (1, 2, 2, 512, 4224), (1, 2, 2, 512, 4096), (100, 2, 64, 96, 4224), (64, 8, 16, 64, 896), (64, 8, 16, 320, 1408),
          (48, 8, 16, 256, 1024), (5, 2, 6, 96, 1152), (12, 3, 40, 256, 1920), (12, 3, 40, 256, 2048), (24, 8, 32, 288, 640),
          (7, 2, 2, 64, 15360), (7, 2, 2, 64, 15488), (1, 1, 4, 96, 15488), (9, 2, 2, 96, 7680), (9, 2, 2, 96, 7808),
-         (6, 1, 1, 32, 30720), (6, 1, 1, 32, 30848)]
+         (6, 1, 1, 32, 30976), (6, 1, 1, 32, 30848)]
 
 
 @pytest.mark.parametrize("T,topk,E,N,K", FORMS)
